@@ -59,11 +59,14 @@ typedef enum {
   PF_ERR_UNSUPPORTED = 8,        /* a mode the library does not implement */
   PF_ERR_CUDA = 9,               /* a CUDA runtime call failed */
   PF_ERR_DEVICE_TIMEOUT = 10,    /* a kernel's bounded wait expired (see status word) */
-  PF_ERR_WORKSPACE = 11          /* workspace too small / not initialised */
+  PF_ERR_WORKSPACE = 11,         /* workspace too small / not initialised */
+  PF_ERR_NONFINITE = 12          /* a NaN or an infinity among values to be held in 8 bits (status word) */
 } pf_status;
 
 typedef enum { PF_W_Q1_G128 = 0, PF_W_INT4_AFFINE_G128 = 1 } pf_wformat;
-typedef enum { PF_KV_F32 = 0, PF_KV_BF16 = 1, PF_KV_F16 = 2 } pf_kvdtype;
+/* PF_KV_E4M3 / PF_KV_INT8: one byte per element and an f32 scale for each PF_KV8_BLOCK slots of
+ * a (layer, kv head), see "8-bit cache" below. Linear and paged caches (no ring); q is f16. */
+typedef enum { PF_KV_F32 = 0, PF_KV_BF16 = 1, PF_KV_F16 = 2, PF_KV_E4M3 = 3, PF_KV_INT8 = 4 } pf_kvdtype;
 
 /* Model configuration ([P1] LayerConfig + the tail's final_norm_eps / vocab). */
 typedef struct {
@@ -96,11 +99,13 @@ typedef struct {
    * position block b = p / PF_KV_BLOCK to the physical block holding positions
    * b * PF_KV_BLOCK .. +PF_KV_BLOCK-1 (same block for every layer and head). Sessions given
    * the same K / V buffers and disjoint tables share one pool. Needs a 16-bit cache and no
-   * ring. */
+   * ring; an 8-bit cache may be paged too. */
   int32_t kv_block_pool;
 } pf_config;
 
 #define PF_KV_BLOCK 128 /* positions per paged KV block: one attention key tile */
+#define PF_KV8_BLOCK 32 /* slots that share one scale in an 8-bit cache */
+#define PF_MAX_TOP 32   /* most alternatives per row (pf_op_logprobs) */
 
 /* One layer's weights ([P1] LayerWeightRefs), all device pointers. Packed tensors
  * come from pf_pack_weights_host (gate_up with interleave_gate_up = 1). */
@@ -131,7 +136,8 @@ const char* pf_last_error(void);      /* thread-local, never NULL */
 const char* pf_status_name(int status);
 int32_t pf_abi_version(void);         /* bumps on any ABI change (2: ring fields, 3: kv_block_pool,
                                         4: split-KV counters in the attention scratch,
-                                        pf_streamk_plan_host) */
+                                        pf_streamk_plan_host; calls and enum values added since
+                                        leave what was there unchanged) */
 
 /* ------------------------------------------------------------------ packing
  * Canonical host formats (the pages name "Q1 block bytes" and an "AoS -> SoA"
@@ -158,7 +164,11 @@ pf_status pf_pack_weights_host(int32_t wfmt, const uint8_t* codes_host,
 size_t pf_kv_bytes(const pf_config* cfg);        /* bytes of ONE of K / V:
                                                     n_layers*nkv*slots*hd*elem, slots =
                                                     ring_capacity (ring), PF_KV_BLOCK *
-                                                    kv_block_pool (paged) or max_seq */
+                                                    kv_block_pool (paged) or max_seq;
+                                                    8-bit: codes, padding, scales */
+/* 8-bit caches: byte offset of the scales in each of K / V: the codes' bytes
+ * n_layers*nkv*slots*hd rounded up to a multiple of 256 (0 for other configurations). */
+size_t pf_kv8_scales_offset(const pf_config* cfg);
 size_t pf_workspace_bytes(const pf_config* cfg); /* activations for max_chunk rows,
                                                     RoPE table, status words */
 /* Validates a configuration; PF_OK or the reason it is not supported. Host only. */
@@ -296,6 +306,17 @@ pf_status pf_decode_step_greedy(pf_session* s, const int32_t* token_in_dev, int3
 pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M, int32_t start_pos,
                             float* logits_all_dev, int32_t* ids_dev, void* stream);
 
+/* Scores a chunk: pf_prefill_verify's path (every position's logits, f32 [M][vocab] in
+ * logits_all_dev), then pf_op_logprobs on them: logprobs_dev [M] = log probability of
+ * targets_dev[t] (device int32, e.g. the next token of the text) after token t, entropy_dev [M]
+ * (may be NULL), and with top > 0 the most likely tokens top_ids_dev [M][top] and their log
+ * probabilities top_logprobs_dev [M][top] (may be NULL). Checks, errors and the KV position as
+ * pf_prefill_verify; a target outside the vocabulary as in pf_op_logprobs, with the session's
+ * status word. */
+pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32_t* targets_dev, int32_t M,
+                           int32_t start_pos, float* logits_all_dev, float* logprobs_dev, float* entropy_dev,
+                           int32_t top, int32_t* top_ids_dev, float* top_logprobs_dev, void* stream);
+
 /* End to end from host memory: copies tokens_host to the device, runs
  * pf_prefill_chunk, copies the last position's logits into logits_host [vocab]
  * (may be NULL) and synchronises the stream. */
@@ -413,6 +434,67 @@ pf_status pf_op_lm_head(int32_t wfmt, const float* x_row_dev, const float* norm_
  * on ties, NaN never chosen (a row without a number gives 0). rows >= 1, n >= 1, ld >= n. */
 pf_status pf_op_argmax(const float* x_dev, int32_t rows, int32_t n, int64_t ld, int32_t* out_dev,
                        void* stream);
+/* Log probabilities of given tokens, entropy and top alternatives of each row of f32 logits
+ * [rows][ld] (n <= ld values a row; what lies behind them is not read). With m the row's
+ * maximum and Z = sum exp(x - m):
+ *   logprobs_dev[r] = x[r][tokens_dev[r]] - m - ln Z    (NULL: not computed, tokens_dev unused)
+ *   entropy_dev[r]  = -sum p ln p, natural logarithms   (NULL: not computed)
+ *   top_ids_dev[r][0 .. top-1] = the indices of the largest logits, largest first, the lowest
+ *     index first among equals (-0 equals +0); top_logprobs_dev (may be NULL) theirs. top 0..32;
+ *     past the row's last number: index -1, log probability NaN.
+ * A logit of -inf has probability 0: it adds nothing to the entropy and its log probability is
+ * -inf. A NaN (never listed) or a +inf among the logits, or a row of -inf alone, makes the row's
+ * logprob, entropy and top_logprobs NaN (the ids stay valid). A token outside [0, n) gets NaN and
+ * records PF_ERR_TOKEN_OUT_OF_VOCAB in *status_dev (if not NULL). No scratch; f32 arithmetic. */
+pf_status pf_op_logprobs(const float* logits_dev, int32_t rows, int32_t n, int64_t ld, const int32_t* tokens_dev,
+                         float* logprobs_dev, float* entropy_dev, int32_t top, int32_t* top_ids_dev,
+                         float* top_logprobs_dev, int32_t* status_dev, void* stream);
+/* ------------------------------------------------------------------ 8-bit cache
+ * A cache buffer (one of K / V, pf_kv_bytes bytes) of a PF_KV_E4M3 or PF_KV_INT8 configuration:
+ *   codes   uint8 [n_layers][nkv][slots][hd], e4m3 (OCP FP8, no infinities) or two's complement;
+ *   scales  f32 [n_layers][nkv][ceil(slots / PF_KV8_BLOCK)] at pf_kv8_scales_offset(cfg).
+ * Element value = code * scale of its slot's block. slots = max_seq, or PF_KV_BLOCK *
+ * kv_block_pool for a paged cache, whose calls take the block table in DEVICE memory
+ * (int32 [ceil(max_seq / PF_KV_BLOCK)], NULL for a linear cache): every entry that the positions
+ * of a call reach must name a block of the pool, distinct blocks for distinct entries. An entry
+ * outside the pool is not followed: the call records PF_ERR_KV_CAPACITY in *status_dev, and its
+ * results for those positions mean nothing. status_dev may be NULL in all three calls.
+ *
+ * pf_op_kv8_store: positions start_pos .. +M-1 of `layer` from f16 rows (K after RoPE), element
+ * (t, kv head, i) at t * tok_stride + head * head_stride + i (strides in elements, multiples of 8;
+ * rows and caches 16-B aligned). For each (kv head, block of 32 positions) with new rows:
+ *   e = the least integer >= -32 with max |new| <= CMAX 2^e, CMAX = 448 (e4m3) or 127 (int8);
+ *   scale s = 2^e, or max(s_old, 2^e) where the block holds positions before start_pos (which
+ *   must then have been stored by this call or lie at a power-of-two scale);
+ *   if s > s_old, the earlier positions' codes become RNE(code * s_old / s);
+ *   new codes = RNE(x / s), ties to even.
+ * Positions past the chunk keep their bytes. A NaN is held as zero and an infinity as the largest
+ * code, neither counts for the maximum, and PF_ERR_NONFINITE is recorded in *status_dev.
+ *
+ * pf_op_kv8_load: out f32 [M][nkv][hd] = the values of positions start_pos .. +M-1 in `cache`
+ * (one of K / V).
+ *
+ * pf_op_attention_kv8: causal GQA attention as pf_op_attention: q f16 [M][nq][hd] at positions
+ * start_pos .., keys 0 .. position of `layer`, out f16 [M][nq hd]; scores and softmax statistics
+ * in f32. Codes and scales of other positions are not used, whatever they hold. scratch_dev:
+ * device, 16-B aligned, at least pf_attention_kv8_scratch_bytes(cfg, M) bytes (which does not fall
+ * as M grows); its first 4 KiB must be zero before the first call, and each call that completes
+ * leaves them zero (after PF_ERR_DEVICE_TIMEOUT zero them again). Calls sharing one scratch must
+ * not overlap in time.
+ * Errors: PF_ERR_UNSUPPORTED (not an 8-bit configuration), PF_ERR_INVALID_ARG (pointers,
+ * alignment, strides, a table with a linear cache or none with a paged one), PF_ERR_EMPTY_CHUNK,
+ * PF_ERR_SHAPE (layer), PF_ERR_KV_CAPACITY (positions), PF_ERR_WORKSPACE, PF_ERR_CUDA. */
+pf_status pf_op_kv8_store(const pf_config* cfg, const uint16_t* k_f16_dev, const uint16_t* v_f16_dev,
+                          int64_t tok_stride, int64_t head_stride, int32_t layer, int32_t start_pos, int32_t M,
+                          const int32_t* block_table_dev, void* k_cache_dev, void* v_cache_dev,
+                          int32_t* status_dev, void* stream);
+pf_status pf_op_kv8_load(const pf_config* cfg, const void* cache_dev, int32_t layer, int32_t start_pos, int32_t M,
+                         const int32_t* block_table_dev, float* out_dev, int32_t* status_dev, void* stream);
+size_t pf_attention_kv8_scratch_bytes(const pf_config* cfg, int32_t M);
+pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q_f16_dev, const void* k_cache_dev,
+                              const void* v_cache_dev, int32_t layer, int32_t start_pos, int32_t M,
+                              const int32_t* block_table_dev, uint16_t* out_f16_dev, void* scratch_dev,
+                              size_t scratch_bytes, int32_t* status_dev, void* stream);
 /* Host RoPE table [max_seq][hd/2][2] = (cos, sin)(p * theta^(-2i/hd)), computed in
  * double and rounded to f32. */
 pf_status pf_rope_table_host(float theta, int32_t head_dim, int32_t max_seq, float* dst_host);

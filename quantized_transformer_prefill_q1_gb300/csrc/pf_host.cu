@@ -46,12 +46,13 @@ pf_status cuda_fail(cudaError_t e, const char* what) {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// bytes of one K / V element as the chunk holds it (an 8-bit cache is filled from f16 rows)
 size_t kv_elem_bytes(int kv_dtype) { return kv_dtype == PF_KV_F32 ? 4 : 2; }
 
 // ------------------------------------------------------------------ workspace layout
 struct WsLayout {
   size_t status, params, tokens, x, y, qkv, q, attn, act, logits, gemm, gemm_bytes, rope;
-  size_t kchunk, vchunk;          // ring mode: the chunk's K / V rows [nkv][max_chunk][hd]
+  size_t kchunk, vchunk;          // ring mode, 8-bit cache: the chunk's K / V rows [nkv][max_chunk][hd]
   size_t attn_part, attn_part_bytes;  // split-KV partial results
   size_t blocks;                      // paged cache: block table [block_table_entries] int32
   size_t total;
@@ -83,10 +84,10 @@ WsLayout ws_layout(const pf_config& c) {
   L.gemm_bytes = gemm_scratch_bytes(c.max_chunk, widest, GEMM_MAX_CTAS);
   L.gemm = take(L.gemm_bytes);
   L.rope = take(static_cast<size_t>(c.max_seq) * (hd / 2) * 2 * 4);
-  const size_t chunk_kv = c.ring_capacity > 0 ? C * c.n_kv_heads * hd * kv_elem_bytes(c.kv_dtype) : 0;
+  const size_t chunk_kv = c.ring_capacity > 0 || kv8(c) ? C * c.n_kv_heads * hd * kv_elem_bytes(c.kv_dtype) : 0;
   L.kchunk = take(chunk_kv);
   L.vchunk = take(chunk_kv);
-  L.attn_part_bytes = attention_partial_bytes_max(c, GEMM_MAX_CTAS);
+  L.attn_part_bytes = kv8(c) ? attention_kv8_scratch_bytes(c, c.max_chunk) : attention_partial_bytes_max(c, GEMM_MAX_CTAS);
   L.attn_part = take(L.attn_part_bytes);
   L.blocks = take(c.kv_block_pool > 0 ? block_table_entries(c) * sizeof(int) : 0);
   L.total = o;
@@ -239,7 +240,7 @@ pf_status check_cfg(const pf_config* c) {
   if (c->vocab < 0) return fail(PF_ERR_SHAPE, "vocab %d", c->vocab);
   if (c->wfmt != PF_W_Q1_G128 && c->wfmt != PF_W_INT4_AFFINE_G128)
     return fail(PF_ERR_INVALID_ARG, "weight format %d", c->wfmt);
-  if (c->kv_dtype != PF_KV_F32 && c->kv_dtype != PF_KV_BF16 && c->kv_dtype != PF_KV_F16)
+  if (c->kv_dtype != PF_KV_F32 && c->kv_dtype != PF_KV_BF16 && c->kv_dtype != PF_KV_F16 && !kv8(*c))
     return fail(PF_ERR_INVALID_ARG, "kv dtype %d", c->kv_dtype);
   if (c->max_seq <= 0) return fail(PF_ERR_SHAPE, "max_seq %d", c->max_seq);
   if (c->max_chunk <= 0 || c->max_chunk > 8192) return fail(PF_ERR_SHAPE, "max_chunk %d: 1..8192", c->max_chunk);
@@ -258,11 +259,14 @@ pf_status check_cfg(const pf_config* c) {
   if (c->kv_block_pool < 0) return fail(PF_ERR_SHAPE, "kv_block_pool %d", c->kv_block_pool);
   if (c->kv_block_pool > 0) {
     if (c->ring_capacity > 0) return fail(PF_ERR_SHAPE, "a paged cache cannot also be a ring");
-    if (!attention_tc_supported(*c))
-      return fail(PF_ERR_UNSUPPORTED, "paged cache: needs a 16-bit cache (bf16 / f16) and a GQA group dividing 128");
+    if (!attention_tc_supported(*c) && !kv8(*c))
+      return fail(PF_ERR_UNSUPPORTED, "paged cache: needs a 16-bit or 8-bit cache and a GQA group dividing 128");
     if (static_cast<int64_t>(c->kv_block_pool) * PF_KV_BLOCK > (int64_t{1} << 30))
       return fail(PF_ERR_SHAPE, "kv_block_pool %d too large", c->kv_block_pool);
   }
+  if (kv8(*c) && (c->max_seq > (1 << 30) || c->n_kv_heads > KV8_MAX_HEADS))
+    return fail(PF_ERR_SHAPE, "8-bit cache: max_seq %d (at most 2^30), kv heads %d (at most %d)", c->max_seq, c->n_kv_heads,
+                KV8_MAX_HEADS);
   return PF_OK;
 }
 
@@ -376,36 +380,70 @@ pf_status enqueue_layer(pf_session* s, int l, float* x, int M, cudaStream_t st, 
   // 3. QK-norm + RoPE + KV store, then causal GQA attention over cache + chunk. A ring cache
   //    takes the chunk's K / V in the chunk buffers first (its later tokens may overwrite
   //    slots its earlier tokens still see) and into the ring after the attention.
-  const bool ring = c.ring_capacity > 0;
+  //    An 8-bit cache takes them in the chunk buffers too, as f16, then in codes before the
+  //    attention, which reads all its keys from the cache.
+  const bool chunked = c.ring_capacity > 0 || kv8(c);
   const int* blocks = c.kv_block_pool > 0 ? wsp<int>(s, s->L.blocks) : nullptr;
-  void* kc = ring ? wsp<void>(s, s->L.kchunk) : s->k;
-  void* vc = ring ? wsp<void>(s, s->L.vchunk) : s->v;
+  void* kc = chunked ? wsp<void>(s, s->L.kchunk) : s->k;
+  void* vc = chunked ? wsp<void>(s, s->L.vchunk) : s->v;
+  pf_config rows = c;  // the type of the rows that step 3 writes
+  if (kv8(c)) rows.kv_dtype = PF_KV_F16;
   PF_TRY(launch_k(s, PF_K_QK_ROPE_KV, st, "qk_norm_rope_kv", [&] {
-    return launch_qk_norm_rope_kv(c, qkv, w.q_norm, w.k_norm, wsp<float>(s, s->L.rope), ring ? 0 : l,
-                                  ring ? c.max_chunk : cache_slots(c), ring ? 0 : 1, start_dev, 0, M, q, kc,
-                                  vc, st, blocks);
+    return launch_qk_norm_rope_kv(rows, qkv, w.q_norm, w.k_norm, wsp<float>(s, s->L.rope), chunked ? 0 : l,
+                                  chunked ? c.max_chunk : cache_slots(c), chunked ? 0 : 1, start_dev, 0, M, q, kc,
+                                  vc, st, chunked ? nullptr : blocks);
   }));
-  AttnArgs aa{};
-  aa.c = &c;
-  aa.q = q;
-  aa.k_cache = s->k;
-  aa.v_cache = s->v;
-  aa.k_chunk = ring ? kc : nullptr;
-  aa.v_chunk = ring ? vc : nullptr;
-  aa.chunk_rows = c.max_chunk;
-  aa.layer = l;
-  aa.start_dev = start_dev;
-  aa.M = M;
-  aa.out = attn;
-  aa.n_split = attention_splits(c, M, std::min(s->sms, GEMM_MAX_CTAS));
-  aa.partial = wsp<float>(s, s->L.attn_part);
-  aa.status = wsp<int>(s, s->L.status);
-  aa.blocks = blocks;
-  PF_TRY(launch_k(s, PF_K_ATTENTION, st, "attention", [&] { return launch_attention(aa, st); }));
-  if (ring)
-    PF_TRY(launch_k(s, PF_K_QK_ROPE_KV, st, "ring store", [&] {
-      return launch_ring_store(c, kc, vc, c.max_chunk, l, start_dev, 0, M, s->k, s->v, st);
-    }));
+  if (kv8(c)) {
+    Kv8StoreArgs sa{};
+    sa.c = &c;
+    sa.k = kc;
+    sa.v = vc;
+    sa.tok_stride = hd;
+    sa.head_stride = static_cast<int64_t>(c.max_chunk) * hd;
+    sa.layer = l;
+    sa.start_dev = start_dev;
+    sa.M = M;
+    sa.k_cache = s->k;
+    sa.v_cache = s->v;
+    sa.blocks = blocks;
+    sa.status = wsp<int>(s, s->L.status);
+    PF_TRY(launch_k(s, PF_K_QK_ROPE_KV, st, "8-bit store", [&] { return launch_kv8_store(sa, st); }));
+    Kv8AttnArgs aa{};
+    aa.c = &c;
+    aa.q = q;
+    aa.k_cache = s->k;
+    aa.v_cache = s->v;
+    aa.layer = l;
+    aa.start_dev = start_dev;
+    aa.M = M;
+    aa.out = attn;
+    aa.scratch = wsp<void>(s, s->L.attn_part);
+    aa.blocks = blocks;
+    aa.status = wsp<int>(s, s->L.status);
+    PF_TRY(launch_k(s, PF_K_ATTENTION, st, "attention", [&] { return launch_attention_kv8(aa, st); }));
+  } else {
+    AttnArgs aa{};
+    aa.c = &c;
+    aa.q = q;
+    aa.k_cache = s->k;
+    aa.v_cache = s->v;
+    aa.k_chunk = chunked ? kc : nullptr;
+    aa.v_chunk = chunked ? vc : nullptr;
+    aa.chunk_rows = c.max_chunk;
+    aa.layer = l;
+    aa.start_dev = start_dev;
+    aa.M = M;
+    aa.out = attn;
+    aa.n_split = attention_splits(c, M, std::min(s->sms, GEMM_MAX_CTAS));
+    aa.partial = wsp<float>(s, s->L.attn_part);
+    aa.status = wsp<int>(s, s->L.status);
+    aa.blocks = blocks;
+    PF_TRY(launch_k(s, PF_K_ATTENTION, st, "attention", [&] { return launch_attention(aa, st); }));
+    if (chunked)
+      PF_TRY(launch_k(s, PF_K_QK_ROPE_KV, st, "ring store", [&] {
+        return launch_ring_store(c, kc, vc, c.max_chunk, l, start_dev, 0, M, s->k, s->v, st);
+      }));
+  }
   // 4. O projection + residual
   PF_TRY(enqueue_gemm(s, PF_K_GEMM_O, c.wfmt, EPI_RESID_ADD, attn, w.o_proj, M, H,
                       c.n_q_heads * hd, x, st));
@@ -518,6 +556,7 @@ const char* pf_status_name(int st) {
     case PF_ERR_CUDA: return "PF_ERR_CUDA";
     case PF_ERR_DEVICE_TIMEOUT: return "PF_ERR_DEVICE_TIMEOUT";
     case PF_ERR_WORKSPACE: return "PF_ERR_WORKSPACE";
+    case PF_ERR_NONFINITE: return "PF_ERR_NONFINITE";
     default: return "PF_ERR_UNKNOWN";
   }
 }
@@ -618,8 +657,16 @@ pf_status pf_pack_weights_host(int32_t wfmt, const uint8_t* codes, const uint16_
 size_t pf_kv_bytes(const pf_config* c) {
   if (check_cfg(c) != PF_OK) return 0;
   const int slots = cache_slots(*c);
+  if (kv8(*c))
+    return kv8_scales_offset(*c) + static_cast<size_t>(c->n_layers) * c->n_kv_heads *
+                                       ((slots + PF_KV8_BLOCK - 1) / PF_KV8_BLOCK) * sizeof(float);
   return static_cast<size_t>(c->n_layers) * c->n_kv_heads * slots * c->head_dim *
          kv_elem_bytes(c->kv_dtype);
+}
+
+size_t pf_kv8_scales_offset(const pf_config* c) {
+  if (check_cfg(c) != PF_OK || !kv8(*c)) return 0;
+  return kv8_scales_offset(*c);
 }
 
 size_t pf_workspace_bytes(const pf_config* c) {
@@ -701,7 +748,7 @@ pf_status pf_session_create(const pf_model* model, void* k, void* v, void* ws, s
   if (e == cudaSuccess) e = cudaMemsetAsync(s->ws + L.status, 0, STATUS_WORDS * 4, st);
   if (e == cudaSuccess) e = cudaMemsetAsync(s->ws + L.gemm, 0, L.gemm_bytes, st);  // tile counters
   if (e == cudaSuccess && L.attn_part_bytes)  // split-KV arrival counters
-    e = cudaMemsetAsync(s->ws + L.attn_part, 0, attention_counter_bytes(c), st);
+    e = cudaMemsetAsync(s->ws + L.attn_part, 0, kv8(c) ? KV8_COUNTER_BYTES : attention_counter_bytes(c), st);
   if (c.kv_block_pool > 0) {  // every position block unassigned (-1)
     s->blocks.assign(block_table_entries(c), -1);
     if (e == cudaSuccess) e = cudaMemsetAsync(s->ws + L.blocks, 0xff, s->blocks.size() * sizeof(int), st);
@@ -785,16 +832,20 @@ pf_status pf_timeline_set(uint64_t* buffer, int64_t capacity) {
   PF_CUDA(timeline_set_gemv(b), "timeline");
   PF_CUDA(timeline_set_attention(b), "timeline");
   PF_CUDA(timeline_set_attention_tc(b), "timeline");
+  PF_CUDA(timeline_set_kv8(b), "timeline");
+  PF_CUDA(timeline_set_attention_kv8(b), "timeline");
+  PF_CUDA(timeline_set_logprobs(b), "timeline");
   return PF_OK;
 }
 
 const char* pf_timeline_kernel_name(int32_t id) {
   static const std::vector<std::string> names = [] {
     std::vector<std::string> n(64);
-    const char* fixed[15] = {"", "rmsnorm", "rmsnorm_reg", "qk_norm_rope_kv", "ring_store", "embed",
+    const char* fixed[19] = {"", "rmsnorm", "rmsnorm_reg", "qk_norm_rope_kv", "ring_store", "embed",
                              "lm_head", "dequant", "set_int", "argmax_rows", "wait_selftest", "lm_head_q1",
-                             "attention_f32", "attention_tc", "attn_combine"};
-    for (int i = 1; i < 15; ++i) n[i] = fixed[i];
+                             "attention_f32", "attention_tc", "attn_combine", "kv8_store", "kv8_load",
+                             "attention_kv8", "logprobs"};
+    for (int i = 1; i < 19; ++i) n[i] = fixed[i];
     const char* epi[3] = {"store", "resid", "swiglu"};
     for (int e = 0; e < 3; ++e) {
       n[TL_GEMM + e] = std::string("gemm_") + epi[e];
@@ -936,11 +987,10 @@ pf_status pf_decode_step_greedy(pf_session* s, const int32_t* token_in_dev, int3
 // P1 encode_full_forward_prefill_verify: the layer loop of one micro-batch, then the
 // batched final RMSNorm on all positions, the LM-head GEMM on all positions and one argmax
 // per position.
-pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M, int32_t start_pos,
-                            float* logits_all_dev, int32_t* ids_dev, void* stream) {
-  if (!s) return fail(PF_ERR_INVALID_ARG, "session is NULL");
+static pf_status prefill_all_logits(pf_session* s, const int32_t* tokens_dev, int32_t M, int32_t start_pos,
+                                    float* logits_all_dev, void* stream) {
   const pf_config& c = s->model.cfg;
-  if (!tokens_dev || !logits_all_dev || !ids_dev) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!tokens_dev || !logits_all_dev) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (!s->model.lm_head || !s->model.final_norm || c.vocab <= 0)
     return fail(PF_ERR_LOGITS, "verify needs the final norm and LM head");
   if (M > c.max_chunk) return fail(PF_ERR_SHAPE, "verify chunk M %d exceeds max_chunk %d", M, c.max_chunk);
@@ -954,8 +1004,17 @@ pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M,
   PF_TRY(launch_k(s, PF_K_RMSNORM, st, "final rmsnorm", [&] {
     return launch_rmsnorm(x, s->model.final_norm, c.final_eps, M, c.hidden, y, st);
   }));
-  PF_TRY(enqueue_gemm(s, PF_K_LM_HEAD, c.wfmt, EPI_STORE_F32, y, s->model.lm_head, M, c.vocab, c.hidden,
-                      logits_all_dev, st));
+  return enqueue_gemm(s, PF_K_LM_HEAD, c.wfmt, EPI_STORE_F32, y, s->model.lm_head, M, c.vocab, c.hidden,
+                      logits_all_dev, st);
+}
+
+pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M, int32_t start_pos,
+                            float* logits_all_dev, int32_t* ids_dev, void* stream) {
+  if (!s) return fail(PF_ERR_INVALID_ARG, "session is NULL");
+  const pf_config& c = s->model.cfg;
+  if (!ids_dev) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  PF_TRY(prefill_all_logits(s, tokens_dev, M, start_pos, logits_all_dev, stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launch_k(s, PF_K_OTHER, st, "argmax", [&] {
     return launch_argmax_rows(logits_all_dev, M, c.vocab, c.vocab, ids_dev, st);
   });
@@ -1140,6 +1199,7 @@ pf_status pf_op_qk_norm_rope_kv(const pf_config* cfg, const float* qkv, const fl
   if (r != PF_OK) return r;
   if (cfg->ring_capacity > 0 || cfg->kv_block_pool > 0)
     return fail(PF_ERR_UNSUPPORTED, "single-step KV store: linear caches only");
+  if (kv8(*cfg)) return fail(PF_ERR_UNSUPPORTED, "single-step KV store: an 8-bit cache is filled by pf_op_kv8_store");
   if (!qkv || !rope || !q || !kc || !vc || (cfg->qk_norm && (!qn || !kn)))
     return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (M <= 0 || layer < 0 || layer >= cfg->n_layers || start < 0 ||
@@ -1158,6 +1218,7 @@ static pf_status attention_op(const pf_config* cfg, const void* q, const void* k
   if (r != PF_OK) return r;
   if (cfg->ring_capacity > 0 || cfg->kv_block_pool > 0)
     return fail(PF_ERR_UNSUPPORTED, "single-step attention: linear caches only");
+  if (kv8(*cfg)) return fail(PF_ERR_UNSUPPORTED, "single-step attention: an 8-bit cache is read by pf_op_attention_kv8");
   if (!q || !kc || !vc || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (M <= 0 || layer < 0 || layer >= cfg->n_layers || start < 0 ||
       static_cast<int64_t>(start) + M > cfg->max_seq)
@@ -1195,7 +1256,7 @@ pf_status pf_op_attention(const pf_config* cfg, const void* q, const void* kc, c
 }
 
 size_t pf_attention_scratch_bytes(const pf_config* cfg, int32_t M, int32_t n_split) {
-  if (check_cfg(cfg) != PF_OK || M <= 0 || n_split < 1 || n_split > 64) return 0;
+  if (check_cfg(cfg) != PF_OK || kv8(*cfg) || M <= 0 || n_split < 1 || n_split > 64) return 0;
   return attention_partial_bytes(*cfg, M, n_split);
 }
 
@@ -1229,6 +1290,140 @@ pf_status pf_op_argmax(const float* x, int32_t rows, int32_t n, int64_t ld, int3
   if (rows <= 0 || n <= 0 || ld < n) return fail(PF_ERR_SHAPE, "rows %d n %d ld %lld", rows, n, (long long)ld);
   PF_CUDA(launch_argmax_rows(x, rows, n, ld, out, static_cast<cudaStream_t>(stream)), "argmax");
   return PF_OK;
+}
+
+// ---------------------------------------------------------------------- 8-bit cache
+// What the three calls check alike: an 8-bit configuration, its block table, the layer and the
+// positions start .. start + M - 1.
+static pf_status check_kv8(const pf_config* cfg, int32_t layer, int32_t start, int32_t M, const int32_t* table) {
+  pf_status r = check_cfg(cfg);
+  if (r != PF_OK) return r;
+  if (!kv8(*cfg)) return fail(PF_ERR_UNSUPPORTED, "kv dtype %d is not an 8-bit type", cfg->kv_dtype);
+  if ((cfg->kv_block_pool > 0) != (table != nullptr))
+    return fail(PF_ERR_INVALID_ARG, cfg->kv_block_pool > 0 ? "a paged cache needs its block table" : "a block table without a paged cache");
+  if (M <= 0) return fail(PF_ERR_EMPTY_CHUNK, "M = %d", M);
+  if (layer < 0 || layer >= cfg->n_layers) return fail(PF_ERR_SHAPE, "layer %d of %d", layer, cfg->n_layers);
+  if (start < 0 || static_cast<int64_t>(start) + M > cfg->max_seq)
+    return fail(PF_ERR_KV_CAPACITY, "positions [%d, %lld) exceed KV capacity %d", start, static_cast<long long>(start) + M,
+                cfg->max_seq);
+  return PF_OK;
+}
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+pf_status pf_op_kv8_store(const pf_config* cfg, const uint16_t* k, const uint16_t* v, int64_t tok_stride, int64_t head_stride,
+                          int32_t layer, int32_t start, int32_t M, const int32_t* table, void* kc, void* vc, int32_t* status,
+                          void* stream) {
+  pf_status r = check_kv8(cfg, layer, start, M, table);
+  if (r != PF_OK) return r;
+  if (!k || !v || !kc || !vc) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(vc))
+    return fail(PF_ERR_INVALID_ARG, "K / V rows and caches must be 16-B aligned");
+  if (tok_stride < 0 || head_stride < 0 || tok_stride % 8 || head_stride % 8)
+    return fail(PF_ERR_INVALID_ARG, "strides %lld / %lld: non-negative multiples of 8 elements", (long long)tok_stride,
+                (long long)head_stride);
+  Kv8StoreArgs a{};
+  a.c = cfg;
+  a.k = k;
+  a.v = v;
+  a.tok_stride = tok_stride;
+  a.head_stride = head_stride;
+  a.layer = layer;
+  a.start_host = start;
+  a.M = M;
+  a.k_cache = kc;
+  a.v_cache = vc;
+  a.blocks = table;
+  a.status = status;
+  PF_CUDA(launch_kv8_store(a, static_cast<cudaStream_t>(stream)), "8-bit store");
+  return PF_OK;
+}
+
+pf_status pf_op_kv8_load(const pf_config* cfg, const void* cache, int32_t layer, int32_t start, int32_t M, const int32_t* table,
+                         float* out, int32_t* status, void* stream) {
+  pf_status r = check_kv8(cfg, layer, start, M, table);
+  if (r != PF_OK) return r;
+  if (!cache || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(cache) || !aligned16(out)) return fail(PF_ERR_INVALID_ARG, "cache and out must be 16-B aligned");
+  PF_CUDA(launch_kv8_load(*cfg, cache, layer, start, M, table, out, status, static_cast<cudaStream_t>(stream)), "8-bit load");
+  return PF_OK;
+}
+
+size_t pf_attention_kv8_scratch_bytes(const pf_config* cfg, int32_t M) {
+  if (check_cfg(cfg) != PF_OK || !kv8(*cfg) || M <= 0) return 0;
+  return attention_kv8_scratch_bytes(*cfg, M);
+}
+
+pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q, const void* kc, const void* vc, int32_t layer,
+                              int32_t start, int32_t M, const int32_t* table, uint16_t* out, void* scratch,
+                              size_t scratch_bytes, int32_t* status, void* stream) {
+  pf_status r = check_kv8(cfg, layer, start, M, table);
+  if (r != PF_OK) return r;
+  if (!q || !kc || !vc || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out))
+    return fail(PF_ERR_INVALID_ARG, "q, caches and out must be 16-B aligned");
+  const size_t need = attention_kv8_scratch_bytes(*cfg, M);
+  if (!scratch || scratch_bytes < need)
+    return fail(PF_ERR_WORKSPACE, "8-bit attention scratch %zu bytes, need %zu", scratch_bytes, need);
+  if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  prepare_all();
+  Kv8AttnArgs a{};
+  a.c = cfg;
+  a.q = q;
+  a.k_cache = kc;
+  a.v_cache = vc;
+  a.layer = layer;
+  a.start_host = start;
+  a.M = M;
+  a.out = out;
+  a.scratch = scratch;
+  a.blocks = table;
+  a.status = status;
+  PF_CUDA(launch_attention_kv8(a, static_cast<cudaStream_t>(stream)), "8-bit attention");
+  return PF_OK;
+}
+
+// ---------------------------------------------------------------------- log probabilities
+static pf_status check_logprobs(const float* logits, int32_t rows, int32_t n, int64_t ld, const int32_t* tokens,
+                                const float* lp, int32_t top, const int32_t* top_ids, const float* top_lp) {
+  if (!logits || (lp && !tokens)) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (rows <= 0 || n <= 0 || ld < n) return fail(PF_ERR_SHAPE, "rows %d n %d ld %lld", rows, n, (long long)ld);
+  if (top < 0 || top > PF_MAX_TOP) return fail(PF_ERR_SHAPE, "top %d outside 0..%d", top, PF_MAX_TOP);
+  if (top > 0 && !top_ids) return fail(PF_ERR_INVALID_ARG, "top %d without top_ids", top);
+  if (top == 0 && (top_ids || top_lp)) return fail(PF_ERR_INVALID_ARG, "top_ids / top_logprobs with top 0");
+  return PF_OK;
+}
+
+pf_status pf_op_logprobs(const float* logits, int32_t rows, int32_t n, int64_t ld, const int32_t* tokens, float* lp,
+                         float* entropy, int32_t top, int32_t* top_ids, float* top_lp, int32_t* status, void* stream) {
+  pf_status r = check_logprobs(logits, rows, n, ld, tokens, lp, top, top_ids, top_lp);
+  if (r != PF_OK) return r;
+  if (!lp && !entropy && top == 0) return fail(PF_ERR_INVALID_ARG, "nothing to compute");
+  PF_CUDA(launch_logprobs({logits, rows, n, ld, tokens, lp, entropy, top, top_ids, top_lp, status},
+                          static_cast<cudaStream_t>(stream)),
+          "logprobs");
+  return PF_OK;
+}
+
+// pf_prefill_verify's path (layers, final norm and LM head at every position) with the scores of the
+// targets in place of the greedy ids.
+pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32_t* targets_dev, int32_t M, int32_t start_pos,
+                           float* logits_all_dev, float* lp, float* entropy, int32_t top, int32_t* top_ids, float* top_lp,
+                           void* stream) {
+  if (!s) return fail(PF_ERR_INVALID_ARG, "session is NULL");
+  if (!lp) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  const int vocab = s->model.cfg.vocab;
+  if (vocab > 0 && M > 0) {
+    pf_status r = check_logprobs(logits_all_dev, M, vocab, vocab, targets_dev, lp, top, top_ids, top_lp);
+    if (r != PF_OK) return r;
+  }
+  pf_status r = prefill_all_logits(s, tokens_dev, M, start_pos, logits_all_dev, stream);
+  if (r != PF_OK) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_k(s, PF_K_OTHER, st, "logprobs", [&] {
+    return launch_logprobs({logits_all_dev, M, vocab, vocab, targets_dev, lp, entropy, top, top_ids, top_lp,
+                            wsp<int>(s, s->L.status)},
+                           st);
+  });
 }
 
 }  // extern "C"

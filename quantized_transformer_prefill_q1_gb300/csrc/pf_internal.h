@@ -161,6 +161,76 @@ size_t attention_counter_bytes(const pf_config& c);
 cudaError_t launch_ring_store(const pf_config& c, const void* k_chunk, const void* v_chunk,
                               int chunk_rows, int layer, const int* start_dev, int start_host, int M,
                               void* k_cache, void* v_cache, cudaStream_t stream);
+// ------------------------------------------------------------------ 8-bit cache (kv8.cu, attention_kv8.cu)
+inline bool kv8(const pf_config& c) { return c.kv_dtype == PF_KV_E4M3 || c.kv_dtype == PF_KV_INT8; }
+inline size_t kv8_scales_offset(const pf_config& c) {
+  const size_t codes = static_cast<size_t>(c.n_layers) * c.n_kv_heads * cache_slots(c) * c.head_dim;
+  return (codes + 255) / 256 * 256;
+}
+// One layer of an 8-bit cache, as the kernels see it (device pointers of that layer).
+struct Kv8Layer {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int slots;         // per kv head
+  int nblk;          // scale blocks per kv head
+  const int* table;  // paged: position block -> physical block, else NULL
+  int pool;          // physical blocks
+};
+Kv8Layer kv8_layer(const pf_config& c, const void* k, const void* v, int layer, const int* table);
+struct Kv8StoreArgs {
+  const pf_config* c;
+  const void* k;  // f16, element (t, kv head, i) at t * tok_stride + kvh * head_stride + i
+  const void* v;
+  int64_t tok_stride, head_stride;  // elements, multiples of 8
+  int layer;
+  const int* start_dev;  // start position in device memory, or NULL to use start_host
+  int start_host;
+  int M;
+  void* k_cache;
+  void* v_cache;
+  const int* blocks;  // paged cache: the block table (device), else NULL
+  int* status;
+};
+cudaError_t launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t stream);
+cudaError_t launch_kv8_load(const pf_config& c, const void* cache, int layer, int start, int M, const int* blocks,
+                            float* out, int* status, cudaStream_t stream);
+struct Kv8AttnArgs {
+  const pf_config* c;
+  const void* q;  // f16 [M][nq][hd]
+  const void* k_cache;
+  const void* v_cache;
+  int layer;
+  const int* start_dev;
+  int start_host;
+  int M;
+  void* out;      // f16 [M][nq * hd]
+  void* scratch;  // attention_kv8_scratch_bytes(c, M) bytes
+  const int* blocks;
+  int* status;
+};
+cudaError_t launch_attention_kv8(const Kv8AttnArgs& a, cudaStream_t stream);
+size_t attention_kv8_scratch_bytes(const pf_config& c, int M);
+// the scratch starts with one arrival counter per kv head, zero before the first launch and
+// after every launch that completes
+constexpr int KV8_MAX_HEADS = 1024;
+constexpr size_t KV8_COUNTER_BYTES = KV8_MAX_HEADS * sizeof(int);
+
+struct LogprobsArgs {
+  const float* logits;
+  int rows, n;
+  int64_t ld;
+  const int* tokens;
+  float* logprobs;
+  float* entropy;
+  int top;
+  int* top_ids;
+  float* top_logprobs;
+  int* status;
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t stream);
+
 cudaError_t launch_embed(const float* E, const int* tokens, int M, int H, int vocab, float* x,
                          int* status, cudaStream_t stream);
 cudaError_t launch_lm_head(int wfmt, const float* x_row, const float* norm_w, float eps,
@@ -214,6 +284,7 @@ enum TimelineId : int {
   TL_RMSNORM = 1, TL_RMSNORM_REG = 2, TL_QK_ROPE_KV = 3, TL_RING_STORE = 4, TL_EMBED = 5,
   TL_LM_HEAD = 6, TL_DEQUANT = 7, TL_SET_INT = 8, TL_ARGMAX = 9, TL_WAIT_SELFTEST = 10,
   TL_LM_HEAD_Q1 = 11, TL_ATTENTION_F32 = 12, TL_ATTENTION_TC = 13, TL_ATTN_COMBINE = 14,
+  TL_KV8_STORE = 15, TL_KV8_LOAD = 16, TL_ATTENTION_KV8 = 17, TL_LOGPROBS = 18,
   TL_GEMM = 20,        // + epilogue (0 store, 1 residual, 2 SwiGLU) + 3 for the CTA-pair form
   TL_GEMM_SMALL = 30,  // + epilogue
   TL_GEMV = 40         // + epilogue
@@ -225,6 +296,9 @@ cudaError_t timeline_set_gemm_small(unsigned long long* buf);
 cudaError_t timeline_set_gemv(unsigned long long* buf);
 cudaError_t timeline_set_attention(unsigned long long* buf);
 cudaError_t timeline_set_attention_tc(unsigned long long* buf);
+cudaError_t timeline_set_kv8(unsigned long long* buf);
+cudaError_t timeline_set_attention_kv8(unsigned long long* buf);
+cudaError_t timeline_set_logprobs(unsigned long long* buf);
 
 int device_sm_count();
 // Tiled tensor map over a 16-bit (bf16 if `bf16`, else f16) array of `rank` dims

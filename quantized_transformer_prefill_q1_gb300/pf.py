@@ -19,15 +19,15 @@ STATUS = {
     0: "PF_OK", 1: "PF_ERR_INVALID_ARG", 2: "PF_ERR_SHAPE", 3: "PF_ERR_EMPTY_CHUNK",
     4: "PF_ERR_NONSEQUENTIAL_START", 5: "PF_ERR_TOKEN_OUT_OF_VOCAB", 6: "PF_ERR_KV_CAPACITY",
     7: "PF_ERR_LOGITS", 8: "PF_ERR_UNSUPPORTED", 9: "PF_ERR_CUDA", 10: "PF_ERR_DEVICE_TIMEOUT",
-    11: "PF_ERR_WORKSPACE",
+    11: "PF_ERR_WORKSPACE", 12: "PF_ERR_NONFINITE",
 }
 W_Q1, W_INT4 = 0, 1
-KV_F32, KV_BF16, KV_F16 = 0, 1, 2
+KV_F32, KV_BF16, KV_F16, KV_E4M3, KV_INT8 = 0, 1, 2, 3, 4
 EPI_STORE_F32, EPI_RESID_ADD, EPI_SWIGLU = 0, 1, 2
 KERNEL_CLASSES = ("rmsnorm", "gemm_qkv", "qk_rope_kv", "attention", "gemm_o", "gemm_gate_up",
                   "gemm_down", "embed", "lm_head", "other")
 _WFMT = {"q1": W_Q1, "int4": W_INT4}
-_KVDT = {"f32": KV_F32, "bf16": KV_BF16, "f16": KV_F16}
+_KVDT = {"f32": KV_F32, "bf16": KV_BF16, "f16": KV_F16, "e4m3": KV_E4M3, "int8": KV_INT8}
 
 
 class PfError(RuntimeError):
@@ -48,6 +48,8 @@ class pf_config(ctypes.Structure):
                 ("sink_count", ctypes.c_int32), ("kv_block_pool", ctypes.c_int32)]
 
 KV_BLOCK = 128  # PF_KV_BLOCK: positions per paged KV block
+KV8_BLOCK = 32  # PF_KV8_BLOCK: slots that share one scale in an 8-bit cache
+MAX_TOP = 32    # PF_MAX_TOP: most alternatives per row of pf_op_logprobs
 
 
 class pf_layer_weights(ctypes.Structure):
@@ -110,6 +112,15 @@ _SIGS = {
     "pf_op_lm_head": ([_I32, _VP, _VP, _F, _VP, _I32, _I32, _VP, _VP], _I32),
     "pf_op_argmax": ([_VP, _I32, _I32, _I64, _VP, _VP], _I32),
     "pf_rope_table_host": ([_F, _I32, _I32, _VP], _I32),
+    "pf_op_logprobs": ([_VP, _I32, _I32, _I64, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP], _I32),
+    "pf_prefill_score": ([_VP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP], _I32),
+    "pf_kv8_scales_offset": ([ctypes.POINTER(pf_config)], _SZ),
+    "pf_op_kv8_store": ([ctypes.POINTER(pf_config), _VP, _VP, _I64, _I64, _I32, _I32, _I32, _VP, _VP, _VP, _VP,
+                         _VP], _I32),
+    "pf_op_kv8_load": ([ctypes.POINTER(pf_config), _VP, _I32, _I32, _I32, _VP, _VP, _VP, _VP], _I32),
+    "pf_attention_kv8_scratch_bytes": ([ctypes.POINTER(pf_config), _I32], _SZ),
+    "pf_op_attention_kv8": ([ctypes.POINTER(pf_config), _VP, _VP, _VP, _I32, _I32, _I32, _VP, _VP, _VP, _SZ, _VP,
+                             _VP], _I32),
     "pf_status_read": ([_VP, _VP], _I32),
     "pf_selftest_bounded_wait": ([_VP, _I64, _I32, _VP], _I32),
 }
@@ -275,6 +286,115 @@ def pf_op_argmax(x, rows, n, ld, out, stream=None):
     check(lib().pf_op_argmax(_ptr(x), rows, n, ld, _ptr(out), _stream(stream)))
 
 
+# Operators over the 8-bit cache and the logits: the tensors' device, type and layout are checked
+# here (PF_ERR_INVALID_ARG), everything else by the library.
+def _dense(t, dtype: str, what: str, numel: int, optional: bool = False) -> Optional[int]:
+    """Address of a contiguous tensor of the current CUDA device holding at least numel elements."""
+    if t is None:
+        if optional:
+            return None
+        raise PfError(1, f"{what} is None")
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise PfError(1, f"{what} is on {t.device}, not on the current CUDA device")
+    if t.dtype != getattr(torch, dtype) or not t.is_contiguous() or t.numel() < numel:
+        raise PfError(1, f"{what}: need at least {numel} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def _is_kv8(cfg) -> bool:
+    return cfg.kv_dtype in (KV_E4M3, KV_INT8)
+
+
+def _kv8_cache(cfg, t, what: str) -> Optional[int]:
+    return _dense(t, "uint8", what, lib().pf_kv_bytes(ctypes.byref(cfg)))
+
+
+def _kv8_table(cfg, t) -> Optional[int]:
+    return _dense(t, "int32", "block table", -(-cfg.max_seq // KV_BLOCK), True)
+
+
+def kv8_cache(cfg, device="cuda"):
+    """One zeroed 8-bit cache buffer (K or V): codes, then scales."""
+    import torch
+    check(lib().pf_config_check(ctypes.byref(cfg)))
+    return torch.zeros(lib().pf_kv_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=device)
+
+
+def kv8_views(cfg, cache):
+    """(codes [n_layers, nkv, slots, hd] float8_e4m3fn / int8, scales [n_layers, nkv, blocks] f32)
+    of one 8-bit cache buffer, as views of it."""
+    import torch
+    at = lib().pf_kv8_scales_offset(ctypes.byref(cfg))
+    if at == 0:
+        raise PfError(8, f"kv dtype {cfg.kv_dtype} is not an 8-bit type")
+    slots = cfg.kv_block_pool * KV_BLOCK if cfg.kv_block_pool > 0 else cfg.max_seq
+    n = cfg.n_layers * cfg.n_kv_heads * slots * cfg.head_dim
+    code = torch.float8_e4m3fn if cfg.kv_dtype == KV_E4M3 else torch.int8
+    nblk = -(-slots // KV8_BLOCK)
+    scales = cache[at:at + 4 * cfg.n_layers * cfg.n_kv_heads * nblk].view(torch.float32)
+    return (cache[:n].view(code).view(cfg.n_layers, cfg.n_kv_heads, slots, cfg.head_dim),
+            scales.view(cfg.n_layers, cfg.n_kv_heads, nblk))
+
+
+def pf_op_kv8_store(cfg, k, v, layer, start, m, k_cache, v_cache, blocks=None, status=None, stream=None):
+    """k, v: f16 [m, nkv, hd], any token and head strides (multiples of 8, the same for both)."""
+    import torch
+    shape = (m, cfg.n_kv_heads, cfg.head_dim)
+    for t in (k, v):
+        if (t.device.type != "cuda" or t.device.index != torch.cuda.current_device() or t.dtype != torch.float16
+                or tuple(t.shape) != shape or t.stride() != k.stride() or t.stride(2) != 1):
+            raise PfError(1, f"K / V rows: need f16 {shape} of equal strides with contiguous elements on the current "
+                             f"CUDA device, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}")
+    check(lib().pf_op_kv8_store(ctypes.byref(cfg), _ptr(k), _ptr(v), k.stride(0), k.stride(1), layer, start, m,
+                                _kv8_table(cfg, blocks), _kv8_cache(cfg, k_cache, "K cache"),
+                                _kv8_cache(cfg, v_cache, "V cache"), _dense(status, "int32", "status", 1, True),
+                                _stream(stream)))
+
+
+def pf_op_kv8_load(cfg, cache, layer, start, m, out, blocks=None, status=None, stream=None):
+    """out: f32 [m, nkv, hd], the values that one cache (K or V) holds at positions start .. start + m - 1."""
+    check(lib().pf_op_kv8_load(ctypes.byref(cfg), _kv8_cache(cfg, cache, "cache"), layer, start, m,
+                               _kv8_table(cfg, blocks),
+                               _dense(out, "float32", "out", max(m, 0) * cfg.n_kv_heads * cfg.head_dim),
+                               _dense(status, "int32", "status", 1, True), _stream(stream)))
+
+
+def pf_attention_kv8_scratch_bytes(cfg, m):
+    return lib().pf_attention_kv8_scratch_bytes(ctypes.byref(cfg), m)
+
+
+def attention_kv8_scratch(cfg, m, device="cuda"):
+    """Scratch (uint8 tensor, its counters zeroed) for pf_op_attention_kv8 on up to m tokens."""
+    import torch
+    check(lib().pf_config_check(ctypes.byref(cfg)))
+    return torch.zeros(pf_attention_kv8_scratch_bytes(cfg, m), dtype=torch.uint8, device=device)
+
+
+def pf_op_attention_kv8(cfg, q, k_cache, v_cache, layer, start, m, out, scratch, blocks=None, status=None,
+                        stream=None):
+    n = max(m, 0) * cfg.n_q_heads * cfg.head_dim
+    check(lib().pf_op_attention_kv8(ctypes.byref(cfg), _dense(q, "float16", "q", n),
+                                    _kv8_cache(cfg, k_cache, "K cache"), _kv8_cache(cfg, v_cache, "V cache"), layer,
+                                    start, m, _kv8_table(cfg, blocks), _dense(out, "float16", "out", n),
+                                    _dense(scratch, "uint8", "scratch", 0), scratch.numel(),
+                                    _dense(status, "int32", "status", 1, True), _stream(stream)))
+
+
+def pf_op_logprobs(logits, rows, n, ld, tokens, logprobs, entropy=None, top=0, top_ids=None, top_logprobs=None,
+                   status=None, stream=None):
+    """Log probability of tokens[r], entropy and the top alternatives of each row of logits [rows, ld]
+    (each output may be None)."""
+    r = max(rows, 0)
+    check(lib().pf_op_logprobs(_dense(logits, "float32", "logits", max(r - 1, 0) * ld + n), rows, n, ld,
+                               _dense(tokens, "int32", "tokens", r, True),
+                               _dense(logprobs, "float32", "logprobs", r, True),
+                               _dense(entropy, "float32", "entropy", r, True), top,
+                               _dense(top_ids, "int32", "top_ids", r * max(top, 0), True),
+                               _dense(top_logprobs, "float32", "top_logprobs", r * max(top, 0), True),
+                               _dense(status, "int32", "status", 1, True), _stream(stream)))
+
+
 def pf_op_embed(e, tokens, m, h, vocab, x, status=None, stream=None):
     check(lib().pf_op_embed(_ptr(e), _ptr(tokens), m, h, vocab, _ptr(x), _ptr(status),
                             _stream(stream)))
@@ -365,7 +485,7 @@ class DeviceModel:
             self.model.lm_head = _ptr(packed(extra["lm_head"]))
 
 
-_KV_TORCH = {KV_F32: "float32", KV_BF16: "bfloat16", KV_F16: "float16"}
+_KV_TORCH = {KV_F32: "float32", KV_BF16: "bfloat16", KV_F16: "float16", KV_E4M3: "uint8", KV_INT8: "uint8"}
 
 
 class Session:
@@ -383,6 +503,8 @@ class Session:
         slots = c.ring_capacity if c.ring_capacity > 0 else (
             c.kv_block_pool * KV_BLOCK if c.kv_block_pool > 0 else c.max_seq)
         shape = (c.n_layers, c.n_kv_heads, slots, c.head_dim)
+        if _is_kv8(c):  # codes and scales in one buffer (kv8_views)
+            shape = (lib().pf_kv_bytes(ctypes.byref(c)),)
         if kv is not None:
             self.k, self.v = kv
         else:
@@ -444,6 +566,18 @@ class Session:
         """Prefill of tokens_dev, then logits [M, vocab] and their argmax [M] at every position."""
         check(lib().pf_prefill_verify(self.h, _ptr(tokens_dev), tokens_dev.shape[0], start, _ptr(logits_all),
                                       _ptr(ids), _stream(stream)))
+
+    def prefill_score(self, tokens_dev, targets_dev, start: int, logits_all, logprobs, entropy=None, top: int = 0,
+                      top_ids=None, top_logprobs=None, stream=None) -> None:
+        """Prefill of tokens_dev, logits [M, vocab] at every position, then pf_op_logprobs of targets_dev [M]."""
+        m, r = tokens_dev.shape[0], tokens_dev.shape[0] * max(top, 0)
+        check(lib().pf_prefill_score(self.h, _dense(tokens_dev, "int32", "tokens", m),
+                                     _dense(targets_dev, "int32", "targets", m), m, start,
+                                     _dense(logits_all, "float32", "logits", m * self.dm.cfg.vocab),
+                                     _dense(logprobs, "float32", "logprobs", m),
+                                     _dense(entropy, "float32", "entropy", m, True), top,
+                                     _dense(top_ids, "int32", "top_ids", r, True),
+                                     _dense(top_logprobs, "float32", "top_logprobs", r, True), _stream(stream)))
 
     def set_profile(self, on: bool) -> None:
         check(lib().pf_session_set_profile(self.h, int(on)))
