@@ -147,6 +147,18 @@ bool encode_tmap_16(CUtensorMap* map, int bf16, int rank, const void* base, cons
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {inner};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(inner), box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_out_2d(CUtensorMap* map, bool f32, const void* base, uint64_t inner, uint64_t outer,
                         uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
   EncodeTiledFn fn = get_encode_fn();
@@ -264,9 +276,10 @@ pf_status check_cfg(const pf_config* c) {
     if (static_cast<int64_t>(c->kv_block_pool) * PF_KV_BLOCK > (int64_t{1} << 30))
       return fail(PF_ERR_SHAPE, "kv_block_pool %d too large", c->kv_block_pool);
   }
-  if (kv8(*c) && (c->max_seq > (1 << 30) || c->n_kv_heads > KV8_MAX_HEADS))
-    return fail(PF_ERR_SHAPE, "8-bit cache: max_seq %d (at most 2^30), kv heads %d (at most %d)", c->max_seq, c->n_kv_heads,
-                KV8_MAX_HEADS);
+  if (kv8(*c) && (c->max_seq > (1 << 30) || c->n_kv_heads > KV8_MAX_HEADS ||
+                  static_cast<int64_t>(c->n_kv_heads) * cache_slots(*c) > 0x7fffffff))
+    return fail(PF_ERR_SHAPE, "8-bit cache: max_seq %d (at most 2^30), kv heads %d (at most %d), kv heads x slots below 2^31",
+                c->max_seq, c->n_kv_heads, KV8_MAX_HEADS);
   return PF_OK;
 }
 
@@ -532,6 +545,7 @@ void prepare_all() {
     prepare_gemm_small_kernels();
     prepare_attention_kernels();
     prepare_attention_tc_kernels();
+    prepare_attention_kv8_kernels();
   });
 }
 

@@ -210,6 +210,10 @@ struct Kv8AttnArgs {
   const int* blocks;
   int* status;
 };
+// Tiled tensor map over bytes [rows][inner] (inner 128 or 64), boxes of box_rows whole rows, swizzled
+// by the row's width.
+bool encode_tmap_8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
+cudaError_t prepare_attention_kv8_kernels();
 cudaError_t launch_attention_kv8(const Kv8AttnArgs& a, cudaStream_t stream);
 size_t attention_kv8_scratch_bytes(const pf_config& c, int M);
 // the scratch starts with one arrival counter per kv head, zero before the first launch and
