@@ -546,6 +546,7 @@ void prepare_all() {
     prepare_attention_kernels();
     prepare_attention_tc_kernels();
     prepare_attention_kv8_kernels();
+    prepare_attention_kv8_tc_kernels();
   });
 }
 
@@ -848,6 +849,7 @@ pf_status pf_timeline_set(uint64_t* buffer, int64_t capacity) {
   PF_CUDA(timeline_set_attention_tc(b), "timeline");
   PF_CUDA(timeline_set_kv8(b), "timeline");
   PF_CUDA(timeline_set_attention_kv8(b), "timeline");
+  PF_CUDA(timeline_set_attention_kv8_tc(b), "timeline");
   PF_CUDA(timeline_set_logprobs(b), "timeline");
   return PF_OK;
 }
@@ -855,11 +857,11 @@ pf_status pf_timeline_set(uint64_t* buffer, int64_t capacity) {
 const char* pf_timeline_kernel_name(int32_t id) {
   static const std::vector<std::string> names = [] {
     std::vector<std::string> n(64);
-    const char* fixed[19] = {"", "rmsnorm", "rmsnorm_reg", "qk_norm_rope_kv", "ring_store", "embed",
+    const char* fixed[20] = {"", "rmsnorm", "rmsnorm_reg", "qk_norm_rope_kv", "ring_store", "embed",
                              "lm_head", "dequant", "set_int", "argmax_rows", "wait_selftest", "lm_head_q1",
                              "attention_f32", "attention_tc", "attn_combine", "kv8_store", "kv8_load",
-                             "attention_kv8", "logprobs"};
-    for (int i = 1; i < 19; ++i) n[i] = fixed[i];
+                             "attention_kv8", "logprobs", "attention_kv8_tc"};
+    for (int i = 1; i < 20; ++i) n[i] = fixed[i];
     const char* epi[3] = {"store", "resid", "swiglu"};
     for (int e = 0; e < 3; ++e) {
       n[TL_GEMM + e] = std::string("gemm_") + epi[e];

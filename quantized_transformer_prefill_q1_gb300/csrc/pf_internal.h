@@ -214,6 +214,10 @@ struct Kv8AttnArgs {
 // by the row's width.
 bool encode_tmap_8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
 cudaError_t prepare_attention_kv8_kernels();
+// the form for more rows than the few-row kernel takes (attention_kv8_tc.cu); no scratch
+cudaError_t prepare_attention_kv8_tc_kernels();
+cudaError_t launch_attention_kv8_tc(const Kv8AttnArgs& a, const Kv8Layer& layer, cudaStream_t stream);
+cudaError_t timeline_set_attention_kv8_tc(unsigned long long* buf);
 cudaError_t launch_attention_kv8(const Kv8AttnArgs& a, cudaStream_t stream);
 size_t attention_kv8_scratch_bytes(const pf_config& c, int M);
 // the scratch starts with one arrival counter per kv head, zero before the first launch and
@@ -262,6 +266,27 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Same, in clusters of `cs` CTAs along x (the grid's x extent a multiple of cs).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t stream, int cs, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 // Same, in clusters of two CTAs along x (the grid's x extent even).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl_pairs(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
@@ -288,7 +313,7 @@ enum TimelineId : int {
   TL_RMSNORM = 1, TL_RMSNORM_REG = 2, TL_QK_ROPE_KV = 3, TL_RING_STORE = 4, TL_EMBED = 5,
   TL_LM_HEAD = 6, TL_DEQUANT = 7, TL_SET_INT = 8, TL_ARGMAX = 9, TL_WAIT_SELFTEST = 10,
   TL_LM_HEAD_Q1 = 11, TL_ATTENTION_F32 = 12, TL_ATTENTION_TC = 13, TL_ATTN_COMBINE = 14,
-  TL_KV8_STORE = 15, TL_KV8_LOAD = 16, TL_ATTENTION_KV8 = 17, TL_LOGPROBS = 18,
+  TL_KV8_STORE = 15, TL_KV8_LOAD = 16, TL_ATTENTION_KV8 = 17, TL_LOGPROBS = 18, TL_ATTENTION_KV8_TC = 19,
   TL_GEMM = 20,        // + epilogue (0 store, 1 residual, 2 SwiGLU) + 3 for the CTA-pair form
   TL_GEMM_SMALL = 30,  // + epilogue
   TL_GEMV = 40         // + epilogue
