@@ -33,9 +33,8 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_ca
 // thread and pass, the block's new rows held in registers between the maximum and the rounding, so
 // each row is read once. Bound: latency at one token (one CTA per head), HBM at long chunks.
 template <int HD, int T>
-__global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* __restrict__ kx,
-                                                               const __half* __restrict__ vx, long long tok_stride,
-                                                               long long head_stride, const int* __restrict__ start_dev,
+__global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx, const __half* vx, long long tok_stride,
+                                                               long long head_stride, const int* start_dev,
                                                                int start_host, int M, Kv8Layer c, int* status) {
   PF_TIMELINE(TL_KV8_STORE);
   constexpr int LPR = HD / 8;                // threads per row
@@ -129,9 +128,9 @@ __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* __r
 
 // Read-back: out[t][kvh][i] = code * scale of position start + t, four codes a thread. HBM bound.
 template <int T>
-__global__ void __launch_bounds__(256) kv8_load_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
+__global__ void __launch_bounds__(256) kv8_load_kernel(const uint8_t* codes, const float* scales,
                                                        Kv8Layer c, int hd, int nkv, int start, long long quads,
-                                                       float4* __restrict__ out, int* status) {
+                                                       float4* out, int* status) {
   PF_TIMELINE(TL_KV8_LOAD);
   griddep_launch_dependents();
   griddep_wait();
