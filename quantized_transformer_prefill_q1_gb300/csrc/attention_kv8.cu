@@ -471,7 +471,7 @@ cudaError_t launch_few(const Kv8AttnArgs& a, const Kv8Layer& L, cudaStream_t str
   const pf_config& c = *a.c;
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(c.n_kv_heads) * L.slots;
-  if (!encode_tmap_8(&tk, L.k, HD, rows, UK) || !encode_tmap_8(&tv, L.v, HD, rows, UK)) return cudaErrorInvalidValue;
+  if (!encode_tmap_8(&tk, L.k, HD, rows, HD, UK, HD) || !encode_tmap_8(&tv, L.v, HD, rows, HD, UK, HD)) return cudaErrorInvalidValue;
   DecParams p{};
   p.c = L;
   p.q = static_cast<const __half*>(a.q);

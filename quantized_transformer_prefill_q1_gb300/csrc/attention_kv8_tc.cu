@@ -5,25 +5,30 @@
 // scale touches a code, and every code is exact in f16.
 //
 // One CTA = one kv head and 128 of its query rows (row = token * G + head in the group) against its
-// share of the key tiles: a cluster of CTAs shares the rows and cuts the keys between them; at the end
+// share of the key tiles: a cluster shares the rows and cuts the keys between its CTAs; at the end
 // every CTA leaves its rows' sums, maxima and O in its shared memory, and each merges its share of the
 // rows over the cluster. No scratch and no second kernel.
 //
-// Warps (20):
-//   0, 2     copies: the Q tile and the K codes (0), the V codes (2), 16 KB a tile at hd 128 into two
-//            stages each;
-//   1        TMEM (three S buffers of 128 columns and O) and the MMAs: S_0, S_1, then per key tile
-//            S_{j+2} = Q K_{j+2}^T and O += P_j V_j (P over S's columns);
-//   4..7     K, 8..11 V: codes converted to f16 into shared memory in the MMA's 128-byte swizzle, two
-//            stages each; the scales;
-//   12..15   softmax of the even key tiles, 16..19 of the odd ones, one thread per row, so that one
+// At hd 128 and more than one row tile, two CTAs work as a pair (cta_group::2, M = 256): two row tiles
+// of the same kv head, the same key tiles, and each CTA converts only half of them (K: 64 of the 128
+// keys, V: 64 of the 128 columns), which is also all that its tensor core reads of them from its own
+// shared memory. One CTA alone moves 224 KB a key tile through shared memory (codes in and out, f16
+// written, read by both products, Q), 1,750 cycles at 128 B a cycle against 1,400 of tensor work; a
+// CTA of a pair 128 KB.
+//
+// Warps (16, registers moved between the warpgroups):
+//   0, 2     copies: Q and the K codes (0), the V codes (2), ST stages ahead;
+//   1        TMEM (three S buffers of 128 columns and O) and the MMAs, S_j = Q K_j^T and
+//            O += P_j V_j (P over S's columns), whichever is ready (in a pair, the even CTA's);
+//   4..7     K and V codes to f16, into shared memory in the MMA's 128-byte swizzle; the scales;
+//   8..11    softmax of the even key tiles, 12..15 of the odd ones, one thread per row, so that one
 //            tile's exponentials run while the next one's maximum is taken. The two share each row's
 //            running maximum: a tile's decision to raise it (only when exceeded by more than 2^8; O is
 //            then rescaled in TMEM) follows the previous tile's, warp by warp through a barrier; the
-//            rest runs side by side. A row's 128 scores stay in registers, which the other
-//            warpgroups give up (setmaxnreg).
+//            rest runs side by side. A row's 128 scores stay in registers.
 // Every wait is bounded; a timeout aborts the CTA and records PF_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv8.cuh"
 
@@ -32,28 +37,33 @@ namespace {
 
 constexpr int TQ = 128;  // rows per CTA
 constexpr int TK = 128;  // keys per tile: one page, four scale blocks
-constexpr int ST = 2;    // K and V stages
 constexpr int NSB = 3;   // S / P buffers
-constexpr int THREADS = 640;
+constexpr int THREADS = 512;
+constexpr int SM_WARP = 8;        // first softmax warp
 constexpr int SM_THREADS = 256;   // softmax threads: two groups of one per row
-constexpr int DQ_THREADS = 128;   // converting threads, K and V each
+constexpr int DQ_THREADS = 128;   // converting threads
 constexpr int NG = TK / PF_KV8_BLOCK;
-constexpr int SCR = 8;   // tiles in the ring of scales (K's conversion may run 4 tiles ahead of a softmax)
+constexpr int SCR = 8;   // tiles in the ring of scales (K's conversion may run 5 tiles ahead of a softmax)
 constexpr int MAX_CLUSTER = 8;
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t COL_O = NSB * TK;  // TMEM: S buffer b at b TK, O at COL_O
 
-template <int HD>
+template <int HD, int PAIR>
 struct TSmem {
+  static constexpr int ST = PAIR ? 3 : 2;          // stages of codes and of f16 tiles, K and V each
+  static constexpr int KR = PAIR ? TK / 2 : TK;    // keys of a K tile that this CTA holds
+  static constexpr int VC = PAIR ? HD / 2 : HD;    // columns of a V tile that this CTA holds
   static constexpr int Q = TQ * HD * 2;
-  static constexpr int KV = TK * HD * 2;
+  static constexpr int KT = KR * HD * 2;           // f16 tiles
+  static constexpr int VT = TK * VC * 2;
+  static constexpr int KCODES = KR * HD;
+  static constexpr int VCODES = TK * VC;
   static constexpr int ROW = HD * 4;  // a row of O at the end, over the idle Q and K tiles
-  static constexpr int CODES = TK * HD;  // codes of a K or V tile
-  static constexpr int TILES = Q + 2 * ST * KV;
-  static constexpr int RINGS = 2 * ST * CODES;
+  static constexpr int TILES = Q + ST * (KT + VT);
+  static constexpr int RINGS = ST * (KCODES + VCODES);
   static constexpr int SCALES = SCR * NG * 4 * 4;
   static constexpr int MAXIMA = TQ * 4;
-  static constexpr int BARS = 384;
+  static constexpr int BARS = 512;
   static constexpr int BYTES = 1024 + TILES + RINGS + SCALES + MAXIMA + BARS;
   // at the end, over the idle tiles: O; over the idle rings: (m, l) of each row, the groups' sums, the
   // weights of the parts
@@ -66,7 +76,7 @@ struct TcParams {
   const int* start_dev;
   int start_host;
   float scale_log2;
-  int cs;  // CTAs per cluster
+  int cs;  // parts of the keys: CTAs (pairs) per cluster
   __half* out;
   int* status;
 };
@@ -118,6 +128,26 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
     }
   }
 }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Pair MMA with A (256 rows: 128 in each CTA's tensor memory at a_tmem) from tensor memory.
+__device__ __forceinline__ void umma_pair_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                      uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -139,8 +169,8 @@ __device__ __forceinline__ float4 ldc128(uint32_t a) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
-// Registers a thread from here on (all warps of a warpgroup alike): 128 x (32 + 56 + 56 + 168 + 168)
-// is the 640 x 96 that the CTA is launched with.
+// Registers a thread from here on (all warps of a warpgroup alike): 128 x (32 + 96 + 192 + 192) is the
+// 512 x 128 that the CTA is launched with.
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -167,61 +197,61 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
-template <int HD, int T>
+template <int HD, int T, int PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const TcParams P) {
+    attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const TcParams P) {
   PF_TIMELINE(TL_ATTENTION_KV8_TC);
-  using L = TSmem<HD>;
+  using L = TSmem<HD, PAIR>;
+  constexpr int ST = L::ST;
   constexpr int NH = HD / 64;  // 64-wide swizzle regions along head_dim
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t q_s = base, k_s = q_s + L::Q, v_s = k_s + ST * L::KV;
-  const uint32_t kc_s = base + L::TILES, vc_s = kc_s + ST * L::CODES;
+  const uint32_t q_s = base, k_s = q_s + L::Q, v_s = k_s + ST * L::KT;
+  const uint32_t kc_s = base + L::TILES, vc_s = kc_s + ST * L::KCODES;
   float4* scales = reinterpret_cast<float4*>(gbase + L::TILES + L::RINGS);  // [SCR][NG] (log2(e) sK / sqrt(hd), log2 sV, 1 / sV, -)
   const uint32_t sc_s = base + L::TILES + L::RINGS;
   volatile float* run_m = reinterpret_cast<volatile float*>(gbase + L::TILES + L::RINGS + L::SCALES);  // [TQ] running maxima
   const uint32_t ml_s = kc_s;  // [TQ] (m, l)
   volatile float* sums = reinterpret_cast<volatile float*>(gbase + L::TILES + TQ * 8);  // [2][TQ]
   const uint32_t bar0 = base + L::TILES + L::RINGS + L::SCALES + L::MAXIMA;
-  auto k_full = [&](int s) { return bar0 + 8u * s; };
-  auto k_empty = [&](int s) { return bar0 + 8u * (2 + s); };
-  auto v_full = [&](int s) { return bar0 + 8u * (4 + s); };
-  auto v_empty = [&](int s) { return bar0 + 8u * (6 + s); };
-  auto s_full = [&](int b) { return bar0 + 8u * (8 + b); };
-  auto s_empty = [&](int b) { return bar0 + 8u * (11 + b); };
-  auto p_full = [&](int b) { return bar0 + 8u * (14 + b); };
-  auto turn = [&](int quarter, int x) { return bar0 + 8u * (17 + 2 * quarter + x); };  // group x's decision on its tile
-  auto sc_full = [&](int s) { return bar0 + 8u * (25 + s); };
-  auto c_full = [&](int v, int s) { return bar0 + 8u * (33 + 2 * v + s); };   // codes of K (v 0), V (1)
-  auto c_empty = [&](int v, int s) { return bar0 + 8u * (37 + 2 * v + s); };
-  const uint32_t q_full = bar0 + 8u * 41, o_final = bar0 + 8u * 42, drain_bar = bar0 + 8u * 43;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (bar0 + 8u * 44 - base));
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bar0 + 8u * 45 - base));
-  static_assert(SCR == 8 && ST == 2 && 8 * 46 <= L::BARS, "barrier area");
+  auto full = [&](int v, int s) { return bar0 + 8u * (3 * v + s); };           // f16 tiles of K (v 0), V (1)
+  auto empty = [&](int v, int s) { return bar0 + 8u * (6 + 3 * v + s); };
+  auto c_full = [&](int v, int s) { return bar0 + 8u * (12 + 3 * v + s); };    // codes
+  auto c_empty = [&](int v, int s) { return bar0 + 8u * (18 + 3 * v + s); };
+  auto s_full = [&](int b) { return bar0 + 8u * (24 + b); };
+  auto s_empty = [&](int b) { return bar0 + 8u * (27 + b); };
+  auto p_full = [&](int b) { return bar0 + 8u * (30 + b); };
+  auto turn = [&](int quarter, int x) { return bar0 + 8u * (33 + 2 * quarter + x); };  // group x's decision on its tile
+  auto sc_full = [&](int s) { return bar0 + 8u * (41 + s); };
+  const uint32_t q_full = bar0 + 8u * 49, q_ready = bar0 + 8u * 50, o_final = bar0 + 8u * 51, drain_bar = bar0 + 8u * 52;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (bar0 + 8u * 53 - base));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bar0 + 8u * 54 - base));
+  static_assert(SCR == 8 && ST <= 3 && 8 * 55 <= L::BARS, "barrier area");
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(k_full(s), DQ_THREADS);
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), DQ_THREADS);
-      mbar_init(v_empty(s), 1);
+    // arrivals are one a warp; a pair's tiles, probabilities and Q are awaited in the even CTA
+    constexpr int BOTH = PAIR ? 2 : 1;
+    for (int s = 0; s < ST; ++s)
       for (int v = 0; v < 2; ++v) {
+        mbar_init(full(v, s), 4 * BOTH);
+        mbar_init(empty(v, s), 1);
         mbar_init(c_full(v, s), 1);
-        mbar_init(c_empty(v, s), DQ_THREADS);
+        mbar_init(c_empty(v, s), 4);
       }
-    }
     for (int b = 0; b < NSB; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(s_empty(b), 1);
-      mbar_init(p_full(b), TQ);
+      mbar_init(p_full(b), 4 * BOTH);
     }
     for (int i = 0; i < 4; ++i)
       for (int x = 0; x < 2; ++x) mbar_init(turn(i, x), 1);
     for (int s = 0; s < SCR; ++s) mbar_init(sc_full(s), NG);
     mbar_init(q_full, 1);
+    mbar_init(q_ready, BOTH);
     mbar_init(o_final, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -230,53 +260,79 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (threadIdx.x < TQ) run_m[threadIdx.x] = -INFINITY;
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();  // the other CTA's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
   const int start = P.start_dev ? *P.start_dev : P.start_host;
   const int G = P.nq / P.nkv, BT = TQ / G;  // tokens per CTA
-  const int n_set = (P.M + BT - 1) / BT;
-  const int cs = P.cs, rank = static_cast<int>(blockIdx.x) % cs;
-  const int set = n_set - 1 - static_cast<int>(blockIdx.x) / cs;  // longest rows first
+  const int cs = P.cs;
+  constexpr int W = PAIR ? 2 : 1;            // row tiles that share their key tiles
+  const int n_set = (P.M + W * BT - 1) / (W * BT);
+  const int rank = static_cast<int>(blockIdx.x) % (W * cs);   // in the cluster
+  const int half = PAIR ? rank & 1 : 0, part = rank / W;
+  const int set = n_set - 1 - static_cast<int>(blockIdx.x) / (W * cs);  // longest rows first
   const int kvh = blockIdx.y;
-  const int t0 = set * BT, t1 = min(t0 + BT, P.M);
-  const int len = start + t1;  // keys that the last row sees
+  const int t0 = (set * W + half) * BT, t1 = min(t0 + BT, P.M);  // a pair's second tile may lie past the last token
+  const int len = start + min((set + 1) * W * BT, P.M);  // keys that the last row sees
   const int n_tiles = (len + TK - 1) / TK;
-  const int jb = static_cast<int>(static_cast<long long>(n_tiles) * rank / cs);
-  const int nt = static_cast<int>(static_cast<long long>(n_tiles) * (rank + 1) / cs) - jb;  // this CTA's tiles jb ..
+  const int jb = static_cast<int>(static_cast<long long>(n_tiles) * part / cs);
+  const int nt = static_cast<int>(static_cast<long long>(n_tiles) * (part + 1) / cs) - jb;  // this CTA's tiles jb ..
   bool all_ok = true;
-
   auto slot_of = [&](int j) {  // of the CTA's tile j; 0 for an entry outside the pool
     const int s = kv8_slot(P.c, (jb + min(j, nt - 1)) * TK);
     if (s < 0 && lane == 0 && P.status) atomicCAS(P.status, 0, PF_ERR_KV_CAPACITY);
     return max(s, 0);
   };
   auto valid_of = [&](int j) { return min(TK, len - (jb + j) * TK); };  // keys of tile j that some row sees
+  // one arrival of a converged warp, on the even CTA's barrier in a pair
+  auto arrive = [&](uint32_t bar) {
+    __syncwarp();
+    if (lane == 0) {
+      if (PAIR && half)
+        mbar_arrive_cta(bar, rank - 1);
+      else
+        mbar_arrive(bar);
+    }
+  };
 
   if (warp < 4) {
     regs_dec<32>();
     if ((warp == 0 || warp == 2) && lane == 0) {
       // -------------------------------------------------------------- copies
       const int v = warp >> 1;
-      const uint8_t* codes = (v ? P.c.v : P.c.k) + static_cast<size_t>(kvh) * P.c.slots * HD;
       if (v == 0) {
         mbar_arrive_expect_tx(q_full, L::Q);
         for (int h = 0; h < NH; ++h) tma_load_3d(q_s + h * (TQ * 128), &tm_q, h * 64, kvh * G, t0, q_full);
       }
+      // K: this CTA's keys, all columns; V: all keys, this CTA's columns (rows past the cache are zeros)
+      const CUtensorMap* map = v ? &tm_v : &tm_k;
+      const uint32_t ring = v ? vc_s : kc_s, bytes = v ? L::VCODES : L::KCODES;
+      const int x0 = v ? half * L::VC : 0, y0 = kvh * P.c.slots + (v ? 0 : half * L::KR);
       int issued = 0, slot = nt > 0 ? slot_of(0) : 0;
       for (int j = 0; j < nt; ++j) {
         const int st = j % ST, next = slot_of(j + 1);
         if (!mbar_wait_long(c_empty(v, st), ((j / ST) & 1) ^ 1, abort_flag)) break;
-        const uint32_t bytes = static_cast<uint32_t>(valid_of(j)) * HD;
         mbar_arrive_expect_tx(c_full(v, st), bytes);
-        bulk_load((v ? vc_s : kc_s) + st * L::CODES, codes + static_cast<size_t>(slot) * HD, bytes, c_full(v, st));
+        tma_load_2d(ring + st * bytes, map, x0, y0 + slot, c_full(v, st));
         ++issued;
         slot = next;
+        if (j == 0 && v == 0 && mbar_wait_long(q_full, 0, abort_flag)) {
+          if (PAIR && half)
+            mbar_arrive_cta(q_ready, rank - 1);
+          else
+            mbar_arrive(q_ready);
+        }
       }
       // landed before shared memory is used otherwise, whatever the others do
       if (v == 0) wait_drain(q_full, 0);
@@ -286,86 +342,118 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc_s = idesc_f16(TQ, TK, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f16(TQ, HD, 0, 1);
-    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort_flag)) != 0; };
-    auto issue_s = [&](int j) -> bool {
-      const int b = j % NSB, st = j % ST;
-      if (!wait(k_full(st), (j / ST) & 1) || !wait(s_empty(b), ((j / NSB) & 1) ^ 1)) return false;
-      tc_fence_after();
+    if (half == 0) {
+      constexpr uint32_t idesc_s = idesc_f16(PAIR ? 2 * TQ : TQ, TK, 0, 0);
+      constexpr uint32_t idesc_o = idesc_f16(PAIR ? 2 * TQ : TQ, HD, 0, 1);
+      const uint16_t mask = static_cast<uint16_t>(3u << rank);
+      auto commit = [&](uint32_t bar) {
+        if (PAIR)
+          umma_pair_commit_warp(bar, mask);
+        else
+          umma_commit_warp(bar);
+      };
+      bool ok = nt == 0 || __all_sync(0xffffffffu, mbar_wait_long(q_ready, 0, abort_flag));
+      // S_js and PV_jp are next. The next tile's scores go before a tile's PV (its softmax waits for
+      // them), those after it behind: a PV that is ready then leaves no gap while S waits for a buffer.
+      int js = 0, jp = 0;
+      uint64_t t_idle = 0;
+      while (ok && jp < nt) {
+        auto s_ready = [&] {
+          return js < nt && __all_sync(0xffffffffu, mbar_test(full(0, js % ST), (js / ST) & 1) &&
+                                                        mbar_test(s_empty(js % NSB), ((js / NSB) & 1) ^ 1));
+        };
+        auto p_ready = [&] {
+          return jp < js && __all_sync(0xffffffffu, mbar_test(p_full(jp % NSB), (jp / NSB) & 1) &&
+                                                        mbar_test(full(1, jp % ST), (jp / ST) & 1));
+        };
+        const bool s_first = js <= jp + 1;
+        bool do_s = s_first && s_ready(), do_p = !do_s && p_ready();
+        if (!do_s && !do_p && !s_first) do_s = s_ready();
+        if (do_s) {
+          const int b = js % NSB, st = js % ST;
+          tc_fence_after();
 #pragma unroll
-      for (int kc = 0; kc < HD / 16; ++kc) {
-        const uint32_t off = (kc >> 2) * (TQ * 128) + (kc & 3) * 32;
-        umma_f16_ss_warp(tmem + b * TK, sdesc_kmajor_sw128(q_s + off), sdesc_kmajor_sw128(k_s + st * L::KV + off), idesc_s, kc > 0);
+          for (int kc = 0; kc < HD / 16; ++kc) {
+            const uint64_t qd = sdesc_kmajor_sw128(q_s + (kc >> 2) * (TQ * 128) + (kc & 3) * 32);
+            const uint64_t kd = sdesc_kmajor_sw128(k_s + st * L::KT + (kc >> 2) * (L::KR * 128) + (kc & 3) * 32);
+            if (PAIR)
+              umma_pair_f16_ss_warp(tmem + b * TK, qd, kd, idesc_s, kc > 0);
+            else
+              umma_f16_ss_warp(tmem + b * TK, qd, kd, idesc_s, kc > 0);
+          }
+          commit(s_full(b));
+          commit(empty(0, st));
+          ++js;
+        } else if (do_p) {
+          const int b = jp % NSB, st = jp % ST;
+          tc_fence_after();
+#pragma unroll
+          for (int kc = 0; kc < TK / 16; ++kc) {
+            const uint64_t vd = sdesc_mnmajor_sw128(v_s + st * L::VT + kc * 2048, TK * 128);
+            if (PAIR)
+              umma_pair_f16_ts_warp(tmem + COL_O, tmem + b * TK + 8 * kc, vd, idesc_o, jp > 0 || kc > 0);
+            else
+              umma_f16_ts_warp(tmem + COL_O, tmem + b * TK + 8 * kc, vd, idesc_o, jp > 0 || kc > 0);
+          }
+          commit(s_empty(b));
+          commit(empty(1, st));
+          ++jp;
+        } else {
+          const uint64_t now = global_timer_ns();
+          if (t_idle == 0) t_idle = now;
+          const bool give_up = *abort_flag || now - t_idle > PF_WAIT_LIMIT_NS;
+          if (__any_sync(0xffffffffu, give_up)) {
+            *abort_flag = 1;
+            ok = false;
+          }
+          continue;
+        }
+        t_idle = 0;
       }
-      umma_commit_warp(s_full(b));
-      umma_commit_warp(k_empty(st));
-      return true;
-    };
-    bool ok = nt == 0 || wait(q_full, 0);
-    if (ok && nt > 0) ok = issue_s(0);
-    if (ok && nt > 1) ok = issue_s(1);
-    for (int j = 0; j < nt && ok; ++j) {
-      const int b = j % NSB, st = j % ST;
-      // S_{j+2} as soon as PV_{j-1} has left its buffer, not behind P_j: the softmax group that
-      // finishes tile j finds its next scores ready
-      if (j + 2 < nt && !(ok = issue_s(j + 2))) break;
-      ok = wait(p_full(b), (j / NSB) & 1) && wait(v_full(st), (j / ST) & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kc = 0; kc < TK / 16; ++kc)
-        umma_f16_ts_warp(tmem + COL_O, tmem + b * TK + 8 * kc, sdesc_mnmajor_sw128(v_s + st * L::KV + kc * 2048, TK * 128), idesc_o,
-                         j > 0 || kc > 0);
-      umma_commit_warp(s_empty(b));
-      umma_commit_warp(v_empty(st));
+      if (ok) {
+        commit(o_final);
+      } else {
+        commit(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
     }
-    if (ok) {
-      umma_commit_warp(o_final);
-    } else {
-      umma_commit_warp(drain_bar);
-      wait_drain(drain_bar, 0);
-    }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < SM_WARP) {
     // ---------------------------------------------------------------- codes to f16
-    regs_dec<56>();
-    const int v = warp >= 8 ? 1 : 0;
-    constexpr int LPR = HD / 8;                // threads per row, 8 codes each: 16 B of f16
-    constexpr int RPP = DQ_THREADS / LPR;      // rows per pass, a multiple of 8: the swizzle is the same in every pass
-    constexpr int NP = TK / RPP;
-    const int tid = threadIdx.x - (v ? 256 : 128);
-    const int row0 = tid / LPR, c8 = tid % LPR;
-    const uint32_t put = (c8 >> 3) * (TK * 128) + row0 * 128 + (((c8 & 7) ^ (row0 & 7)) << 4);
-    // the scales of tile j's block tid (K threads 0 .. 3); 1 for a block past the sequence
+    regs_dec<96>();
+    const int tid = threadIdx.x - 128;
+    // the scales of tile j's block tid (threads 0 .. 3); 1 for a block past the sequence
     float sk = 1.f, sv = 1.f;
     auto load_scales = [&](int j) {
       sk = sv = 1.f;
-      if (v == 0 && tid < NG && j < nt && tid * PF_KV8_BLOCK < valid_of(j)) {
+      if (tid < NG && j < nt && tid * PF_KV8_BLOCK < valid_of(j)) {
         const int slot = max(kv8_slot(P.c, (jb + j) * TK), 0);
         const size_t at = static_cast<size_t>(kvh) * P.c.nblk + slot / PF_KV8_BLOCK + tid;
         sk = P.c.ks[at];
         sv = P.c.vs[at];
       }
     };
-    load_scales(0);
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % ST;
-      const uint32_t codes = (v ? vc_s : kc_s) + st * L::CODES;
-      if (!mbar_wait_long(c_full(v, st), (j / ST) & 1, abort_flag)) break;
+    // A tile of ROWS x C codes (K or V of tile j): 8 codes a thread and pass, one 16-byte piece of f16 in
+    // regions of 64 columns (rows of 128 B, swizzled). Rows a pass are a multiple of 8: one swizzle.
+    auto convert = [&](auto rows_c, auto cols_c, int v, int j, uint32_t ring, uint32_t tiles, int valid) -> bool {
+      constexpr int ROWS = decltype(rows_c)::value, C = decltype(cols_c)::value;
+      constexpr int LPR = C / 8, RPP = DQ_THREADS / LPR, NP = ROWS / RPP;
+      const int st = j % ST, row0 = tid / LPR, c8 = tid % LPR;
+      const uint32_t codes = ring + st * (ROWS * C) + tid * 8;
+      const uint32_t put = tiles + st * (ROWS * C * 2) + (c8 >> 3) * (ROWS * 128) + row0 * 128 + (((c8 & 7) ^ (row0 & 7)) << 4);
+      if (!__all_sync(0xffffffffu, mbar_wait_long(c_full(v, st), (j / ST) & 1, abort_flag))) return false;
       // the codes into registers at once: their stage takes the next copy while these wait for room
-      const int valid = valid_of(j);
       uint2 w[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        w[i] = make_uint2(0, 0);  // keys past the last row's are zeros
+        w[i] = make_uint2(0, 0);  // keys past the last row's are zeros: their codes may be NaN
         if (row0 + i * RPP < valid)
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i].x), "=r"(w[i].y) : "r"(codes + tid * 8 + i * RPP * HD));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i].x), "=r"(w[i].y) : "r"(codes + i * RPP * C));
       }
-      mbar_arrive(c_empty(v, st));
-      if (!mbar_wait_long(v ? v_empty(st) : k_empty(st), ((j / ST) & 1) ^ 1, abort_flag)) break;
-      const uint32_t tile = (v ? v_s : k_s) + st * L::KV;
-      // K_{j-2}'s product is done, so PV_{j-5} is: softmaxes of tiles j - 4 on may still read their scales
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c_empty(v, st));
+      if (!__all_sync(0xffffffffu, mbar_wait_long(empty(v, st), ((j / ST) & 1) ^ 1, abort_flag))) return false;
       if (v == 0 && tid < NG) {
+        // (K_{j-3}'s product is done, so PV_{j-6} is: softmaxes of tiles j - 5 on may still read their scales)
         const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);
         // the factor of the scores stays > 0: a hidden key's -inf stays -inf
         scales[(j % SCR) * NG + tid] = make_float4(fmaxf(sk * P.scale_log2, 1e-37f), __log2f(svc), 1.f / svc, 0.f);
@@ -376,16 +464,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t h0, h1, h2, h3;
         Kv8<T>::pairs(w[i].x, h0, h1);
         Kv8<T>::pairs(w[i].y, h2, h3);
-        sts128(tile + put + i * RPP * 128, h0, h1, h2, h3);
+        sts128(put + i * RPP * 128, h0, h1, h2, h3);
       }
       fence_proxy_async_smem();
-      mbar_arrive(v ? v_full(st) : k_full(st));
+      arrive(full(v, st));
+      return true;
+    };
+    load_scales(0);
+    for (int j = 0; j < nt; ++j) {
+      const int valid = valid_of(j);
+      if (!convert(std::integral_constant<int, L::KR>{}, std::integral_constant<int, HD>{}, 0, j, kc_s, k_s, valid - half * L::KR)) break;
       load_scales(j + 1);
+      if (!convert(std::integral_constant<int, TK>{}, std::integral_constant<int, L::VC>{}, 1, j, vc_s, v_s, valid)) break;
     }
-  } else if (warp >= 12) {
+  } else if (warp >= SM_WARP) {
     // ---------------------------------------------------------------- softmax rows
-    regs_inc<168>();
-    const int x = (warp - 12) >> 2, quarter = warp & 3;
+    regs_inc<192>();
+    const int x = (warp - SM_WARP) >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane;
     const uint32_t lane_off = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t obuf = tmem + lane_off + COL_O;
@@ -497,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_full(b));
+      arrive(p_full(b));
     }
     // ---------------------------------------------------------------- O, m, l to shared memory
     if (ok) ok = mbar_wait_long(o_final, 0, abort_flag);
@@ -532,18 +627,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
-  if (warp >= 12 && all_ok) {
+  if (warp >= SM_WARP && all_ok) {
     // this CTA's rows: the weights of their parts, a row a thread, then four columns a lane and two
     // (hd 64: four) rows a pass and warp
-    const int rb = TQ * rank / cs, re = min(TQ * (rank + 1) / cs, (t1 - t0) * G);
+    // (a pair's two row tiles are merged apart, each over the CTAs that hold it)
+    const int rb = TQ * part / cs, re = min(TQ * (part + 1) / cs, (t1 - t0) * G);
     float* wts = const_cast<float*>(sums) + 2 * TQ;  // [row][cs]
-    const int my = rb + (static_cast<int>(threadIdx.x) - 384);
+    const int my = rb + (static_cast<int>(threadIdx.x) - 32 * SM_WARP);
     if (my < re) {
       float mr = -INFINITY, lr = 0.f;
       float2 ml[MAX_CLUSTER];
 #pragma unroll
       for (int s = 0; s < MAX_CLUSTER; ++s) {
-        ml[s] = s < cs ? ldc64(map_cta(ml_s + my * 8, s)) : make_float2(-INFINITY, 0.f);
+        ml[s] = s < cs ? ldc64(map_cta(ml_s + my * 8, W * s + half)) : make_float2(-INFINITY, 0.f);
         mr = fmaxf(mr, ml[s].x);
       }
 #pragma unroll
@@ -560,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int U = 2;
     const int sub = lane / (HD / 4);
     const uint32_t piece = static_cast<uint32_t>(lane % (HD / 4));
-    for (int row0 = rb + ((warp - 12) * RPW + sub); row0 < re; row0 += U * 8 * RPW) {
+    for (int row0 = rb + ((warp - SM_WARP) * RPW + sub); row0 < re; row0 += U * 8 * RPW) {
       float4 acc[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -570,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int row = min(row0 + u * 8 * RPW, re - 1);
-          o[u] = ldc128(map_cta(base + row * L::ROW + ((piece ^ (row & (HD / 4 - 1))) << 4), s));
+          o[u] = ldc128(map_cta(base + row * L::ROW + ((piece ^ (row & (HD / 4 - 1))) << 4), W * s + half));
           w[u] = wts[row * cs + s];
         }
 #pragma unroll
@@ -590,22 +686,29 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // nobody leaves while others read its shared memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort_flag && P.status) atomicCAS(P.status, 0, PF_ERR_DEVICE_TIMEOUT);
 }
 
-template <int HD, int T>
-cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& L, cudaStream_t stream) {
+template <int HD, int T, int PAIR>
+cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream) {
+  using L = TSmem<HD, PAIR>;
   const pf_config& c = *a.c;
-  const int G = c.n_q_heads / c.n_kv_heads, BT = TQ / G;
-  CUtensorMap tq;
+  const int G = c.n_q_heads / c.n_kv_heads, BT = TQ / G, W = PAIR ? 2 : 1;
+  CUtensorMap tq, tk, tv;
   const uint64_t qd[3] = {static_cast<uint64_t>(HD), static_cast<uint64_t>(c.n_q_heads), static_cast<uint64_t>(a.M)};
   const uint64_t qs[2] = {static_cast<uint64_t>(HD) * 2, static_cast<uint64_t>(c.n_q_heads) * HD * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(BT)};
-  if (!encode_tmap_16(&tq, 0, 3, a.q, qd, qs, qb)) return cudaErrorInvalidValue;
+  const uint64_t rows = static_cast<uint64_t>(c.n_kv_heads) * l.slots;
+  if (!encode_tmap_16(&tq, 0, 3, a.q, qd, qs, qb) || !encode_tmap_8(&tk, l.k, HD, rows, HD, L::KR, 0) ||
+      !encode_tmap_8(&tv, l.v, HD, rows, L::VC, TK, 0))
+    return cudaErrorInvalidValue;
   TcParams p{};
-  p.c = L;
+  p.c = l;
   p.M = a.M;
   p.nq = c.n_q_heads;
   p.nkv = c.n_kv_heads;
@@ -614,34 +717,45 @@ cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& L, cudaStream_t stream)
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   p.out = static_cast<__half*>(a.out);
   p.status = a.status;
-  const int sets = (a.M + BT - 1) / BT;
+  const int sets = (a.M + W * BT - 1) / (W * BT);
   // as many CTAs on a set of rows as fill the GPU once
-  const int cs = std::max(1, std::min<int>(MAX_CLUSTER, device_sm_count() / (sets * c.n_kv_heads)));
-  p.cs = cs;
-  return launch_pdl_cluster(attn_kv8_tc_kernel<HD, T>, dim3(cs * sets, c.n_kv_heads), dim3(THREADS), TSmem<HD>::BYTES, stream, cs,
-                            tq, p);
+  const long long ctas = static_cast<long long>(W) * sets * c.n_kv_heads;
+  p.cs = static_cast<int>(std::max<long long>(1, std::min<long long>(MAX_CLUSTER / W, device_sm_count() / ctas)));
+  return launch_pdl_cluster(attn_kv8_tc_kernel<HD, T, PAIR>, dim3(W * p.cs * sets, c.n_kv_heads), dim3(THREADS), L::BYTES, stream,
+                            W * p.cs, tq, tk, tv, p);
 }
 
+// Pairs at hd 128 as soon as there are two row tiles.
 template <int HD, int T>
+cudaError_t launch_form(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream) {
+  const pf_config& c = *a.c;
+  if (HD == 128 && a.M > TQ / (c.n_q_heads / c.n_kv_heads)) return launch<128, T, 1>(a, l, stream);
+  return launch<HD, T, 0>(a, l, stream);
+}
+
+template <int HD, int T, int PAIR>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(attn_kv8_tc_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, TSmem<HD>::BYTES);
+  return cudaFuncSetAttribute(attn_kv8_tc_kernel<HD, T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, TSmem<HD, PAIR>::BYTES);
 }
 
 }  // namespace
 
 cudaError_t prepare_attention_kv8_tc_kernels() {
   cudaError_t e = cudaSuccess, r;
-  if ((r = set_attr<128, PF_KV_E4M3>()) != cudaSuccess) e = r;
-  if ((r = set_attr<128, PF_KV_INT8>()) != cudaSuccess) e = r;
-  if ((r = set_attr<64, PF_KV_E4M3>()) != cudaSuccess) e = r;
-  if ((r = set_attr<64, PF_KV_INT8>()) != cudaSuccess) e = r;
+  if ((r = set_attr<128, PF_KV_E4M3, 0>()) != cudaSuccess) e = r;
+  if ((r = set_attr<128, PF_KV_INT8, 0>()) != cudaSuccess) e = r;
+  if ((r = set_attr<128, PF_KV_E4M3, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr<128, PF_KV_INT8, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr<64, PF_KV_E4M3, 0>()) != cudaSuccess) e = r;
+  if ((r = set_attr<64, PF_KV_INT8, 0>()) != cudaSuccess) e = r;
   return e;
 }
 
-cudaError_t launch_attention_kv8_tc(const Kv8AttnArgs& a, const Kv8Layer& L, cudaStream_t stream) {
+cudaError_t launch_attention_kv8_tc(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream) {
   const pf_config& c = *a.c;
-  if (c.head_dim == 128) return c.kv_dtype == PF_KV_E4M3 ? launch<128, PF_KV_E4M3>(a, L, stream) : launch<128, PF_KV_INT8>(a, L, stream);
-  return c.kv_dtype == PF_KV_E4M3 ? launch<64, PF_KV_E4M3>(a, L, stream) : launch<64, PF_KV_INT8>(a, L, stream);
+  if (c.head_dim == 128)
+    return c.kv_dtype == PF_KV_E4M3 ? launch_form<128, PF_KV_E4M3>(a, l, stream) : launch_form<128, PF_KV_INT8>(a, l, stream);
+  return c.kv_dtype == PF_KV_E4M3 ? launch_form<64, PF_KV_E4M3>(a, l, stream) : launch_form<64, PF_KV_INT8>(a, l, stream);
 }
 
 }  // namespace pf

@@ -210,9 +210,10 @@ struct Kv8AttnArgs {
   const int* blocks;
   int* status;
 };
-// Tiled tensor map over bytes [rows][inner] (inner 128 or 64), boxes of box_rows whole rows, swizzled
-// by the row's width.
-bool encode_tmap_8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
+// Tiled tensor map over bytes [rows][inner], boxes of box_rows x box_inner, swizzled by `swizzle_bytes`
+// (128 or 64, the box's width, or 0).
+bool encode_tmap_8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
+                   int swizzle_bytes);
 cudaError_t prepare_attention_kv8_kernels();
 // the form for more rows than the few-row kernel takes (attention_kv8_tc.cu); no scratch
 cudaError_t prepare_attention_kv8_tc_kernels();
