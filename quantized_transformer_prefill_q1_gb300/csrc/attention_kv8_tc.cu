@@ -20,7 +20,8 @@
 //   0, 2     copies: Q and the K codes (0), the V codes (2), ST stages ahead;
 //   1        TMEM (three S buffers of 128 columns and O) and the MMAs, S_j = Q K_j^T and
 //            O += P_j V_j (P over S's columns), whichever is ready (in a pair, the even CTA's);
-//   4..7     K and V codes to f16, into shared memory in the MMA's 128-byte swizzle; the scales;
+//   3        the scales;
+//   4..7     K and V codes to f16, into shared memory in the MMA's 128-byte swizzle;
 //   8..11    softmax of the even key tiles, 12..15 of the odd ones, one thread per row, so that one
 //            tile's exponentials run while the next one's maximum is taken. The two share each row's
 //            running maximum: a tile's decision to raise it (only when exceeded by more than 2^8; O is
@@ -38,14 +39,16 @@ namespace {
 constexpr int TQ = 128;  // rows per CTA
 constexpr int TK = 128;  // keys per tile: one page, four scale blocks
 constexpr int NSB = 3;   // S / P buffers
+constexpr int LA = 1;    // tiles that the K codes run ahead of the V codes
 constexpr int THREADS = 512;
 constexpr int SM_WARP = 8;        // first softmax warp
 constexpr int SM_THREADS = 256;   // softmax threads: two groups of one per row
 constexpr int DQ_THREADS = 128;   // converting threads
 constexpr int NG = TK / PF_KV8_BLOCK;
-constexpr int SCR = 8;   // tiles in the ring of scales (K's conversion may run 5 tiles ahead of a softmax)
+constexpr int SCR = 8;   // tiles in the ring of scales
 constexpr int MAX_CLUSTER = 8;
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr int IDLE_NS = 20;
 constexpr uint32_t COL_O = NSB * TK;  // TMEM: S buffer b at b TK, O at COL_O
 
 template <int HD, int PAIR>
@@ -169,7 +172,7 @@ __device__ __forceinline__ float4 ldc128(uint32_t a) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
-// Registers a thread from here on (all warps of a warpgroup alike): 128 x (32 + 96 + 192 + 192) is the
+// Registers a thread from here on (all warps of a warpgroup alike): 128 x (48 + 80 + 192 + 192) is the
 // 512 x 128 that the CTA is launched with.
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -195,6 +198,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 template <int HD, int T, int PAIR>
@@ -225,10 +234,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto p_full = [&](int b) { return bar0 + 8u * (30 + b); };
   auto turn = [&](int quarter, int x) { return bar0 + 8u * (33 + 2 * quarter + x); };  // group x's decision on its tile
   auto sc_full = [&](int s) { return bar0 + 8u * (41 + s); };
+  auto sc_free = [&](int s) { return bar0 + 8u * (55 + s); };
   const uint32_t q_full = bar0 + 8u * 49, q_ready = bar0 + 8u * 50, o_final = bar0 + 8u * 51, drain_bar = bar0 + 8u * 52;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (bar0 + 8u * 53 - base));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bar0 + 8u * 54 - base));
-  static_assert(SCR == 8 && ST <= 3 && 8 * 55 <= L::BARS, "barrier area");
+  static_assert(SCR == 8 && ST <= 3 && 8 * 63 <= L::BARS, "barrier area");
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,7 +259,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 4; ++i)
       for (int x = 0; x < 2; ++x) mbar_init(turn(i, x), 1);
-    for (int s = 0; s < SCR; ++s) mbar_init(sc_full(s), NG);
+    for (int s = 0; s < SCR; ++s) {
+      mbar_init(sc_full(s), 1);
+      mbar_init(sc_free(s), 4);
+    }
     mbar_init(q_full, 1);
     mbar_init(q_ready, BOTH);
     mbar_init(o_final, 1);
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp < 4) {
-    regs_dec<32>();
+    regs_dec<48>();
     if ((warp == 0 || warp == 2) && lane == 0) {
       // -------------------------------------------------------------- copies
       const int v = warp >> 1;
@@ -339,6 +352,33 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = max(0, issued - ST); j < issued; ++j) wait_drain(c_full(v, j % ST), (j / ST) & 1);
     }
     __syncwarp();
+    if (warp == 3) {
+      // -------------------------------------------------------------- scales, a lane a block of 32 keys
+      auto load = [&](int j, float& sk, float& sv) {  // 1 for a block past the sequence
+        sk = sv = 1.f;
+        if (lane < NG && j < nt && lane * PF_KV8_BLOCK < valid_of(j)) {
+          const size_t at = static_cast<size_t>(kvh) * P.c.nblk + max(kv8_slot(P.c, (jb + j) * TK), 0) / PF_KV8_BLOCK + lane;
+          sk = P.c.ks[at];
+          sv = P.c.vs[at];
+        }
+      };
+      float sk, sv, nk, nv;
+      load(0, sk, sv);
+      load(1, nk, nv);
+      for (int j = 0; j < nt; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait_long(sc_free(j % SCR), ((j / SCR) & 1) ^ 1, abort_flag))) break;
+        if (lane < NG) {
+          const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);
+          // the factor of the scores stays > 0: a hidden key's -inf stays -inf
+          scales[(j % SCR) * NG + lane] = make_float4(fmaxf(sk * P.scale_log2, 1e-37f), __log2f(svc), 1.f / svc, 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_full(j % SCR));
+        sk = nk;
+        sv = nv;
+        load(j + 2, nk, nv);
+      }
+    }
   }
   if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -401,6 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           const uint64_t now = global_timer_ns();
           if (t_idle == 0) t_idle = now;
+          __nanosleep(IDLE_NS);  // a warp that polls takes issue slots from those it waits for
           const bool give_up = *abort_flag || now - t_idle > PF_WAIT_LIMIT_NS;
           if (__any_sync(0xffffffffu, give_up)) {
             *abort_flag = 1;
@@ -419,19 +460,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4 && warp < SM_WARP) {
     // ---------------------------------------------------------------- codes to f16
-    regs_dec<96>();
+    regs_dec<80>();
     const int tid = threadIdx.x - 128;
-    // the scales of tile j's block tid (threads 0 .. 3); 1 for a block past the sequence
-    float sk = 1.f, sv = 1.f;
-    auto load_scales = [&](int j) {
-      sk = sv = 1.f;
-      if (tid < NG && j < nt && tid * PF_KV8_BLOCK < valid_of(j)) {
-        const int slot = max(kv8_slot(P.c, (jb + j) * TK), 0);
-        const size_t at = static_cast<size_t>(kvh) * P.c.nblk + slot / PF_KV8_BLOCK + tid;
-        sk = P.c.ks[at];
-        sv = P.c.vs[at];
-      }
-    };
     // A tile of ROWS x C codes (K or V of tile j): 8 codes a thread and pass, one 16-byte piece of f16 in
     // regions of 64 columns (rows of 128 B, swizzled). Rows a pass are a multiple of 8: one swizzle.
     auto convert = [&](auto rows_c, auto cols_c, int v, int j, uint32_t ring, uint32_t tiles, int valid) -> bool {
@@ -452,13 +482,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(c_empty(v, st));
       if (!__all_sync(0xffffffffu, mbar_wait_long(empty(v, st), ((j / ST) & 1) ^ 1, abort_flag))) return false;
-      if (v == 0 && tid < NG) {
-        // (K_{j-3}'s product is done, so PV_{j-6} is: softmaxes of tiles j - 5 on may still read their scales)
-        const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);
-        // the factor of the scores stays > 0: a hidden key's -inf stays -inf
-        scales[(j % SCR) * NG + tid] = make_float4(fmaxf(sk * P.scale_log2, 1e-37f), __log2f(svc), 1.f / svc, 0.f);
-        mbar_arrive(sc_full(j % SCR));
-      }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         uint32_t h0, h1, h2, h3;
@@ -470,12 +493,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       arrive(full(v, st));
       return true;
     };
-    load_scales(0);
-    for (int j = 0; j < nt; ++j) {
-      const int valid = valid_of(j);
-      if (!convert(std::integral_constant<int, L::KR>{}, std::integral_constant<int, HD>{}, 0, j, kc_s, k_s, valid - half * L::KR)) break;
-      load_scales(j + 1);
-      if (!convert(std::integral_constant<int, TK>{}, std::integral_constant<int, L::VC>{}, 1, j, vc_s, v_s, valid)) break;
+    // K runs LA tiles ahead of V, as the scores do ahead of P V
+    for (int j = 0; j < nt + LA; ++j) {
+      if (j < nt && !convert(std::integral_constant<int, L::KR>{}, std::integral_constant<int, HD>{}, 0, j, kc_s, k_s, valid_of(j) - half * L::KR))
+        break;
+      if (j >= LA && !convert(std::integral_constant<int, TK>{}, std::integral_constant<int, L::VC>{}, 1, j - LA, vc_s, v_s, valid_of(j - LA)))
+        break;
     }
   } else if (warp >= SM_WARP) {
     // ---------------------------------------------------------------- softmax rows
@@ -565,34 +588,35 @@ __global__ void __launch_bounds__(THREADS, 1)
         m = m_new;
       }
       const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen no key: every weight 2^-inf = 0
-      // P over the first half of S's columns
+      // P over the first half of S's columns. Every step runs over 32 columns before the next one does:
+      // the exponentials of a few columns at a time would each wait for the step before.
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const float4 sc = factors(g);
         const float off = sc.y - mm;
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        float u[32];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          u[e] = __uint_as_float(v[32 * g + e]);
+          u[e + 1] = __uint_as_float(v[32 * g + e + 1]);
+          fma2(u[e], u[e + 1], sc.x, off);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) u[e] = ex2t(u[e]);
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float a = __uint_as_float(v[32 * g + e]), c = __uint_as_float(v[32 * g + e + 1]);
-          float d = __uint_as_float(v[32 * g + e + 2]), f = __uint_as_float(v[32 * g + e + 3]);
-          fma2(a, c, sc.x, off);
-          fma2(d, f, sc.x, off);
-          a = ex2t(a);
-          c = ex2t(c);
-          d = ex2t(d);
-          f = ex2t(f);
-          add2(s0, s1, a, c);
-          add2(s2, s3, d, f);
-          pk[e / 2] = f16x2t(a, c);
-          pk[e / 2 + 1] = f16x2t(d, f);
-        }
-        l = fmaf((s0 + s1) + (s2 + s3), sc.z, l);
+        for (int e = 0; e < 32; e += 2) pk[e / 2] = f16x2t(u[e], u[e + 1]);
         tmem_st_32x32b_x16(sbuf + 16 * g, pk);
+#pragma unroll
+        for (int w = 16; w > 1; w >>= 1)
+#pragma unroll
+          for (int e = 0; e < w; e += 2) add2(u[e], u[e + 1], u[e + w], u[e + w + 1]);
+        l = fmaf(u[0] + u[1], sc.z, l);
       }
       tmem_st_wait();
       tc_fence_before();
       arrive(p_full(b));
+      if (lane == 0) mbar_arrive(sc_free(j % SCR));
     }
     // ---------------------------------------------------------------- O, m, l to shared memory
     if (ok) ok = mbar_wait_long(o_final, 0, abort_flag);
@@ -602,6 +626,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float m_fin = run_m[r];
       sums[x * TQ + r] = m == -INFINITY ? 0.f : l * ex2t(m - m_fin);
       bar_and(1, SM_THREADS, true);
+      const int t = t0 + r / G;
+      const float inv = cs == 1 ? __fdividef(1.f, sums[r] + sums[TQ + r]) : 1.f;
+      __half* out = P.out + (static_cast<size_t>(t) * P.nq + kvh * G + r % G) * HD;
       // 16-byte piece q of a row at piece q ^ (row % (HD / 4)): a warp's rows hit different banks
       const uint32_t dst = base + r * L::ROW;
 #pragma unroll 1
@@ -614,9 +641,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+        if (cs == 1) {  // the whole row is here: straight to the output
+          if (t < t1) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          sts128(dst + (((8 * c + q) ^ (r & (HD / 4 - 1))) << 4), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = f16x2t(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            sts128(dst + (((8 * c + q) ^ (r & (HD / 4 - 1))) << 4), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
       }
       if (x == 0)
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml_s + r * 8), "f"(m_fin), "f"(sums[r] + sums[TQ + r]) : "memory");
@@ -626,59 +666,61 @@ __global__ void __launch_bounds__(THREADS, 1)
   // every CTA of the cluster has its rows in shared memory; each merges its share of them
   tc_fence_before();
   __syncwarp();
-  cluster_sync_all();
-  if (warp >= SM_WARP && all_ok) {
+  if (cs > 1) cluster_sync_all();
+  if (warp >= SM_WARP && all_ok && cs > 1) {
     // this CTA's rows: the weights of their parts, a row a thread, then four columns a lane and two
     // (hd 64: four) rows a pass and warp
     // (a pair's two row tiles are merged apart, each over the CTAs that hold it)
     const int rb = TQ * part / cs, re = min(TQ * (part + 1) / cs, (t1 - t0) * G);
     float* wts = const_cast<float*>(sums) + 2 * TQ;  // [row][cs]
     const int my = rb + (static_cast<int>(threadIdx.x) - 32 * SM_WARP);
+    // (a row's parts are all requested before the first is used, and the CTA's own is read as its own:
+    // loads from other CTAs move about 16 B a cycle)
+    constexpr int NP = MAX_CLUSTER / W;
     if (my < re) {
       float mr = -INFINITY, lr = 0.f;
-      float2 ml[MAX_CLUSTER];
+      float2 ml[NP];
 #pragma unroll
-      for (int s = 0; s < MAX_CLUSTER; ++s) {
-        ml[s] = s < cs ? ldc64(map_cta(ml_s + my * 8, W * s + half)) : make_float2(-INFINITY, 0.f);
-        mr = fmaxf(mr, ml[s].x);
-      }
+      for (int s = 0; s < NP; ++s) ml[s] = s < cs ? ldc64(map_cta(ml_s + my * 8, W * s + half)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int s = 0; s < MAX_CLUSTER; ++s) {
+      for (int s = 0; s < NP; ++s) mr = fmaxf(mr, ml[s].x);
+#pragma unroll
+      for (int s = 0; s < NP; ++s) {
         ml[s].x = ml[s].x == -INFINITY ? 0.f : ex2t(ml[s].x - mr);
         lr = fmaf(ml[s].x, ml[s].y, lr);
       }
 #pragma unroll
-      for (int s = 0; s < MAX_CLUSTER; ++s)
-        if (s < cs) wts[my * cs + s] = ml[s].x / lr;
+      for (int s = 0; s < NP; ++s)
+        if (s < cs) wts[my * cs + s] = __fdividef(ml[s].x, lr);
     }
     bar_and(1, SM_THREADS, true);
     constexpr int RPW = 128 / HD;  // rows a warp's 32 lanes cover
-    constexpr int U = 2;
+    constexpr int U = PAIR ? 2 : 1;
     const int sub = lane / (HD / 4);
     const uint32_t piece = static_cast<uint32_t>(lane % (HD / 4));
     for (int row0 = rb + ((warp - SM_WARP) * RPW + sub); row0 < re; row0 += U * 8 * RPW) {
-      float4 acc[U];
+      float4 o[U][NP];
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < cs; ++s) {
-        float4 o[U];
-        float w[U];
+      for (int u = 0; u < U; ++u) {
+        const int row = min(row0 + u * 8 * RPW, re - 1);
+        const uint32_t at = base + row * L::ROW + ((piece ^ (row & (HD / 4 - 1))) << 4);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int row = min(row0 + u * 8 * RPW, re - 1);
-          o[u] = ldc128(map_cta(base + row * L::ROW + ((piece ^ (row & (HD / 4 - 1))) << 4), W * s + half));
-          w[u] = wts[row * cs + s];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)  // a part without a key of the row has weight 0 and O 0
-          acc[u] = make_float4(fmaf(w[u], o[u].x, acc[u].x), fmaf(w[u], o[u].y, acc[u].y), fmaf(w[u], o[u].z, acc[u].z), fmaf(w[u], o[u].w, acc[u].w));
+        for (int s = 0; s < NP; ++s)
+          if (s < cs) o[u][s] = s == part ? lds128f(at) : ldc128(map_cta(at, W * s + half));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int row = row0 + u * 8 * RPW;
-        if (row < re)
-          *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(t0 + row / G) * P.nq + kvh * G + row % G) * HD + 4 * piece) =
-              make_uint2(f16x2t(acc[u].x, acc[u].y), f16x2t(acc[u].z, acc[u].w));
+        if (row >= re) break;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < NP; ++s)
+          if (s < cs) {  // a part without a key of the row has weight 0 and O 0
+            const float w = wts[row * cs + s];
+            acc = make_float4(fmaf(w, o[u][s].x, acc.x), fmaf(w, o[u][s].y, acc.y), fmaf(w, o[u][s].z, acc.z), fmaf(w, o[u][s].w, acc.w));
+          }
+        *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(t0 + row / G) * P.nq + kvh * G + row % G) * HD + 4 * piece) =
+            make_uint2(f16x2t(acc.x, acc.y), f16x2t(acc.z, acc.w));
       }
     }
   }
@@ -693,6 +735,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (threadIdx.x == 0 && *abort_flag && P.status) atomicCAS(P.status, 0, PF_ERR_DEVICE_TIMEOUT);
 }
+
+// Clusters of `size` CTAs that the GPU runs at once (they must each lie in one GPC, so large ones leave
+// SMs unused); filled by prepare_attention_kv8_tc_kernels.
+int g_active[2][MAX_CLUSTER + 1];  // [pair][size]
 
 template <int HD, int T, int PAIR>
 cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream) {
@@ -718,9 +764,12 @@ cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream)
   p.out = static_cast<__half*>(a.out);
   p.status = a.status;
   const int sets = (a.M + W * BT - 1) / (W * BT);
-  // as many CTAs on a set of rows as fill the GPU once
-  const long long ctas = static_cast<long long>(W) * sets * c.n_kv_heads;
-  p.cs = static_cast<int>(std::max<long long>(1, std::min<long long>(MAX_CLUSTER / W, device_sm_count() / ctas)));
+  // As many CTAs on a set of rows as run at once: a second wave would cost more than the parts save
+  // (128 tokens of 32/8 heads over 8,192 keys: 56 us in 16 clusters of 8, of which 15 run at once, 42 in clusters of 6).
+  const long long groups = static_cast<long long>(sets) * c.n_kv_heads;
+  p.cs = 1;
+  for (int cs = 2; cs <= MAX_CLUSTER / W; ++cs)
+    if (groups <= g_active[PAIR][W * cs]) p.cs = cs;
   return launch_pdl_cluster(attn_kv8_tc_kernel<HD, T, PAIR>, dim3(W * p.cs * sets, c.n_kv_heads), dim3(THREADS), L::BYTES, stream,
                             W * p.cs, tq, tk, tv, p);
 }
@@ -735,7 +784,23 @@ cudaError_t launch_form(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t st
 
 template <int HD, int T, int PAIR>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(attn_kv8_tc_kernel<HD, T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, TSmem<HD, PAIR>::BYTES);
+  using L = TSmem<HD, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(attn_kv8_tc_kernel<HD, T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  for (int size = 2; size <= MAX_CLUSTER && e == cudaSuccess; ++size) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;  // one CTA an SM whatever the instance: HD and T make no difference
+    if (cudaOccupancyMaxActiveClusters(&n, attn_kv8_tc_kernel<HD, T, PAIR>, &cfg) == cudaSuccess) g_active[PAIR][size] = n;
+  }
+  return e;
 }
 
 }  // namespace
