@@ -65,7 +65,9 @@ typedef enum {
 
 typedef enum { PF_W_Q1_G128 = 0, PF_W_INT4_AFFINE_G128 = 1 } pf_wformat;
 /* PF_KV_E4M3 / PF_KV_INT8: one byte per element and an f32 scale for each PF_KV8_BLOCK slots of
- * a (layer, kv head), see "8-bit cache" below. Linear and paged caches (no ring); q is f16. */
+ * a (layer, kv head), see "8-bit cache" below. Linear and paged caches (no ring); q is f16. A
+ * session rounds a chunk's K and V to f16, stores them in 8 bits and attends to what the cache then
+ * holds, the chunk's own positions included; a K or V beyond f16 is recorded as PF_ERR_NONFINITE. */
 typedef enum { PF_KV_F32 = 0, PF_KV_BF16 = 1, PF_KV_F16 = 2, PF_KV_E4M3 = 3, PF_KV_INT8 = 4 } pf_kvdtype;
 
 /* Model configuration ([P1] LayerConfig + the tail's final_norm_eps / vocab). */
@@ -476,7 +478,10 @@ pf_status pf_op_logprobs(const float* logits_dev, int32_t rows, int32_t n, int64
  *
  * pf_op_attention_kv8: causal GQA attention as pf_op_attention: q f16 [M][nq][hd] at positions
  * start_pos .., keys 0 .. position of `layer`, out f16 [M][nq hd]; scores and softmax statistics
- * in f32. Codes and scales of other positions are not used, whatever they hold. scratch_dev:
+ * in f32, the weights rounded to f16 for their product with the values. Positions from
+ * start_pos + M on are not used, whatever their codes and scales hold; scales of earlier blocks are
+ * positive and finite, and a NaN code (0x7f / 0xff of e4m3, which the store never writes) at a position
+ * below start_pos + M may make any row's output NaN. scratch_dev:
  * device, 16-B aligned, at least pf_attention_kv8_scratch_bytes(cfg, M) bytes (which does not fall
  * as M grows); its first 4 KiB must be zero before the first call, and each call that completes
  * leaves them zero (after PF_ERR_DEVICE_TIMEOUT zero them again). Calls sharing one scratch must

@@ -280,29 +280,87 @@ def test_attention_zero_values_and_queries(kind, m):
     check_attention(c, q, attend(c, q, start, m), start, m)
 
 
-@pytest.mark.parametrize("m", [1, 3, 40])
-def test_attention_long_cache(m):
-    """Enough keys for every split, one layer of two behind an offset; against a float64 product on the GPU."""
-    nq, nkv, hd, start = 32, 8, 128, 20011
-    L = start + m
-    c = Cache("e4m3", nkv, hd, L + 5, True, nq, seed=3)
-    g = torch.Generator(device="cuda").manual_seed(4)
+def random_cache(kind, nq, nkv, hd, L, paged, seed):
+    """A filled cache pair without the numpy mirror, and its values [L, nkv, hd] read back in float64."""
+    c = Cache.__new__(Cache)
+    rng = np.random.default_rng(seed)
+    pages = -(-(L + 5) // pf.KV_BLOCK)
+    c.pool = pages + 1 if paged else 0
+    c.kind, c.layer, c.nkv, c.hd, c.rng = kind, 1, nkv, hd, rng
+    c.table_dev = torch.from_numpy(rng.permutation(c.pool)[:pages].astype(np.int32)).cuda() if paged else None
+    c.cfg = config(kind, nq, nkv, hd, L + 5, c.pool)
+    c.status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c.dev, val = {}, {}
+    for w in "kv":
+        c.dev[w] = pf.kv8_cache(c.cfg)
+        c.dev[w].copy_(torch.randint(256, c.dev[w].shape, device="cuda", generator=g, dtype=torch.uint8))
     k, v = (torch.randn(L, nkv, hd, device="cuda", generator=g).half() for _ in range(2))
     for s in range(0, L, 8192):
         n = min(8192, L - s)
-        pf.pf_op_kv8_store(c.cfg, k[s:s + n], v[s:s + n], c.layer, s, n, c.dev["k"], c.dev["v"], c.table_dev, c.status)
-    val = {}
+        pf.pf_op_kv8_store(c.cfg, k[s:s + n], v[s:s + n], 1, s, n, c.dev["k"], c.dev["v"], c.table_dev, c.status)
     for w in "kv":
         t = torch.empty(L, nkv, hd, device="cuda")
-        pf.pf_op_kv8_load(c.cfg, c.dev[w], c.layer, 0, L, t, c.table_dev)
+        pf.pf_op_kv8_load(c.cfg, c.dev[w], 1, 0, L, t, c.table_dev)
         val[w] = t.double()
-    q = queries(c, m, nq, 1.0)
-    out = attend(c, q, start, m)[:m].double().view(m, nq, hd)
+    return c, val
+
+
+def check_norms(c, val, q, out, start, m):
+    """Per head within the norm bound of check_attention, against a float64 product on the GPU."""
+    nq, L = q.shape[1], start + m
+    G = nq // c.nkv
+    out = out[:m].double().view(m, nq, c.hd)
     see = torch.arange(L, device="cuda")[None, :] <= start + torch.arange(m, device="cuda")[:, None]
     for h in range(nq):
-        s = (q[:, h].double() @ val["k"][:, h // 4].T / hd ** 0.5).masked_fill(~see, -float("inf"))
-        want = torch.softmax(s, 1) @ val["v"][:, h // 4]
-        assert float((out[:, h] - want).norm() / want.norm()) <= 5e-4, h  # as in check_attention
+        s = (q[:, h].double() @ val["k"][:L, h // G].T / c.hd ** 0.5).masked_fill(~see, -float("inf"))
+        want = torch.softmax(s, 1) @ val["v"][:L, h // G]
+        assert float((out[:, h] - want).norm() / want.norm()) <= 5e-4, h
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("m,start", [(1, 20011), (3, 20011), (40, 20011), (520, 1000), (512, 4095), (1, 60000)])
+def test_attention_long_cache(kind, m, start):
+    """Every form at full size: all splits of the few-row kernel, clusters with and without parts of the keys."""
+    nq, nkv, hd = 32, 8, 128
+    c, val = random_cache(kind, nq, nkv, hd, start + m, m % 2 == 1, 3)
+    q = queries(c, m, nq, 1.0)
+    check_norms(c, val, q, attend(c, q, start, m), start, m)
+    pf.pf_status_read(c.status)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_drawn(seed):
+    """Sizes over the whole range."""
+    rng = np.random.default_rng(100 + seed)
+    nq, nkv, hd = [(32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (32, 4, 128), (2, 2, 64), (8, 8, 128), (64, 2, 64)][seed % 8]
+    m = int(np.exp(rng.uniform(0, np.log(400))))
+    start = int(np.exp(rng.uniform(0, np.log(9000)))) - 1
+    c, val = random_cache("e4m3" if rng.random() < 0.5 else "int8", nq, nkv, hd, start + m, rng.random() < 0.5, seed)
+    q = queries(c, m, nq, 1.5)
+    out = attend(c, q, start, m)
+    check_norms(c, val, q, out, start, m)
+    assert bool((out[m:] == 3).all())
+    pf.pf_status_read(c.status)
+
+
+@pytest.mark.parametrize("ms", [(1, 1), (1, 300), (64, 64)])
+def test_attention_on_two_streams_at_once(ms):
+    """Calls that overlap, each with its own scratch, do not touch each other."""
+    c, val = random_cache("e4m3", 8, 2, 128, 6000, True, 7)
+    calls = []
+    for i, m in enumerate(ms):
+        q = queries(c, m, 8, 1.0)
+        calls.append((q, 6000 - m, m, pf.attention_kv8_scratch(c.cfg, m), torch.zeros(m, 1024, dtype=torch.float16, device="cuda"),
+                      torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, start, m, scratch, out, st in calls:
+            with torch.cuda.stream(st):
+                attend(c, q, start, m, scratch, out)
+    torch.cuda.synchronize()
+    for q, start, m, scratch, out, _ in calls:
+        check_norms(c, val, q, out, start, m)
 
 
 def test_attention_repeats_and_shares_scratch():
