@@ -19,9 +19,10 @@
 // it has, so ties and constant rows end in as few sorts as any other. What the warps kept is ranked by
 // counting.
 //
-// Bound: HBM (4 bytes a logit) for many rows: 512 x 151,936 with 20 alternatives 58.4 us = 5.3 TB/s, 0.80
-// of the measured copy rate (54.1 without alternatives; 512 threads a CTA 63.7 and 57.2). Latency for
-// few: one row 10.7 us (6.7).
+// Bound: HBM (4 bytes a logit) for many rows: 512 x 151,936 with 20 alternatives 60.0 us = 5.2 TB/s, 0.78
+// of the measured copy rate (55.3 with the ones summed like the others, which loses an entropy near 0
+// by 1e-6 of itself and more; 72 with __expf in place of the bare instruction, 79 with expf). Latency for
+// few: one row 11.1 us.
 #include "ptx.cuh"
 
 namespace pf {
@@ -89,25 +90,37 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int count, Key* sorte
   __syncthreads();
 }
 
+constexpr float LOG2E = 1.4426950408889634f;
+// 2^x (relative error 2^-22; subnormal results flush to zero, which next to a weight of 1 is nothing).
+// With the product x log2(e) before it, a weight e^d is off by about (2^-22 + |d| 2^-24) of itself.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// m the maximum, n how many values equal it, s and t the sums over the others: S = n + s. Apart from
+// the ones, since a row of one likely token has S = 1 + (little), and ln S and the entropy are that little.
 struct Sums {
-  float m, s, t;
+  float m, n, s, t;
 };
-// Brings (m, s, t) to the maximum m_new >= m.
+// Brings a to the maximum m_new >= m.
 __device__ __forceinline__ void raise(Sums& a, float m_new) {
-  if (a.m == -INFINITY) {  // nothing summed yet
-    a.m = m_new;
-    return;
-  }
-  const float d = a.m - m_new, w = __expf(d);
-  a.t = a.s > 0.f && d > -1e30f ? w * fmaf(d, a.s, a.t) : w * a.t;
-  a.s *= w;
+  if (a.m == m_new) return;
+  const float d = a.m - m_new, w = expf(d), all = a.n + a.s;
+  a.t = all > 0.f && d > -1e30f ? w * fmaf(d, all, a.t) : w * a.t;  // (0 before the first number: d = -inf)
+  a.s = w * all;
+  a.n = 0.f;
   a.m = m_new;
 }
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
   const float m = fmaxf(a.m, b.m);
   raise(a, m);
   raise(b, m);
-  return {m, a.s + b.s, a.t + b.t};
+  return {m, a.n + b.n, a.s + b.s, a.t + b.t};
+}
+__device__ __forceinline__ Sums shfl_xor(Sums a, int o) {
+  return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.n, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+          __shfl_xor_sync(0xffffffffu, a.t, o)};
 }
 
 __device__ __forceinline__ uint32_t map_cta(uint32_t a, uint32_t rank) {
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 4)
   __shared__ int chosen[THREADS];     // first quads to read again: one batch (from the front), all of a thread's (from the back)
   __shared__ int n_batch, n_all, n_kept;
   __shared__ Sums part[WARPS];
-  __shared__ Sums mine;
+  __shared__ __align__(16) Sums mine;
   griddep_launch_dependents();
   griddep_wait();
   const int row = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
@@ -160,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 4)
     for (int u = 0; u < Q; ++u)
       f[u] = q + u * THREADS < q1 ? load(q + u * THREADS) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   };
-  Sums a{-INFINITY, 0.f, 0.f};
+  Sums a{-INFINITY, 0.f, 0.f, 0.f};
   float other = -INFINITY;  // largest value outside the batch at best_q, which holds the maximum
   int best_q = q0 + threadIdx.x;
   float4 next[Q];
@@ -185,19 +198,22 @@ __global__ void __launch_bounds__(THREADS, 4)
     }
     const float mm = a.m == -INFINITY ? 0.f : a.m;
     float s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
+    float all[2] = {0.f, 0.f};  // the ones too: their number is what s lacks (cheaper than counting them)
 #pragma unroll
     for (int e = 0; e < 4 * Q; ++e) {
-      const float d = v[e] - mm, w = __expf(d);
-      s[e & 1] += w;
+      const float d = v[e] - mm, w = ex2(d * LOG2E);
+      s[e & 1] += d == 0.f ? 0.f : w;
+      all[e & 1] += w;
       t[e & 1] = fmaf(fmaxf(d, -1e30f), w, t[e & 1]);  // -inf has weight 0, and 0 * -inf would be NaN
     }
+    a.n += rintf((all[0] + all[1]) - (s[0] + s[1]));
     a.s += s[0] + s[1];
     a.t += t[0] + t[1];
   }
   const float best = a.m;  // the thread's maximum (-inf without a number)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.t, o)});
+    a = join(a, shfl_xor(a, o));
   if (lane == 0) part[warp] = a;
   if (top > 0) {
     maxima[threadIdx.x] = best;
@@ -294,10 +310,10 @@ __global__ void __launch_bounds__(THREADS, 4)
     rank_keys(lists, n_kept, sorted);
   }
   if (warp == 0) {
-    a = lane < WARPS ? part[lane] : Sums{-INFINITY, 0.f, 0.f};
+    a = lane < WARPS ? part[lane] : Sums{-INFINITY, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.t, o)});
+      a = join(a, shfl_xor(a, o));
     if (lane == 0) mine = a;
     __syncwarp();
   }
@@ -307,9 +323,7 @@ __global__ void __launch_bounds__(THREADS, 4)
       if (threadIdx.x < cs) {
         const uint32_t at = map_cta(smem_u32(&mine), threadIdx.x);
         Sums b;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + 4) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.t) : "r"(at + 8) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b.m), "=f"(b.n), "=f"(b.s), "=f"(b.t) : "r"(at) : "memory");
         part[threadIdx.x] = b;
       }
       if (threadIdx.x < cs * top) {
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 4)
     }
     if (warp == 0) {
       const Key list = top > 0 ? sorted[lane] : 0ull;
-      const float ls = logf(a.s);
+      const float ls = logf(a.n) + log1pf(a.s / a.n);  // ln S
       if (lane == 0) {
         if (lp) {
           const int t = tokens[row];
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 4)
             lp[row] = x[t] - a.m - ls;
           }
         }
-        if (ent) ent[row] = ls - a.t / a.s;
+        if (ent) ent[row] = ls - a.t / (a.n + a.s);
       }
       if (lane < top) {
         const size_t at = static_cast<size_t>(row) * top + lane;

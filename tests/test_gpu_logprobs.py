@@ -33,7 +33,10 @@ def reference(x, n, tokens, top):
     with np.errstate(all="ignore"):
         m = x.max(1, keepdims=True)
         e = np.exp(x - m)
-        d = x - m - np.log(e.sum(1, keepdims=True))  # the maximum first: logits near 1e30 keep the rest
+        # the maximum first (logits near 1e30 keep the rest), and the ones of the sum apart: in float64 too
+        # log(1 + 1e-15) has no digits
+        top_n = (x == m).sum(1, keepdims=True)
+        d = x - m - np.log(top_n) - np.log1p(np.where((x == m) & (e == 1), 0.0, e).sum(1, keepdims=True) / top_n)
         p = e / e.sum(1, keepdims=True)
         ent = -np.where(p > 0, p * d, np.where(np.isnan(p), np.nan, 0.0)).sum(1)
         lp = d[np.arange(rows), tokens]
@@ -132,6 +135,22 @@ def test_large_spread_and_offset():
         beyond = np.isinf(rtlp.astype(np.float32))  # a gap of 6e38 is not an f32: it rounds to -inf
         assert beyond[3, 1:].all() and np.array_equal(tlp[beyond], rtlp.astype(np.float32)[beyond])
         assert np.all(np.abs(tlp - rtlp)[~beyond] <= (2.0 ** -22 * np.abs(rtlp) + 2e-5)[~beyond])
+
+
+@pytest.mark.parametrize("gap", [4.0, 9.0, 16.0, 40.0])
+def test_one_likely_token(gap):
+    """A row of one likely token: ln S and the entropy are tiny and still right in their own size. The weights
+    of the others are off by at most 2^-22 + gap' 2^-23 of themselves (gap' their distance, at most 60 here)
+    and by as much again in their sum, the logarithm and the quotient by a few 2^-24."""
+    x = logits(6, 30011, 12, 1.0)
+    x[:, 777] = x.amax(1) + gap
+    x[3, 778] = x[3, 777]  # two alike
+    tok = torch.full((6,), 777, dtype=torch.int32, device="cuda")
+    lp, ent, _, _ = call(x, 30011, tok, 3)
+    rlp, rent, _, _ = reference(x, 30011, np.full(6, 777), 3)
+    rel = 2 * (2.0 ** -22 + 60 * 2.0 ** -23)
+    assert np.all(np.abs(lp - rlp) <= rel * np.abs(rlp) + 1e-37), (lp, rlp)
+    assert np.all(np.abs(ent - rent) <= rel * np.abs(rent) + 1e-37), (ent, rent)
 
 
 def test_tokens_outside_the_vocabulary():
