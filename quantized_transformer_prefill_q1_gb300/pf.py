@@ -289,17 +289,21 @@ def pf_op_argmax(x, rows, n, ld, out, stream=None):
 
 # Operators over the 8-bit cache and the logits: the tensors' device, type and layout are checked
 # here (PF_ERR_INVALID_ARG), everything else by the library. These are small calls: the checks read
-# a tensor's fields only (about 0.5 us a tensor).
+# a tensor's fields only (about 0.3 us a tensor).
 _torch = None
 
 
-def _device() -> int:
-    """Index of the current CUDA device (imports torch on first use); no tensor's without a GPU."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch.cuda.current_device() if _torch.cuda.is_initialized() or _torch.cuda.is_available() else -2
+def _here():
+    """Index of the current CUDA device (no tensor's without a GPU), as a function fixed on first use."""
+    global _torch, _here
+    import torch
+    _torch = torch
+    if torch.cuda.is_available():
+        torch.cuda.current_device()  # initialises CUDA
+        _here = torch._C._cuda_getDevice
+    else:
+        _here = lambda: -2  # noqa: E731
+    return _here()
 
 
 def _dense(t, dev: int, dtype: str, what: str, numel: int, optional: bool = False) -> Optional[int]:
@@ -308,24 +312,24 @@ def _dense(t, dev: int, dtype: str, what: str, numel: int, optional: bool = Fals
         if optional:
             return None
         raise PfError(1, f"{what} is None")
+    if t.get_device() == dev and t.dtype is getattr(_torch, dtype) and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != dev:
         raise PfError(1, f"{what} is on {t.device}, not on the current CUDA device")
-    if t.dtype is not getattr(_torch, dtype) or not t.is_contiguous() or t.numel() < numel:
-        raise PfError(1, f"{what}: need at least {numel} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
+    raise PfError(1, f"{what}: need at least {numel} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
+
+
+def _on(dev: int, stream) -> Optional[int]:
+    """The stream, or the current one of CUDA device `dev`."""
+    return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _is_kv8(cfg) -> bool:
     return cfg.kv_dtype in (KV_E4M3, KV_INT8)
 
 
-def _kv8_args(cfg, dev: int, caches, blocks, status):
-    """(cfg by reference, cache addresses, block table, status) of an 8-bit cache's call."""
-    ref = ctypes.byref(cfg)
-    n = lib().pf_kv_bytes(ref)
-    return (ref, [_dense(t, dev, "uint8", "cache", n) for t in caches],
-            _dense(blocks, dev, "int32", "block table", -(-cfg.max_seq // KV_BLOCK), True),
-            _dense(status, dev, "int32", "status", 1, True))
+def _table(cfg, dev: int, blocks) -> Optional[int]:
+    return None if blocks is None else _dense(blocks, dev, "int32", "block table", -(-cfg.max_seq // KV_BLOCK))
 
 
 def kv8_cache(cfg, device="cuda"):
@@ -353,24 +357,24 @@ def kv8_views(cfg, cache):
 
 def pf_op_kv8_store(cfg, k, v, layer, start, m, k_cache, v_cache, blocks=None, status=None, stream=None):
     """k, v: f16 [m, nkv, hd], any token and head strides (multiples of 8, the same for both)."""
-    dev = _device()
-    strides = k.stride()
-    for t in (k, v):
-        if (t.get_device() != dev or t.dtype is not _torch.float16 or t.shape != (m, cfg.n_kv_heads, cfg.head_dim)
-                or t.stride() != strides or strides[2] != 1):
-            raise PfError(1, f"K / V rows: need f16 {(m, cfg.n_kv_heads, cfg.head_dim)} of equal strides with contiguous "
-                             f"elements on the current CUDA device, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}")
-    ref, (kc, vc), table, st = _kv8_args(cfg, dev, (k_cache, v_cache), blocks, status)
-    check(lib().pf_op_kv8_store(ref, k.data_ptr(), v.data_ptr(), strides[0], strides[1], layer, start, m, table, kc, vc, st,
-                                _stream(stream)))
+    dev, l, ref = _here(), lib(), ctypes.byref(cfg)
+    st = k.stride()
+    if (k.get_device() != dev or v.get_device() != dev or k.dtype is not _torch.float16 or v.dtype is not _torch.float16
+            or k.shape != (m, cfg.n_kv_heads, cfg.head_dim) or v.shape != k.shape or v.stride() != st or st[2] != 1):
+        raise PfError(1, f"K / V rows: need f16 {(m, cfg.n_kv_heads, cfg.head_dim)} of equal strides with contiguous elements "
+                         f"on the current CUDA device, got {[(tuple(t.shape), t.dtype, t.stride(), str(t.device)) for t in (k, v)]}")
+    n = l.pf_kv_bytes(ref)
+    check(l.pf_op_kv8_store(ref, k.data_ptr(), v.data_ptr(), st[0], st[1], layer, start, m, _table(cfg, dev, blocks),
+                            _dense(k_cache, dev, "uint8", "K cache", n), _dense(v_cache, dev, "uint8", "V cache", n),
+                            _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
 def pf_op_kv8_load(cfg, cache, layer, start, m, out, blocks=None, status=None, stream=None):
     """out: f32 [m, nkv, hd], the values that one cache (K or V) holds at positions start .. start + m - 1."""
-    dev = _device()
-    ref, (c,), table, st = _kv8_args(cfg, dev, (cache,), blocks, status)
-    check(lib().pf_op_kv8_load(ref, c, layer, start, m, table,
-                               _dense(out, dev, "float32", "out", m * cfg.n_kv_heads * cfg.head_dim), st, _stream(stream)))
+    dev, l, ref = _here(), lib(), ctypes.byref(cfg)
+    check(l.pf_op_kv8_load(ref, _dense(cache, dev, "uint8", "cache", l.pf_kv_bytes(ref)), layer, start, m, _table(cfg, dev, blocks),
+                           _dense(out, dev, "float32", "out", m * cfg.n_kv_heads * cfg.head_dim),
+                           _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
 def pf_attention_kv8_scratch_bytes(cfg, m):
@@ -387,25 +391,26 @@ def attention_kv8_scratch(cfg, m, device="cuda"):
 def pf_op_attention_kv8(cfg, q, k_cache, v_cache, layer, start, m, out, scratch, blocks=None, status=None,
                         stream=None):
     """Causal attention of q f16 [m, nq, hd] over the 8-bit caches, into out f16 [m, nq * hd]."""
-    dev, n = _device(), m * cfg.n_q_heads * cfg.head_dim
-    ref, (kc, vc), table, st = _kv8_args(cfg, dev, (k_cache, v_cache), blocks, status)
-    check(lib().pf_op_attention_kv8(ref, _dense(q, dev, "float16", "q", n), kc, vc, layer, start, m, table,
-                                    _dense(out, dev, "float16", "out", n), _dense(scratch, dev, "uint8", "scratch", 0),
-                                    scratch.numel(), st, _stream(stream)))
+    dev, l, ref = _here(), lib(), ctypes.byref(cfg)
+    n, nc = m * cfg.n_q_heads * cfg.head_dim, l.pf_kv_bytes(ref)
+    check(l.pf_op_attention_kv8(ref, _dense(q, dev, "float16", "q", n), _dense(k_cache, dev, "uint8", "K cache", nc),
+                                _dense(v_cache, dev, "uint8", "V cache", nc), layer, start, m, _table(cfg, dev, blocks),
+                                _dense(out, dev, "float16", "out", n), _dense(scratch, dev, "uint8", "scratch", 0),
+                                scratch.numel(), _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
 def pf_op_logprobs(logits, rows, n, ld, tokens, logprobs, entropy=None, top=0, top_ids=None, top_logprobs=None,
                    status=None, stream=None):
     """Log probability of tokens[r], entropy and the top alternatives of each row of logits [rows, ld]
     (each output may be None)."""
-    dev = _device()
+    dev = _here()
     check(lib().pf_op_logprobs(_dense(logits, dev, "float32", "logits", (rows - 1) * ld + n), rows, n, ld,
                                _dense(tokens, dev, "int32", "tokens", rows, True),
                                _dense(logprobs, dev, "float32", "logprobs", rows, True),
                                _dense(entropy, dev, "float32", "entropy", rows, True), top,
                                _dense(top_ids, dev, "int32", "top_ids", rows * top, True),
                                _dense(top_logprobs, dev, "float32", "top_logprobs", rows * top, True),
-                               _dense(status, dev, "int32", "status", 1, True), _stream(stream)))
+                               _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
 def pf_op_embed(e, tokens, m, h, vocab, x, status=None, stream=None):
@@ -583,7 +588,7 @@ class Session:
     def prefill_score(self, tokens_dev, targets_dev, start: int, logits_all, logprobs, entropy=None, top: int = 0,
                       top_ids=None, top_logprobs=None, stream=None) -> None:
         """Prefill of tokens_dev, logits [M, vocab] at every position, then pf_op_logprobs of targets_dev [M]."""
-        m, dev = tokens_dev.shape[0], _device()
+        m, dev = tokens_dev.shape[0], _here()
         check(lib().pf_prefill_score(self.h, _dense(tokens_dev, dev, "int32", "tokens", m),
                                      _dense(targets_dev, dev, "int32", "targets", m), m, start,
                                      _dense(logits_all, dev, "float32", "logits", m * self.dm.cfg.vocab),
@@ -591,7 +596,7 @@ class Session:
                                      _dense(entropy, dev, "float32", "entropy", m, True), top,
                                      _dense(top_ids, dev, "int32", "top_ids", m * top, True),
                                      _dense(top_logprobs, dev, "float32", "top_logprobs", m * top, True),
-                                     _stream(stream)))
+                                     _on(dev, stream)))
 
     def set_profile(self, on: bool) -> None:
         check(lib().pf_session_set_profile(self.h, int(on)))
