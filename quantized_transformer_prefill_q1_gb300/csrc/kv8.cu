@@ -29,9 +29,36 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// Eight f16 values times inv (a power of two from 2^-15 to 2^15) to codes. The product is exact in f16
+// unless it is below 2^-14, where both types' codes are 0 (their smallest nonzero values' halves are
+// 2^-10 and 1/2) whatever it was rounded to, so the code has one rounding.
+template <int T>
+__device__ __forceinline__ uint2 encode8(uint4 raw, __half2 inv) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t n[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&w[2 * j]), inv), b = __hmul2(*reinterpret_cast<const __half2*>(&w[2 * j + 1]), inv);
+    if (T == PF_KV_E4M3) {
+      asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\tmov.b32 %0, {x, y};\n\t}"
+          : "=r"(n[j])
+          : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+    } else {
+      // 1536 + x, |x| <= 127, has steps of 1 in f16: the sum rounds x to an integer, ties to even, and its
+      // low byte is that integer's
+      const __half2 m = __floats2half2_rn(1536.f, 1536.f);
+      const __half2 c = __hadd2(a, m), d = __hadd2(b, m);
+      n[j] = __byte_perm(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d), 0x6420);
+    }
+  }
+  return make_uint2(n[0], n[1]);
+}
+
 // One CTA = one block of 32 positions of one kv head, K (blockIdx.z 0) or V (1). Eight values a
 // thread and pass, the block's new rows held in registers between the maximum and the rounding, so
-// each row is read once. Bound: latency at one token (one CTA per head), HBM at long chunks.
+// each row is read once; both in packed f16 arithmetic (in f32, one value at a time, the ALU was 68 %
+// busy and 8,192 tokens of 8 heads of 128 took 15.5 us). Bound: latency at one token (one CTA per
+// head), HBM at long chunks.
 template <int HD, int T>
 __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx, const __half* vx, long long tok_stride,
                                                                long long head_stride, const int* start_dev,
@@ -67,17 +94,27 @@ __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx,
     if (r >= lo && base + r < end)
       raw[i] = *reinterpret_cast<const uint4*>(x + (base + r - start) * tok_stride + kvh * head_stride + col);
   }
-  float amax = 0.f;
-  bool odd = false;  // a NaN or an infinity
+  __half2 top = __floats2half2_rn(0.f, 0.f);  // NaN if there is one
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      const float a = fabsf(f.x), b = fabsf(f.y);
-      if (a <= 65504.f) amax = fmaxf(amax, a); else odd = true;
-      if (b <= 65504.f) amax = fmaxf(amax, b); else odd = true;
+    for (int j = 0; j < 4; ++j) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2*>(&w[j])));
+  }
+  const float2 tops = __half22float2(top);
+  const bool odd = !(tops.x <= 65504.f && tops.y <= 65504.f);  // a NaN or an infinity
+  float amax = fmaxf(tops.x, tops.y);
+  if (odd) {  // the finite values' maximum, one by one
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        if (fabsf(f.x) <= 65504.f) amax = fmaxf(amax, fabsf(f.x));
+        if (fabsf(f.y) <= 65504.f) amax = fmaxf(amax, fabsf(f.y));
+      }
     }
   }
 #pragma unroll
@@ -89,6 +126,8 @@ __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx,
   const float s_new = pow2i(scale_exponent<T>(amax));
   const float s = fmaxf(s_old, s_new);
   const float inv = 1.f / s;  // exact: s is a power of two
+  const bool packed = !bad && inv <= 0x1p15f && inv >= 0x1p-15f;
+  const __half2 inv2 = __floats2half2_rn(inv, inv);
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = row0 + i * RPP;
@@ -107,6 +146,8 @@ __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx,
         }
         *dst = make_uint2(o[0], o[1]);
       }
+    } else if (base + r < end && packed) {
+      *dst = encode8<T>(raw[i], inv2);
     } else if (base + r < end) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       uint32_t n[2] = {0, 0};
@@ -126,29 +167,43 @@ __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx,
   }
 }
 
-// Read-back: out[t][kvh][i] = code * scale of position start + t, four codes a thread. HBM bound.
-template <int T>
-__global__ void __launch_bounds__(256) kv8_load_kernel(const uint8_t* codes, const float* scales,
-                                                       Kv8Layer c, int hd, int nkv, int start, long long quads,
-                                                       float4* out, int* status) {
+// Read-back: out[t][kvh][i] = code * scale of position start + t. A warp takes four tokens of one kv head
+// (hd 64: eight), four codes a lane, so that every access is contiguous and four are in flight. HBM bound.
+constexpr int LD_TOKENS = 32;  // tokens per CTA at hd 128
+template <int HD, int T>
+__global__ void __launch_bounds__(256) kv8_load_kernel(const uint8_t* codes, const float* scales, Kv8Layer c, int nkv, int start,
+                                                       int M, float* out, int* status) {
   PF_TIMELINE(TL_KV8_LOAD);
+  constexpr int LPR = HD / 4, RPW = 32 / LPR;  // lanes per row, rows per warp and pass
   griddep_launch_dependents();
   griddep_wait();
-  const int qpr = hd / 4;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < quads; i += 256ll * gridDim.x) {
-    const long long row = i / qpr;  // (token, kv head)
-    const int q = static_cast<int>(i - row * qpr);
-    const int t = static_cast<int>(row / nkv), kvh = static_cast<int>(row - static_cast<long long>(t) * nkv);
+  const int lane = threadIdx.x & 31, kvh = blockIdx.y;
+  const int t0 = (static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5)) * 4 * RPW + lane / LPR, d = (lane % LPR) * 4;
+  codes += static_cast<size_t>(kvh) * c.slots * HD + d;
+  scales += static_cast<size_t>(kvh) * c.nblk;
+  uint32_t w[4];
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + i * RPW;
+    w[i] = 0;
+    s[i] = 0.f;
+    if (t >= M) continue;
     const int slot = kv8_slot(c, start + t);
     if (slot < 0) {
-      out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (status) atomicCAS(status, 0, PF_ERR_KV_CAPACITY);
       continue;
     }
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (static_cast<size_t>(kvh) * c.slots + slot) * hd + 4 * q);
-    const float s = scales[static_cast<size_t>(kvh) * c.nblk + slot / PF_KV8_BLOCK];
-    out[i] = make_float4(Kv8<T>::decode(w & 255u) * s, Kv8<T>::decode((w >> 8) & 255u) * s,
-                         Kv8<T>::decode((w >> 16) & 255u) * s, Kv8<T>::decode(w >> 24) * s);
+    w[i] = *reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(slot) * HD);
+    s[i] = scales[slot / PF_KV8_BLOCK];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + i * RPW;
+    if (t >= M) break;
+    *reinterpret_cast<float4*>(out + (static_cast<size_t>(t) * nkv + kvh) * HD + d) =
+        make_float4(Kv8<T>::decode(w[i] & 255u) * s[i], Kv8<T>::decode((w[i] >> 8) & 255u) * s[i],
+                    Kv8<T>::decode((w[i] >> 16) & 255u) * s[i], Kv8<T>::decode(w[i] >> 24) * s[i]);
   }
 }
 
@@ -193,14 +248,13 @@ cudaError_t launch_kv8_store(const Kv8StoreArgs& a, cudaStream_t stream) {
 cudaError_t launch_kv8_load(const pf_config& c, const void* cache, int layer, int start, int M, const int* blocks,
                             float* out, int* status, cudaStream_t stream) {
   const Kv8Layer L = kv8_layer(c, cache, nullptr, layer, blocks);
-  const long long quads = static_cast<long long>(M) * c.n_kv_heads * c.head_dim / 4;
-  const int grid = static_cast<int>(quads / 256 + 1 < 152 * 8 ? quads / 256 + 1 : 152 * 8);
+  const int tokens = c.head_dim == 128 ? LD_TOKENS : 2 * LD_TOKENS;
   auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(grid), dim3(256), 0, stream, static_cast<const uint8_t*>(L.k), static_cast<const float*>(L.ks),
-                      L, static_cast<int>(c.head_dim), static_cast<int>(c.n_kv_heads), start, quads, reinterpret_cast<float4*>(out),
-                      status);
+    return launch_pdl(kernel, dim3((M + tokens - 1) / tokens, c.n_kv_heads), dim3(256), 0, stream, static_cast<const uint8_t*>(L.k),
+                      static_cast<const float*>(L.ks), L, static_cast<int>(c.n_kv_heads), start, M, out, status);
   };
-  return c.kv_dtype == PF_KV_E4M3 ? go(kv8_load_kernel<PF_KV_E4M3>) : go(kv8_load_kernel<PF_KV_INT8>);
+  if (c.head_dim == 128) return c.kv_dtype == PF_KV_E4M3 ? go(kv8_load_kernel<128, PF_KV_E4M3>) : go(kv8_load_kernel<128, PF_KV_INT8>);
+  return c.kv_dtype == PF_KV_E4M3 ? go(kv8_load_kernel<64, PF_KV_E4M3>) : go(kv8_load_kernel<64, PF_KV_INT8>);
 }
 
 }  // namespace pf
