@@ -16,17 +16,17 @@
 // written, read by both products, Q), 1,750 cycles at 128 B a cycle against 1,400 of tensor work; a
 // CTA of a pair 128 KB.
 //
-// Warps (16, registers moved between the warpgroups):
+// Warps (16):
 //   0, 2     copies: Q and the K codes (0), the V codes (2), ST stages ahead;
 //   1        TMEM (three S buffers of 128 columns and O) and the MMAs, S_j = Q K_j^T and
 //            O += P_j V_j (P over S's columns), whichever is ready (in a pair, the even CTA's);
 //   3        the scales;
 //   4..7     K and V codes to f16, into shared memory in the MMA's 128-byte swizzle;
-//   8..11    softmax of the even key tiles, 12..15 of the odd ones, one thread per row, so that one
-//            tile's exponentials run while the next one's maximum is taken. The two share each row's
-//            running maximum: a tile's decision to raise it (only when exceeded by more than 2^8; O is
-//            then rescaled in TMEM) follows the previous tile's, warp by warp through a barrier; the
-//            rest runs side by side. A row's 128 scores stay in registers.
+//   8..15    softmax, two threads per row (64 keys each; the maxima meet in shared memory, warp pair by
+//            warp pair): S from TMEM, running maximum raised only when exceeded by more than 2^8 (then O
+//            is rescaled in TMEM), P as f16 back. (Two groups of four warps on alternate key tiles, a
+//            whole row a thread, held each S buffer twice as long: 300 us where this takes @@ for 512
+//            tokens of 32/8 heads at 32,256.)
 // Every wait is bounded; a timeout aborts the CTA and records PF_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
 #include <type_traits>
@@ -42,7 +42,7 @@ constexpr int NSB = 3;   // S / P buffers
 constexpr int LA = 1;    // tiles that the K codes run ahead of the V codes
 constexpr int THREADS = 512;
 constexpr int SM_WARP = 8;        // first softmax warp
-constexpr int SM_THREADS = 256;   // softmax threads: two groups of one per row
+constexpr int SM_THREADS = 256;   // softmax threads: two per row
 constexpr int DQ_THREADS = 128;   // converting threads
 constexpr int NG = TK / PF_KV8_BLOCK;
 constexpr int SCR = 8;   // tiles in the ring of scales
@@ -53,7 +53,8 @@ constexpr uint32_t COL_O = NSB * TK;  // TMEM: S buffer b at b TK, O at COL_O
 
 template <int HD, int PAIR>
 struct TSmem {
-  static constexpr int ST = PAIR ? 3 : 2;          // stages of codes and of f16 tiles, K and V each
+  static constexpr int ST = PAIR ? 3 : 2;          // stages of f16 tiles, K and V each
+  static constexpr int CK = ST, CV = !PAIR && HD == 128 ? 1 : ST;  // stages of codes (what shared memory leaves)
   static constexpr int KR = PAIR ? TK / 2 : TK;    // keys of a K tile that this CTA holds
   static constexpr int VC = PAIR ? HD / 2 : HD;    // columns of a V tile that this CTA holds
   static constexpr int Q = TQ * HD * 2;
@@ -63,9 +64,9 @@ struct TSmem {
   static constexpr int VCODES = TK * VC;
   static constexpr int ROW = HD * 4;  // a row of O at the end, over the idle Q and K tiles
   static constexpr int TILES = Q + ST * (KT + VT);
-  static constexpr int RINGS = ST * (KCODES + VCODES);
+  static constexpr int RINGS = CK * KCODES + CV * VCODES;
   static constexpr int SCALES = SCR * NG * 4 * 4;
-  static constexpr int MAXIMA = TQ * 4;
+  static constexpr int MAXIMA = 4 * TQ * 4;  // of each row, half and (tile parity)
   static constexpr int BARS = 512;
   static constexpr int BYTES = 1024 + TILES + RINGS + SCALES + MAXIMA + BARS;
   // at the end, over the idle tiles: O; over the idle rings: (m, l) of each row, the groups' sums, the
@@ -172,12 +173,6 @@ __device__ __forceinline__ float4 ldc128(uint32_t a) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
-// Registers a thread from here on (all warps of a warpgroup alike): 128 x (48 + 80 + 192 + 192) is the
-// 512 x 128 that the CTA is launched with.
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // x * c + o on two values at once, and x + y.
 __device__ __forceinline__ void fma2(float& a, float& b, float c, float o) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
@@ -218,10 +213,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t q_s = base, k_s = q_s + L::Q, v_s = k_s + ST * L::KT;
-  const uint32_t kc_s = base + L::TILES, vc_s = kc_s + ST * L::KCODES;
+  const uint32_t kc_s = base + L::TILES, vc_s = kc_s + L::CK * L::KCODES;
   float4* scales = reinterpret_cast<float4*>(gbase + L::TILES + L::RINGS);  // [SCR][NG] (log2(e) sK / sqrt(hd), log2 sV, 1 / sV, -)
   const uint32_t sc_s = base + L::TILES + L::RINGS;
-  volatile float* run_m = reinterpret_cast<volatile float*>(gbase + L::TILES + L::RINGS + L::SCALES);  // [TQ] running maxima
+  volatile float* maxima = reinterpret_cast<volatile float*>(gbase + L::TILES + L::RINGS + L::SCALES);  // [2][2][TQ]
   const uint32_t ml_s = kc_s;  // [TQ] (m, l)
   volatile float* sums = reinterpret_cast<volatile float*>(gbase + L::TILES + TQ * 8);  // [2][TQ]
   const uint32_t bar0 = base + L::TILES + L::RINGS + L::SCALES + L::MAXIMA;
@@ -232,7 +227,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto s_full = [&](int b) { return bar0 + 8u * (24 + b); };
   auto s_empty = [&](int b) { return bar0 + 8u * (27 + b); };
   auto p_full = [&](int b) { return bar0 + 8u * (30 + b); };
-  auto turn = [&](int quarter, int x) { return bar0 + 8u * (33 + 2 * quarter + x); };  // group x's decision on its tile
   auto sc_full = [&](int s) { return bar0 + 8u * (41 + s); };
   auto sc_free = [&](int s) { return bar0 + 8u * (55 + s); };
   const uint32_t q_full = bar0 + 8u * 49, q_ready = bar0 + 8u * 50, o_final = bar0 + 8u * 51, drain_bar = bar0 + 8u * 52;
@@ -255,13 +249,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int b = 0; b < NSB; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(s_empty(b), 1);
-      mbar_init(p_full(b), 4 * BOTH);
+      mbar_init(p_full(b), 8 * BOTH);
     }
-    for (int i = 0; i < 4; ++i)
-      for (int x = 0; x < 2; ++x) mbar_init(turn(i, x), 1);
     for (int s = 0; s < SCR; ++s) {
       mbar_init(sc_full(s), 1);
-      mbar_init(sc_free(s), 4);
+      mbar_init(sc_free(s), 8);
     }
     mbar_init(q_full, 1);
     mbar_init(q_ready, BOTH);
@@ -271,7 +263,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (threadIdx.x < TQ) run_m[threadIdx.x] = -INFINITY;
   if (warp == 1) {
     if (PAIR) {
       tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -320,7 +311,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp < 4) {
-    regs_dec<48>();
     if ((warp == 0 || warp == 2) && lane == 0) {
       // -------------------------------------------------------------- copies
       const int v = warp >> 1;
@@ -334,8 +324,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int x0 = v ? half * L::VC : 0, y0 = kvh * P.c.slots + (v ? 0 : half * L::KR);
       int issued = 0, slot = nt > 0 ? slot_of(0) : 0;
       for (int j = 0; j < nt; ++j) {
-        const int st = j % ST, next = slot_of(j + 1);
-        if (!mbar_wait_long(c_empty(v, st), ((j / ST) & 1) ^ 1, abort_flag)) break;
+        const int sc = v ? L::CV : L::CK, st = j % sc, next = slot_of(j + 1);
+        if (!mbar_wait_long(c_empty(v, st), ((j / sc) & 1) ^ 1, abort_flag)) break;
         mbar_arrive_expect_tx(c_full(v, st), bytes);
         tma_load_2d(ring + st * bytes, map, x0, y0 + slot, c_full(v, st));
         ++issued;
@@ -349,7 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // landed before shared memory is used otherwise, whatever the others do
       if (v == 0) wait_drain(q_full, 0);
-      for (int j = max(0, issued - ST); j < issued; ++j) wait_drain(c_full(v, j % ST), (j / ST) & 1);
+      const int sc = v ? L::CV : L::CK;
+      for (int j = max(0, issued - sc); j < issued; ++j) wait_drain(c_full(v, j % sc), (j / sc) & 1);
     }
     __syncwarp();
     if (warp == 3) {
@@ -460,17 +451,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4 && warp < SM_WARP) {
     // ---------------------------------------------------------------- codes to f16
-    regs_dec<80>();
     const int tid = threadIdx.x - 128;
     // A tile of ROWS x C codes (K or V of tile j): 8 codes a thread and pass, one 16-byte piece of f16 in
     // regions of 64 columns (rows of 128 B, swizzled). Rows a pass are a multiple of 8: one swizzle.
     auto convert = [&](auto rows_c, auto cols_c, int v, int j, uint32_t ring, uint32_t tiles, int valid) -> bool {
       constexpr int ROWS = decltype(rows_c)::value, C = decltype(cols_c)::value;
       constexpr int LPR = C / 8, RPP = DQ_THREADS / LPR, NP = ROWS / RPP;
-      const int st = j % ST, row0 = tid / LPR, c8 = tid % LPR;
-      const uint32_t codes = ring + st * (ROWS * C) + tid * 8;
+      const int cs = v ? L::CV : L::CK, cst = j % cs, st = j % ST, row0 = tid / LPR, c8 = tid % LPR;
+      const uint32_t codes = ring + cst * (ROWS * C) + tid * 8;
       const uint32_t put = tiles + st * (ROWS * C * 2) + (c8 >> 3) * (ROWS * 128) + row0 * 128 + (((c8 & 7) ^ (row0 & 7)) << 4);
-      if (!__all_sync(0xffffffffu, mbar_wait_long(c_full(v, st), (j / ST) & 1, abort_flag))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_long(c_full(v, cst), (j / cs) & 1, abort_flag))) return false;
       // the codes into registers at once: their stage takes the next copy while these wait for room
       uint2 w[NP];
 #pragma unroll
@@ -480,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[i].x), "=r"(w[i].y) : "r"(codes + i * RPP * C));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(c_empty(v, st));
+      if (lane == 0) mbar_arrive(c_empty(v, cst));
       if (!__all_sync(0xffffffffu, mbar_wait_long(empty(v, st), ((j / ST) & 1) ^ 1, abort_flag))) return false;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -502,116 +492,111 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= SM_WARP) {
     // ---------------------------------------------------------------- softmax rows
-    regs_inc<192>();
-    const int x = (warp - SM_WARP) >> 2, quarter = warp & 3;
+    const int x = (warp - SM_WARP) >> 2, quarter = warp & 3;  // keys [64 x, 64 x + 64) of each tile
     const int r = 32 * quarter + lane;
     const uint32_t lane_off = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t obuf = tmem + lane_off + COL_O;
     const int first_pos = start + t0, pos = first_pos + r / G;
-    float m = -INFINITY, l = 0.f;  // of this group's tiles; m follows the row's running maximum
-    bool ok = true;
-    for (int j = x; j < nt; j += 2) {
+    float m = -INFINITY, l = 0.f;  // l of this thread's keys
+    bool ok = true, failed = false;
+    for (int j = 0; j < nt; ++j) {
       const int b = j % NSB;
       const uint32_t sbuf = tmem + lane_off + b * TK;
-      // tcgen05.ld / st are warp-collective: waits are voted on
-      ok = __all_sync(0xffffffffu, mbar_wait_long(sc_full(j % SCR), (j / SCR) & 1, abort_flag) && mbar_wait_long(s_full(b), (j / NSB) & 1, abort_flag));
-      if (!ok) break;
+      // tcgen05.ld / st are warp-collective and the two warps of a quarter meet in every tile: a failed
+      // wait is carried to that meeting, where both stop
+      const bool got = mbar_wait_long(sc_full(j % SCR), (j / SCR) & 1, abort_flag) && mbar_wait_long(s_full(b), (j / NSB) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, got) && !failed;
       tc_fence_after();
-      const int lim = pos - (jb + j) * TK;  // last visible column
+      const int lim = pos - (jb + j) * TK - 64 * x;  // last visible one of this thread's columns
       const bool masked = (jb + j) * TK + TK - 1 > first_pos;
-      // a block's factors, read where they are used: registers are scarce
-      const uint32_t sc_at = sc_s + (j % SCR) * NG * 16;
+      const uint32_t sc_at = sc_s + ((j % SCR) * NG + 2 * x) * 16;
       auto factors = [&](int g) {
         float4 f;
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(sc_at + 16 * g));
         return f;
       };
-      uint32_t v[TK];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) tmem_ld_32x32b_x32(sbuf + 32 * g, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * g));
-      tmem_ld_wait();
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < TK; ++e)
-          if (e > lim) v[e] = 0xff800000u;  // -inf
-      }
+      const float4 sc[2] = {factors(0), factors(1)};
+      uint32_t v[64];
       float um = -INFINITY;
+      if (ok) {
+        tmem_ld_32x32b_x32(sbuf + 64 * x, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld_32x32b_x32(sbuf + 64 * x + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_ld_wait();
+        if (masked) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float mx[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(v[32 * g + e]);
-#pragma unroll
-        for (int e = 4; e < 28; e += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(v[32 * g + e + q]), __uint_as_float(v[32 * g + e + 4 + q]));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(v[32 * g + 28 + q]));
-        const float4 sc = factors(g);
-        um = fmaxf(um, fmaf(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])), sc.x, sc.y));
-      }
-      // the row's running maximum, after the other group's decision on tile j - 1
-      if (j > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait_long(turn(quarter, 1 - x), ((j - 1) >> 1) & 1, abort_flag));
-        if (!ok) break;
-      }
-      const float m_run = run_m[r];
-      const bool need = um > m_run + RESCALE_LOG2;  // on the first tile too
-      const float m_new = need ? um : m_run;
-      const bool any = __any_sync(0xffffffffu, need);
-      if (any) {
-        run_m[r] = m_new;
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(turn(quarter, x));
-      if (any && j > 0) {
-        // O holds P_0 .. P_{j-1} V (the other group's P_{j-1} uses the maximum before this one):
-        // wait for PV_{j-1}, then scale it in place; PV_j waits for this thread's P_j. (The barrier of
-        // j - 1's buffer: its phase before, j - 4's, ended before S_{j-1} was issued, and its phase
-        // after waits for P_j, so the parity names one phase.)
-        ok = __all_sync(0xffffffffu, mbar_wait_long(s_empty((j - 1) % NSB), ((j - 1) / NSB) & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        const float alpha = need ? ex2t(m_run - m_new) : 1.f;
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(obuf + 32 * c, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st_32x32b_x32(obuf + 32 * c, o);
+          for (int e = 0; e < 64; ++e)
+            if (e > lim) v[e] = 0xff800000u;  // -inf
         }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float mx[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(v[32 * g + e]);
+#pragma unroll
+          for (int e = 4; e < 28; e += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(v[32 * g + e + q]), __uint_as_float(v[32 * g + e + 4 + q]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(v[32 * g + 28 + q]));
+          um = fmaxf(um, fmaf(max3(mx[0], mx[1], fmaxf(mx[2], mx[3])), sc[g].x, sc[g].y));
+        }
+        maxima[(2 * (j & 1) + x) * TQ + r] = um;
       }
-      if (m != m_new) {  // raised here or by the other group since this group's last tile
-        l *= m == -INFINITY ? 0.f : ex2t(m - m_new);
-        m = m_new;
+      // both halves of the rows have been read (P goes over them) and their maxima are in
+      tc_fence_before();
+      ok = bar_and(2 + quarter, 64, ok);
+      if (!ok) break;
+      tc_fence_after();
+      um = fmaxf(um, maxima[(2 * (j & 1) + 1 - x) * TQ + r]);
+      const bool need = um > m + RESCALE_LOG2;  // the first tile's too; the row's two threads decide alike
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = need ? ex2t(m - um) : 1.f;
+        l *= alpha;
+        if (j > 0) {
+          // O holds P_0 .. P_{j-1} V: wait for PV_{j-1}, then scale this thread's half of the row's columns;
+          // PV_j waits for this thread's P_j. (j - 1's buffer: its phase before ended before S_{j-1} was
+          // issued, its phase after waits for P_j: the parity names one phase.)
+          if (__all_sync(0xffffffffu, mbar_wait_long(s_empty((j - 1) % NSB), ((j - 1) / NSB) & 1, abort_flag))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = x * (HD / 64); c < (x + 1) * (HD / 64); ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(obuf + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_32x32b_x32(obuf + 32 * c, o);
+            }
+          } else {
+            failed = true;
+          }
+        }
+        if (need) m = um;
       }
       const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen no key: every weight 2^-inf = 0
-      // P over the first half of S's columns. Every step runs over 32 columns before the next one does:
-      // the exponentials of a few columns at a time would each wait for the step before.
+      // P over the first half of S's columns, this thread's 32 of them
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float4 sc = factors(g);
-        const float off = sc.y - mm;
-        float u[32];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          u[e] = __uint_as_float(v[32 * g + e]);
-          u[e + 1] = __uint_as_float(v[32 * g + e + 1]);
-          fma2(u[e], u[e + 1], sc.x, off);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) u[e] = ex2t(u[e]);
+      for (int g = 0; g < 2; ++g) {
+        const float off = sc[g].y - mm;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) pk[e / 2] = f16x2t(u[e], u[e + 1]);
-        tmem_st_32x32b_x16(sbuf + 16 * g, pk);
-#pragma unroll
-        for (int w = 16; w > 1; w >>= 1)
-#pragma unroll
-          for (int e = 0; e < w; e += 2) add2(u[e], u[e + 1], u[e + w], u[e + w + 1]);
-        l = fmaf(u[0] + u[1], sc.z, l);
+        for (int e = 0; e < 32; e += 4) {
+          float a = __uint_as_float(v[32 * g + e]), c = __uint_as_float(v[32 * g + e + 1]);
+          float d = __uint_as_float(v[32 * g + e + 2]), f = __uint_as_float(v[32 * g + e + 3]);
+          fma2(a, c, sc[g].x, off);
+          fma2(d, f, sc[g].x, off);
+          a = ex2t(a);
+          c = ex2t(c);
+          d = ex2t(d);
+          f = ex2t(f);
+          add2(s0, s1, a, c);
+          add2(s2, s3, d, f);
+          pk[e / 2] = f16x2t(a, c);
+          pk[e / 2 + 1] = f16x2t(d, f);
+        }
+        l = fmaf((s0 + s1) + (s2 + s3), sc[g].z, l);
+        tmem_st_32x32b_x16(sbuf + 32 * x + 16 * g, pk);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -619,12 +604,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive(sc_free(j % SCR));
     }
     // ---------------------------------------------------------------- O, m, l to shared memory
-    if (ok) ok = mbar_wait_long(o_final, 0, abort_flag);
-    all_ok = bar_and(1, SM_THREADS, ok);  // every MMA that reads the tiles is done, every maximum decided
+    if (ok) ok = !failed && mbar_wait_long(o_final, 0, abort_flag);
+    all_ok = bar_and(1, SM_THREADS, ok);  // every MMA that reads the tiles is done
     if (all_ok) {
       tc_fence_after();
-      const float m_fin = run_m[r];
-      sums[x * TQ + r] = m == -INFINITY ? 0.f : l * ex2t(m - m_fin);
+      sums[x * TQ + r] = l;
       bar_and(1, SM_THREADS, true);
       const int t = t0 + r / G;
       const float inv = cs == 1 ? __fdividef(1.f, sums[r] + sums[TQ + r]) : 1.f;
@@ -659,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (x == 0)
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml_s + r * 8), "f"(m_fin), "f"(sums[r] + sums[TQ + r]) : "memory");
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml_s + r * 8), "f"(m), "f"(sums[r] + sums[TQ + r]) : "memory");
     }
   }
 
