@@ -25,9 +25,20 @@
 //   8..15    softmax, two threads per row (64 keys each; the maxima meet in shared memory, warp pair by
 //            warp pair): S from TMEM, running maximum raised only when exceeded by more than 2^8 (then O
 //            is rescaled in TMEM), P as f16 back. (Two groups of four warps on alternate key tiles, a
-//            whole row a thread, held each S buffer twice as long: 300 us where this takes @@ for 512
+//            whole row a thread, held each S buffer twice as long: 300 us where this takes 292 for 512
 //            tokens of 32/8 heads at 32,256.)
 // Every wait is bounded; a timeout aborts the CTA and records PF_ERR_DEVICE_TIMEOUT.
+//
+// Rounding: P to f16 (the value codes' type in the product), the output to f16; all else f32.
+//
+// Bound (512 tokens of 32/8 heads of 128 over 32,768 int8 keys: 292 us = 0.93 PFLOP/s, 0.49 of the
+// measured burst peak on 128 of 152 SMs): a key tile takes 2,200 cycles (clock stamps in a copy). The two
+// products take about 1,000 each, for 512 of arithmetic: 128 columns do not hide the load of an A operand
+// (16 x 128 in about 93 cycles), and the conversions' shared-memory traffic adds to it. The softmax alone
+// would take 1,850. Without the conversions 265 us, without the exponentials and maxima 246, without the
+// products 250. Tried and slower: both row tiles in one CTA (340), one CTA a row tile (341), P through
+// shared memory (357). A chunk of 64 tokens at position 0, one tile a CTA, takes 10 us: 1 to set up,
+// 1.5 to load, 1 to convert, 3 from the scores to O, 2 to merge.
 #include <algorithm>
 #include <type_traits>
 
@@ -48,7 +59,6 @@ constexpr int NG = TK / PF_KV8_BLOCK;
 constexpr int SCR = 8;   // tiles in the ring of scales
 constexpr int MAX_CLUSTER = 8;
 constexpr float RESCALE_LOG2 = 8.f;
-constexpr int IDLE_NS = 20;
 constexpr uint32_t COL_O = NSB * TK;  // TMEM: S buffer b at b TK, O at COL_O
 
 template <int HD, int PAIR>
@@ -432,7 +442,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           const uint64_t now = global_timer_ns();
           if (t_idle == 0) t_idle = now;
-          __nanosleep(IDLE_NS);  // a warp that polls takes issue slots from those it waits for
           const bool give_up = *abort_flag || now - t_idle > PF_WAIT_LIMIT_NS;
           if (__any_sync(0xffffffffu, give_up)) {
             *abort_flag = 1;
