@@ -25,10 +25,10 @@
 //
 // Rounding: P to f16 (the value codes' type in the product), the output to f16; all else f32.
 //
-// Bound: HBM for long caches (one token of 32/8 heads of 128 over 131,072 e4m3 keys 45.3 us = 5.9 TB/s,
-// 0.89 of the measured copy rate; converting e4m3 takes 85 codes a cycle and SM, of which 23 arrive),
-// launch, load and merge latency for short ones (6.6 us over 512 keys, 8.7 over 8,192). With 16 rows the
-// merge of wide parts and the second MMA column block show: four tokens over 8,192 keys 12.6 us.
+// Bound: HBM for long caches (one token of 32/8 heads of 128 over 131,072 e4m3 keys 45.4 us = 5.9 TB/s,
+// 0.88 of the measured copy rate; converting e4m3 takes 85 codes a cycle and SM, of which 23 arrive),
+// launch, load and merge latency for short ones (6.4 us over 512 keys, int8 9.2 over 8,192). With 16 rows the
+// merge of wide parts and the second MMA column block show: four tokens over 8,192 int8 keys 13.1 us.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -41,7 +41,9 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int UK = PF_KV8_BLOCK;      // keys per unit: one scale block
 constexpr int MAX_SPLIT = 64;         // parts per kv head (one kv head, 16 rows, 131,072 keys: 22.5 us; 128 parts 24.2,
                                       // since one CTA merges them)
-constexpr int FEW_ROWS = 16;          // most rows per kv head of this kernel
+// Most rows per kv head of this kernel. 16 rows (four tokens of 32/8 heads of 128, int8) here and in the form
+// for chunks: 13.1 and 18.4 us over 8,192 keys, 20.4 and 48.2 over 32,768, 9.2 and 8.6 over 512.
+constexpr int FEW_ROWS = 16;
 constexpr float RESCALE_LOG2 = 8.f;
 
 template <int HD, int NB>

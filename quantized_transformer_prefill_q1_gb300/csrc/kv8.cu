@@ -57,8 +57,9 @@ __device__ __forceinline__ uint2 encode8(uint4 raw, __half2 inv) {
 // One CTA = one block of 32 positions of one kv head, K (blockIdx.z 0) or V (1). Eight values a
 // thread and pass, the block's new rows held in registers between the maximum and the rounding, so
 // each row is read once; both in packed f16 arithmetic (in f32, one value at a time, the ALU was 68 %
-// busy and 8,192 tokens of 8 heads of 128 took 15.5 us). Bound: latency at one token (one CTA per
-// head), HBM at long chunks.
+// busy and 8,192 tokens of 8 heads of 128 took 15.5 us under the profiler, now 11.5 with the ALU 37 % busy).
+// Bound: latency at one token (one CTA per head; 1.9 us), memory at long chunks (8,192 tokens 6.4 us in a
+// replayed graph, part of it in L2).
 template <int HD, int T>
 __global__ void __launch_bounds__(ST_THREADS) kv8_store_kernel(const __half* kx, const __half* vx, long long tok_stride,
                                                                long long head_stride, const int* start_dev,

@@ -19,10 +19,10 @@
 // it has, so ties and constant rows end in as few sorts as any other. What the warps kept is ranked by
 // counting.
 //
-// Bound: HBM (4 bytes a logit) for many rows: 512 x 151,936 with 20 alternatives 60.0 us = 5.2 TB/s, 0.78
+// Bound: HBM (4 bytes a logit) for many rows: 512 x 151,936 with 20 alternatives 60.8 us = 5.1 TB/s, 0.77
 // of the measured copy rate (55.3 with the ones summed like the others, which loses an entropy near 0
 // by 1e-6 of itself and more; 72 with __expf in place of the bare instruction, 79 with expf). Latency for
-// few: one row 11.1 us.
+// few: one row 11.2 us.
 #include "ptx.cuh"
 
 namespace pf {
