@@ -37,8 +37,8 @@
 // (16 x 128 in about 93 cycles), and the conversions' shared-memory traffic adds to it. The softmax alone
 // would take 1,850. Without the conversions 265 us, without the exponentials and maxima 246, without the
 // products 250. Tried and slower: both row tiles in one CTA (340), one CTA a row tile (341), P through
-// shared memory (357). A chunk of 64 tokens at position 0, one tile a CTA, takes 9.3 us (stamped when it
-// took 10: 1 to set up, 1.5 to load, 1 to convert, 3 from the scores to O, 2 to merge). The MMA warp polls
+// shared memory (357). A chunk of 64 tokens at position 0, one tile and no cluster, takes 7.2 us (in
+// a cluster, stamped, 10: 1 to set up, 1.5 to load, 1 to convert, 3 from the scores to O, 2 to merge). The MMA warp polls
 // without sleeping: with 20 ns between its looks the case above took 293 us.
 #include <algorithm>
 #include <type_traits>
@@ -58,7 +58,7 @@ constexpr int SM_THREADS = 256;   // softmax threads: two per row
 constexpr int DQ_THREADS = 128;   // converting threads
 constexpr int NG = TK / PF_KV8_BLOCK;
 constexpr int SCR = 8;   // tiles in the ring of scales
-constexpr int MAX_CLUSTER = 8;
+constexpr int PORTABLE_CLUSTER = 8, MAX_CLUSTER = 16;  // above 8 by the attribute that set_attr sets
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr uint32_t COL_O = NSB * TK;  // TMEM: S buffer b at b TK, O at COL_O
 
@@ -212,7 +212,9 @@ __device__ __forceinline__ float4 lds128f(uint32_t a) {
   return v;
 }
 
-template <int HD, int T, int PAIR>
+// CL: most CTAs of its clusters. (The merge holds a row's parts in registers; one instance for 16 took up to 5 %
+// more time where 8 do.)
+template <int HD, int T, int PAIR, int CL>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const TcParams P) {
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int my = rb + (static_cast<int>(threadIdx.x) - 32 * SM_WARP);
     // (a row's parts are all requested before the first is used, and the CTA's own is read as its own:
     // loads from other CTAs move about 16 B a cycle)
-    constexpr int NP = MAX_CLUSTER / W;
+    constexpr int NP = CL / W;
     if (my < re) {
       float mr = -INFINITY, lr = 0.f;
       float2 ml[NP];
@@ -760,12 +762,18 @@ cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream)
   const int sets = (a.M + W * BT - 1) / (W * BT);
   // As many CTAs on a set of rows as run at once: a second wave would cost more than the parts save
   // (128 tokens of 32/8 heads over 8,192 keys: 56 us in 16 clusters of 8, of which 15 run at once, 42 in clusters of 6).
+  // And no part without a key tile, which would only lengthen the merge; a start on the device is not known
+  // here: such calls go by the longest sequence. (8 tokens of 32/8 heads, int8, before both: in clusters of 8
+  // 8.7 us over 8 keys, 19.0 over 8,200 and 47.6 over 32,008; now 6.0, 15.8 and 34.5. Parts up to the number of
+  // tiles are the rule's end, not always its best: 32 tokens of 32/4 heads over 1,032 keys take 11.4 in 9, 11.1 in 8.)
   const long long groups = static_cast<long long>(sets) * c.n_kv_heads;
+  const int tiles = ((a.start_dev ? c.max_seq : a.start_host + a.M) + TK - 1) / TK;
   p.cs = 1;
-  for (int cs = 2; cs <= MAX_CLUSTER / W; ++cs)
+  for (int cs = 2; cs <= std::min(MAX_CLUSTER / W, tiles); ++cs)
     if (groups <= g_active[PAIR][W * cs]) p.cs = cs;
-  return launch_pdl_cluster(attn_kv8_tc_kernel<HD, T, PAIR>, dim3(W * p.cs * sets, c.n_kv_heads), dim3(THREADS), L::BYTES, stream,
-                            W * p.cs, tq, tk, tv, p);
+  const auto kernel = W * p.cs > PORTABLE_CLUSTER ? attn_kv8_tc_kernel<HD, T, PAIR, MAX_CLUSTER>
+                                                  : attn_kv8_tc_kernel<HD, T, PAIR, PORTABLE_CLUSTER>;
+  return launch_pdl_cluster(kernel, dim3(W * p.cs * sets, c.n_kv_heads), dim3(THREADS), L::BYTES, stream, W * p.cs, tq, tk, tv, p);
 }
 
 // Pairs at hd 128 as soon as there are two row tiles.
@@ -776,11 +784,13 @@ cudaError_t launch_form(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t st
   return launch<HD, T, 0>(a, l, stream);
 }
 
-template <int HD, int T, int PAIR>
-cudaError_t set_attr() {
+template <int HD, int T, int PAIR, int CL>
+cudaError_t set_attr_cl() {
   using L = TSmem<HD, PAIR>;
-  cudaError_t e = cudaFuncSetAttribute(attn_kv8_tc_kernel<HD, T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-  for (int size = 2; size <= MAX_CLUSTER && e == cudaSuccess; ++size) {
+  const auto kernel = attn_kv8_tc_kernel<HD, T, PAIR, CL>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e == cudaSuccess && CL > PORTABLE_CLUSTER) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int size = CL > PORTABLE_CLUSTER ? PORTABLE_CLUSTER + 1 : 2; size <= CL && e == cudaSuccess; ++size) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(size);
     cfg.blockDim = dim3(THREADS);
@@ -792,9 +802,15 @@ cudaError_t set_attr() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;  // one CTA an SM whatever the instance: HD and T make no difference
-    if (cudaOccupancyMaxActiveClusters(&n, attn_kv8_tc_kernel<HD, T, PAIR>, &cfg) == cudaSuccess) g_active[PAIR][size] = n;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) g_active[PAIR][size] = n;
   }
   return e;
+}
+
+template <int HD, int T, int PAIR>
+cudaError_t set_attr() {
+  const cudaError_t e = set_attr_cl<HD, T, PAIR, PORTABLE_CLUSTER>(), f = set_attr_cl<HD, T, PAIR, MAX_CLUSTER>();
+  return e != cudaSuccess ? e : f;
 }
 
 }  // namespace

@@ -329,6 +329,23 @@ def test_attention_long_cache(kind, m, start):
     pf.pf_status_read(c.status)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("nq,nkv,hd,m,start",
+                         [(16, 2, 128, 5, 1500), (16, 2, 128, 16, 2030), (16, 1, 128, 3, 4000), (8, 2, 64, 40, 5000),
+                          (16, 1, 64, 77, 1100), (32, 4, 128, 30, 3001), (64, 1, 128, 1, 2047), (64, 1, 64, 3, 9000),
+                          (8, 8, 64, 100, 28), (32, 8, 128, 20, 107), (32, 8, 128, 20, 108), (32, 8, 128, 20, 109)])
+def test_attention_wide_clusters(kind, nq, nkv, hd, m, start):
+    """Few rows over many keys, whose tiles are cut over 9 to 16 CTAs or their pairs, down to one part a tile and
+    uneven ones; and chunks that end just before, at and behind the first tile's end (one part, then two)."""
+    for paged in (False, True):
+        c, val = random_cache(kind, nq, nkv, hd, start + m, paged, seed=m + start)
+        q = queries(c, m, nq, 1.0)
+        out = attend(c, q, start, m)
+        check_norms(c, val, q, out, start, m)
+        assert torch.equal(attend(c, q, start, m)[:m], out[:m])
+        pf.pf_status_read(c.status)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_attention_drawn(seed):
     """Sizes over the whole range."""
