@@ -7,7 +7,10 @@
 // One CTA = one kv head and 128 of its query rows (row = token * G + head in the group) against its
 // share of the key tiles: a cluster shares the rows and cuts the keys between its CTAs; at the end
 // every CTA leaves its rows' sums, maxima and O in its shared memory, and each merges its share of the
-// rows over the cluster. No scratch and no second kernel.
+// rows over the cluster. No scratch and no second kernel. Where a cluster has more CTAs than its rows have
+// key tiles (its size is that of the longest rows, or of the longest sequence when the start is on the
+// device), the ones left over copy nothing, hold no part and only help to merge; rows with one part go
+// straight to the output.
 //
 // At hd 128 and more than one row tile, two CTAs work as a pair (cta_group::2, M = 256): two row tiles
 // of the same kv head, the same key tiles, and each CTA converts only half of them (K: 64 of the 128
@@ -303,8 +306,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int t0 = (set * W + half) * BT, t1 = min(t0 + BT, P.M);  // a pair's second tile may lie past the last token
   const int len = start + min((set + 1) * W * BT, P.M);  // keys that the last row sees
   const int n_tiles = (len + TK - 1) / TK;
-  const int jb = static_cast<int>(static_cast<long long>(n_tiles) * part / cs);
-  const int nt = static_cast<int>(static_cast<long long>(n_tiles) * (part + 1) / cs) - jb;  // this CTA's tiles jb ..
+  const int parts = min(cs, n_tiles);  // each has a tile; a CTA past them has none, and nothing reads its shared memory
+  // its tiles jb .. (at most 2^30 positions: the products stay below 2^28)
+  const int jb = n_tiles * min(part, parts) / parts, nt = n_tiles * min(part + 1, parts) / parts - jb;
   bool all_ok = true;
   auto slot_of = [&](int j) {  // of the CTA's tile j; 0 for an entry outside the pool
     const int s = kv8_slot(P.c, (jb + min(j, nt - 1)) * TK);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   };
 
-  if (warp < 4) {
+  if (warp < 4 && nt > 0) {
     if ((warp == 0 || warp == 2) && lane == 0) {
       // -------------------------------------------------------------- copies
       const int v = warp >> 1;
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const CUtensorMap* map = v ? &tm_v : &tm_k;
       const uint32_t ring = v ? vc_s : kc_s, bytes = v ? L::VCODES : L::KCODES;
       const int x0 = v ? half * L::VC : 0, y0 = kvh * P.c.slots + (v ? 0 : half * L::KR);
-      int issued = 0, slot = nt > 0 ? slot_of(0) : 0;
+      int issued = 0, slot = slot_of(0);
       for (int j = 0; j < nt; ++j) {
         const int sc = v ? L::CV : L::CK, st = j % sc, next = slot_of(j + 1);
         if (!mbar_wait_long(c_empty(v, st), ((j / sc) & 1) ^ 1, abort_flag)) break;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (half == 0) {
+    if (half == 0 && nt > 0) {
       constexpr uint32_t idesc_s = idesc_f16(PAIR ? 2 * TQ : TQ, TK, 0, 0);
       constexpr uint32_t idesc_o = idesc_f16(PAIR ? 2 * TQ : TQ, HD, 0, 1);
       const uint16_t mask = static_cast<uint16_t>(3u << rank);
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
           umma_commit_warp(bar);
       };
-      bool ok = nt == 0 || __all_sync(0xffffffffu, mbar_wait_long(q_ready, 0, abort_flag));
+      bool ok = __all_sync(0xffffffffu, mbar_wait_long(q_ready, 0, abort_flag));
       // S_js and PV_jp are next. The next tile's scores go before a tile's PV (its softmax waits for
       // them), those after it behind: a PV that is ready then leaves no gap while S waits for a buffer.
       int js = 0, jp = 0;
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (j >= LA && !convert(std::integral_constant<int, TK>{}, std::integral_constant<int, L::VC>{}, 1, j - LA, vc_s, v_s, valid_of(j - LA)))
         break;
     }
-  } else if (warp >= SM_WARP) {
+  } else if (warp >= SM_WARP && nt > 0) {
     // ---------------------------------------------------------------- softmax rows
     const int x = (warp - SM_WARP) >> 2, quarter = warp & 3;  // keys [64 x, 64 x + 64) of each tile
     const int r = 32 * quarter + lane;
@@ -623,21 +627,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       sums[x * TQ + r] = l;
       bar_and(1, SM_THREADS, true);
       const int t = t0 + r / G;
-      const float inv = cs == 1 ? __fdividef(1.f, sums[r] + sums[TQ + r]) : 1.f;
+      const float inv = parts == 1 ? __fdividef(1.f, sums[r] + sums[TQ + r]) : 1.f;
       __half* out = P.out + (static_cast<size_t>(t) * P.nq + kvh * G + r % G) * HD;
       // 16-byte piece q of a row at piece q ^ (row % (HD / 4)): a warp's rows hit different banks
       const uint32_t dst = base + r * L::ROW;
 #pragma unroll 1
       for (int c = x * (HD / 64); c < (x + 1) * (HD / 64); ++c) {
         uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld_32x32b_x32(obuf + 32 * c, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (cs == 1) {  // the whole row is here: straight to the output
+        tmem_ld_32x32b_x32(obuf + 32 * c, o);
+        tmem_ld_wait();
+        if (parts == 1) {  // the whole row is here: straight to the output
           if (t < t1) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -659,16 +658,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
-  // every CTA of the cluster has its rows in shared memory; each merges its share of them
+  // every part of the cluster has its rows in shared memory; each CTA merges its share of them
   tc_fence_before();
   __syncwarp();
   if (cs > 1) cluster_sync_all();
-  if (warp >= SM_WARP && all_ok && cs > 1) {
+  if (warp >= SM_WARP && all_ok && parts > 1) {
     // this CTA's rows: the weights of their parts, a row a thread, then four columns a lane and two
     // (hd 64: four) rows a pass and warp
     // (a pair's two row tiles are merged apart, each over the CTAs that hold it)
     const int rb = TQ * part / cs, re = min(TQ * (part + 1) / cs, (t1 - t0) * G);
-    float* wts = const_cast<float*>(sums) + 2 * TQ;  // [row][cs]
+    float* wts = const_cast<float*>(sums) + 2 * TQ;  // [row][parts]
     const int my = rb + (static_cast<int>(threadIdx.x) - 32 * SM_WARP);
     // (a row's parts are all requested before the first is used, and the CTA's own is read as its own:
     // loads from other CTAs move about 16 B a cycle)
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float mr = -INFINITY, lr = 0.f;
       float2 ml[NP];
 #pragma unroll
-      for (int s = 0; s < NP; ++s) ml[s] = s < cs ? ldc64(map_cta(ml_s + my * 8, W * s + half)) : make_float2(-INFINITY, 0.f);
+      for (int s = 0; s < NP; ++s) ml[s] = s < parts ? ldc64(map_cta(ml_s + my * 8, W * s + half)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int s = 0; s < NP; ++s) mr = fmaxf(mr, ml[s].x);
 #pragma unroll
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 #pragma unroll
       for (int s = 0; s < NP; ++s)
-        if (s < cs) wts[my * cs + s] = __fdividef(ml[s].x, lr);
+        if (s < parts) wts[my * parts + s] = __fdividef(ml[s].x, lr);
     }
     bar_and(1, SM_THREADS, true);
     constexpr int RPW = 128 / HD;  // rows a warp's 32 lanes cover
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at = base + row * L::ROW + ((piece ^ (row & (HD / 4 - 1))) << 4);
 #pragma unroll
         for (int s = 0; s < NP; ++s)
-          if (s < cs) o[u][s] = s == part ? lds128f(at) : ldc128(map_cta(at, W * s + half));
+          if (s < parts) o[u][s] = s == part ? lds128f(at) : ldc128(map_cta(at, W * s + half));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -711,8 +710,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < NP; ++s)
-          if (s < cs) {  // a part without a key of the row has weight 0 and O 0
-            const float w = wts[row * cs + s];
+          if (s < parts) {  // a part without a visible key of the row has weight 0 and an O of zeros times values
+            const float w = wts[row * parts + s];
             acc = make_float4(fmaf(w, o[u][s].x, acc.x), fmaf(w, o[u][s].y, acc.y), fmaf(w, o[u][s].z, acc.z), fmaf(w, o[u][s].w, acc.w));
           }
         *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(t0 + row / G) * P.nq + kvh * G + row % G) * HD + 4 * piece) =
@@ -762,8 +761,10 @@ cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream)
   const int sets = (a.M + W * BT - 1) / (W * BT);
   // As many CTAs on a set of rows as run at once: a second wave would cost more than the parts save
   // (128 tokens of 32/8 heads over 8,192 keys: 56 us in 16 clusters of 8, of which 15 run at once, 42 in clusters of 6).
-  // And no part without a key tile, which would only lengthen the merge; a start on the device is not known
-  // here: such calls go by the longest sequence. (8 tokens of 32/8 heads, int8, before both: in clusters of 8
+  // And not more CTAs than the longest rows have key tiles. A start on the device is not known here: such
+  // calls go by the longest sequence, and the kernel leaves out the CTAs that have no tile (a 12-layer session's
+  // chunks of 8, 64 and 200 tokens at 0: 572, 985 and 1,358 us with room for 33,000 positions, 585, 984 and 1,365
+  // with room for 512). (8 tokens of 32/8 heads, int8, before both: in clusters of 8
   // 8.7 us over 8 keys, 19.0 over 8,200 and 47.6 over 32,008; now 6.0, 15.8 and 34.5. Parts up to the number of
   // tiles are the rule's end, not always its best: 32 tokens of 32/4 heads over 1,032 keys take 11.4 in 9, 11.1 in 8.)
   const long long groups = static_cast<long long>(sets) * c.n_kv_heads;

@@ -1,0 +1,71 @@
+"""The 8-bit cache's attention at the edges of what its calls allow: queries that are NaN, sessions whose clusters
+are larger than the keys at hand."""
+import dataclasses
+
+import numpy as np
+import pytest
+
+import test_gpu_kv8 as T
+from oracle import prefill_oracle as O
+from quantized_transformer_prefill_q1_gb300 import pf, synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("nq,nkv,hd,start,m,nan_at", [
+    # row sets of 64 tokens in CTA pairs, the earlier ones with fewer key tiles than the last
+    (32, 8, 128, 0, 200, (0, 5, 31, 32, 63, 64, 150)),
+    (16, 1, 128, 0, 300, (0, 1, 3, 4, 9, 17, 290)),
+    # one CTA a row tile of 128 tokens
+    (8, 8, 64, 0, 300, (0, 1, 64, 127, 128, 299)),
+    (4, 2, 64, 100, 200, (0, 20, 63, 64, 199)),
+    # the few-row form
+    (8, 2, 128, 700, 4, (0, 2, 3)),
+    (8, 1, 64, 5, 1, ()),
+])
+def test_a_nan_query_stays_in_its_own_row(nq, nkv, hd, start, m, nan_at):
+    """A token's query of one head made NaN (of f16's largest pattern, whose pairs read as f32 are NaN too): that
+    row is NaN, every other row keeps its bits."""
+    c, val = T.random_cache("int8", nq, nkv, hd, start + m, True, seed=m)
+    q = T.queries(c, m, nq, 1.0)
+    want = T.attend(c, q, start, m)
+    T.check_norms(c, val, q, want, start, m)
+    nan = torch.tensor([0x7fff], dtype=torch.int16, device="cuda").view(torch.float16)
+    for t in nan_at:
+        h = t % nq
+        bad = q.clone()
+        bad[t, h] = nan
+        got = T.attend(c, bad, start, m)[:m].view(m, nq, hd)
+        assert bool(torch.isnan(got[t, h]).all()), t
+        got[t, h] = want[:m].view(m, nq, hd)[t, h]
+        assert torch.equal(got.view(m, -1), want[:m]), t
+    pf.pf_status_read(c.status)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_session_with_room_for_far_more_keys(monkeypatch, kind, hd):
+    """Chunks of several row tiles at the start of a long cache (the clusters are those of its length, most of
+    their CTAs have no key tile yet), a short one, decoded tokens: logits within 2e-2 of the oracle with the same
+    cache, as in the session tests of short caches."""
+    s = dataclasses.replace(synth.TINY, n_layers=2, vocab=3000, max_seq=4500, n_q_heads=8, n_kv_heads=2, head_dim=hd, kv_dtype="f16")
+    layers, extra = synth.model_inputs(s)
+    toks = synth.tokens(700, s.vocab, seed=2)
+    T.oracle_with_8_bits(monkeypatch, kind)
+    dm = pf.DeviceModel(dataclasses.replace(s, kv_dtype=kind), layers, extra, max_chunk=280)
+    sess = pf.Session(dm)
+    om = O.OracleModel(s, layers, extra)
+    logits = torch.empty(s.vocab, device="cuda")
+    ids = torch.from_numpy(toks.astype(np.int32)).cuda()
+    at = 0
+    for m in (150, 9, 280, 1, 40, 1):
+        _, want = om.forward_chunk(om.embed(toks[at:at + m]), at, True)
+        if m == 1:
+            sess.decode_step(ids[at:at + 1], logits)
+        else:
+            sess.prefill_chunk(toks[at:at + m], at, logits)
+        sess.sync()
+        at += m
+        assert O.rel_l2(logits.cpu().numpy(), want) <= 2e-2, (at, m)
+    assert sess.position == at
