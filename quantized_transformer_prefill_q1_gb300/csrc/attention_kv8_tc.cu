@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(sc_at + 16 * g));
         return f;
       };
-      const float4 sc[2] = {factors(0), factors(1)};
+      float4 sc[2] = {factors(0), factors(1)};
       uint32_t v[64];
       float um = -INFINITY;
       if (ok) {
@@ -565,7 +565,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       um = fmaxf(um, maxima[(2 * (j & 1) + 1 - x) * TQ + r]);
       const bool need = um > m + RESCALE_LOG2;  // the first tile's too; the row's two threads decide alike
-      if (__any_sync(0xffffffffu, need)) {
+      // The weights' exponent s sK + (log2 sV - m) is rounded apart from m, by up to an ulp of m, and from |m| = 2^27
+      // on that alone would take a weight out of f16's range. Scores that large are rounded before the difference,
+      // as their maximum was (elsewhere the branch costs 0.6 % for long lists of keys, 2.4 for 512 tokens at 1,536).
+      const bool far = fabsf(um) > 0x1p20f && um != -INFINITY;
+      if (__any_sync(0xffffffffu, need || far)) {
         const float alpha = need ? ex2t(m - um) : 1.f;
         l *= alpha;
         if (j > 0) {
@@ -588,6 +592,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (need) m = um;
+        if (far) {  // v becomes the exponent itself, with factor 1 and offset m - m
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float a = __uint_as_float(v[e]), c = __uint_as_float(v[e + 1]);
+            fma2(a, c, sc[e >> 5].x, sc[e >> 5].y);
+            add2(a, c, -mm, -mm);
+            v[e] = __float_as_uint(a);
+            v[e + 1] = __float_as_uint(c);
+          }
+          sc[0].x = sc[1].x = 1.f;
+          sc[0].y = sc[1].y = mm;
+        }
       }
       const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen no key: every weight 2^-inf = 0
       // P over the first half of S's columns, this thread's 32 of them

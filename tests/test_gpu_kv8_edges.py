@@ -69,3 +69,35 @@ def test_session_with_room_for_far_more_keys(monkeypatch, kind, hd):
         at += m
         assert O.rel_l2(logits.cpu().numpy(), want) <= 2e-2, (at, m)
     assert sess.position == at
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("nq,nkv,hd,start,m", [(8, 2, 128, 500, 1), (8, 2, 128, 500, 4), (8, 2, 128, 500, 20), (8, 2, 128, 500, 100),
+                                               (4, 4, 64, 300, 70), (16, 1, 128, 90, 60)])
+def test_scores_of_hundreds_of_millions(kind, sign, nq, nkv, hd, start, m):
+    """Queries and keys near f16's largest values, and all scores of either sign: the output is the value of the
+    largest score (where no other one is within the scores' f32 error, 2 hd 2^-24 sum |q k| / sqrt(hd) each as in
+    check_attention, plus the scale's and the sum's rounding, 2^-22 of the score). Its weight is rounded to f16 in
+    the product and not in the sum, 2^-11, as is the output, 2^-11 and 2^-25; three f32 roundings more."""
+    c = T.Cache(kind, nkv, hd, start + m, False, nq, seed=hd + m)
+    k, v = c.rows(start + m, False), c.rows(start + m, False)
+    k = np.clip(np.abs(k.astype(np.float64)) * 16000 + 8000, 0, 60000).astype(np.float16)
+    c.store(k, v, 0)
+    q = (sign * np.clip(np.abs(c.rng.standard_normal((m, nq, hd))) * 16000 + 8000, 0, 60000)).astype(np.float16)
+    out = T.attend(c, torch.from_numpy(q).cuda(), start, m)[:m].cpu().numpy().astype(np.float64).reshape(m, nq, hd)
+    assert np.isfinite(out).all()
+    kd, vd = c.values("k", start + m), c.values("v", start + m)
+    checked = 0
+    for h in range(nq):
+        s = q[:, h].astype(np.float64) @ kd[h // (nq // nkv)].T / np.sqrt(hd)  # all of one sign: |s| is the sum of |q k|
+        s[np.arange(start + m)[None, :] > start + np.arange(m)[:, None]] = -np.inf
+        order = np.argsort(s, 1)
+        best, second = s[np.arange(m), order[:, -1]], s[np.arange(m), order[:, -2]]
+        apart = best - second > 2 * (2 * hd * 2.0 ** -24 + 2.0 ** -22) * np.abs(second) + 200
+        assert np.abs(best).min() > 1.5e9
+        want = vd[h // (nq // nkv)][order[:, -1]]
+        bound = (2 * 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + 2.0 ** -25
+        assert np.all((np.abs(out[:, h] - want) <= bound)[apart])
+        checked += int(apart.sum())
+    assert checked >= nq * m // 2
