@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int s = i % L::NS;
       const uint32_t kt = ring + s * (2 * L::TILE), vt = kt + L::TILE;
       const float c_k = sk * P.scale_log2;
-      const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);
+      const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);  // scales lie in 0 .. 2^16: moves values by less than 2^-51
       const float lsv = __log2f(svc), isv = 1.f / svc;
       if (i + 1 < nu) {
         sk = ks[sl[1] / UK];

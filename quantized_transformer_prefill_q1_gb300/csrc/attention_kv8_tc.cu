@@ -376,6 +376,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < nt; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait_long(sc_free(j % SCR), ((j / SCR) & 1) ^ 1, abort_flag))) break;
         if (lane < NG) {
+          // (scales lie in 0 .. 2^16: the lower limit keeps the logarithm finite and moves values by less than 2^-51,
+          // the upper one is for what is no scale)
           const float svc = fminf(fmaxf(sv, 0x1p-60f), 0x1p60f);
           // the factor of the scores stays > 0: a hidden key's -inf stays -inf
           scales[(j % SCR) * NG + lane] = make_float4(fmaxf(sk * P.scale_log2, 1e-37f), __log2f(svc), 1.f / svc, 0.f);

@@ -5,6 +5,7 @@ import dataclasses
 import numpy as np
 import pytest
 
+import kv8_reference as R
 import test_gpu_kv8 as T
 from oracle import prefill_oracle as O
 from quantized_transformer_prefill_q1_gb300 import pf, synth
@@ -101,3 +102,74 @@ def test_scores_of_hundreds_of_millions(kind, sign, nq, nkv, hd, start, m):
         assert np.all((np.abs(out[:, h] - want) <= bound)[apart])
         checked += int(apart.sum())
     assert checked >= nq * m // 2
+
+
+def given_cache(kind, nq, codes, scales, max_seq):
+    """A linear cache of the given value codes [nkv, L, hd] (numbers of the 8-bit type) and scales [nkv, blocks], by w."""
+    nkv, L, hd = codes["k"].shape
+    c = T.Cache(kind, nkv, hd, max_seq, False, nq)
+    for w in "kv":
+        c.codes[w] = R.encode(kind, codes[w])
+        c.scales[w] = scales[w].astype(np.float32)
+        dev, s = pf.kv8_views(c.cfg, c.dev[w])
+        dev.view(torch.uint8)[c.layer, :, :L] = torch.from_numpy(c.codes[w]).cuda()
+        s[c.layer, :, :scales[w].shape[1]] = torch.from_numpy(c.scales[w]).cuda()
+    return c
+
+
+def check_scaled(c, q, out, start, m):
+    """check_attention's bound elementwise, with its term for weights that are subnormal in f16 taken from what the
+    weights are: probability times V scale, relative to the row's largest, 2^-25 of that for each code. A V
+    scale below 2^-60 counts as that: codes up to 448 give at most 2^-51."""
+    L, hd = start + m, c.hd
+    k, v = c.values("k", L), c.values("v", L)
+    qd = q.cpu().numpy().astype(np.float64)
+    want, mag, _, big = R.attention(qd, k, v, start)
+    got = out[:m].cpu().numpy().astype(np.float64).reshape(want.shape)
+    s_err = (2 * hd + 8) * 2.0 ** -24 * big
+    G = qd.shape[1] // c.nkv
+    see = np.arange(L)[None, :] <= start + np.arange(m)[:, None]
+    for h in range(qd.shape[1]):
+        s = np.where(see, qd[:, h] @ k[h // G].T / np.sqrt(hd), -np.inf)
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        top = (p * np.repeat(c.scales["v"][h // G].astype(np.float64), R.BLOCK)[:L]).max(1)[:, None]
+        codes = np.abs(R.decode(c.kind, c.codes["v"][h // G][:L])).sum(0)[None, :]
+        bound = 2.0 ** -11 * np.abs(want[:, h]) + (2.0 ** -11 + 2 * np.expm1(s_err) + 2.0 ** -20) * mag[:, h]
+        bound += 2.0 ** -25 * top * codes + 2.0 ** -24 + 2.0 ** -51
+        assert np.all(np.abs(got[:, h] - want[:, h]) <= bound), h
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("m", [1, 3, 40, 300])
+def test_value_scales_at_the_ends_of_their_range(kind, m):
+    """Blocks of V at 2^16 (whose keys have weights of about 2^-23), 2^-40, 1, 0 and 2^-100: the small ones give
+    nothing that an f16 holds."""
+    nq, hd, start = 4, 64, 420
+    L = start + m
+    rng = np.random.default_rng(m)
+    nblk = -(-L // R.BLOCK)
+    blocks = np.arange(L) // R.BLOCK % 5
+    k = rng.integers(-1, 2, (1, L, hd)).astype(np.float64)
+    k[:, blocks == 0] = -4
+    v = np.rint(rng.uniform(-14, 14, (1, L, hd))) * 8  # codes of both types
+    scale = np.array([2.0 ** 16, 2.0 ** -40, 1.0, 0.0, 2.0 ** -100])[np.arange(nblk) % 5][None]
+    c = given_cache(kind, nq, {"k": k, "v": v}, {"k": np.ones((1, nblk)), "v": scale}, L + 3)
+    q = torch.from_numpy((0.5 + 0.02 * rng.standard_normal((m, nq, hd))).astype(np.float16)).cuda()
+    check_scaled(c, q, T.attend(c, q, start, m), start, m)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("m", [1, 3, 40, 300])
+def test_key_scales_at_the_ends_of_their_range(kind, m):
+    """Blocks of K at 2^16 (queries are multiples of 2^-8, so that scores are of a few hundreds), 2^-40, 0 and 1."""
+    nq, hd, start = 4, 64, 420
+    L = start + m
+    rng = np.random.default_rng(m)
+    nblk = -(-L // R.BLOCK)
+    k = rng.integers(-1, 2, (1, L, hd)) * (rng.random((1, L, hd)) < 0.2).astype(np.float64)
+    v = np.rint(rng.uniform(-14, 14, (1, L, hd))) * 8
+    scale = np.array([2.0 ** 16, 2.0 ** -40, 0.0, 1.0])[np.arange(nblk) % 4][None]
+    c = given_cache(kind, nq, {"k": k, "v": v}, {"k": scale, "v": np.ones((1, nblk))}, L + 3)
+    q = torch.from_numpy((rng.integers(-3, 4, (m, nq, hd)) * 2.0 ** -8).astype(np.float16)).cuda()
+    check_scaled(c, q, T.attend(c, q, start, m), start, m)
