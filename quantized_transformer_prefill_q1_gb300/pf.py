@@ -319,6 +319,15 @@ def _dense(t, dev: int, dtype: str, what: str, numel: int, optional: bool = Fals
     raise PfError(1, f"{what}: need at least {numel} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
 
 
+def _rows(t, dev: int, what: str, rows: int, n: int, ld: int) -> Optional[int]:
+    """Address of f32 rows of n values, ld apart: a view [>= rows, >= n] of such strides, or contiguous elements."""
+    if t is not None and t.dim() == 2 and t.shape[0] >= rows and t.shape[1] >= n:
+        st = t.stride()
+        if ((st[0] == ld or rows == 1) and (st[1] == 1 or n == 1) and t.get_device() == dev and t.dtype is _torch.float32):
+            return t.data_ptr()
+    return _dense(t, dev, "float32", what, (rows - 1) * ld + n)
+
+
 def _on(dev: int, stream) -> Optional[int]:
     """The stream, or the current one of CUDA device `dev`."""
     return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(dev)
@@ -401,10 +410,10 @@ def pf_op_attention_kv8(cfg, q, k_cache, v_cache, layer, start, m, out, scratch,
 
 def pf_op_logprobs(logits, rows, n, ld, tokens, logprobs, entropy=None, top=0, top_ids=None, top_logprobs=None,
                    status=None, stream=None):
-    """Log probability of tokens[r], entropy and the top alternatives of each row of logits [rows, ld]
-    (each output may be None)."""
+    """Log probability of tokens[r], entropy and the top alternatives of each row of logits [rows, ld], or of a
+    view [rows, n] whose rows are ld apart (each output may be None)."""
     dev = _here()
-    check(lib().pf_op_logprobs(_dense(logits, dev, "float32", "logits", (rows - 1) * ld + n), rows, n, ld,
+    check(lib().pf_op_logprobs(_rows(logits, dev, "logits", rows, n, ld), rows, n, ld,
                                _dense(tokens, dev, "int32", "tokens", rows, True),
                                _dense(logprobs, dev, "float32", "logprobs", rows, True),
                                _dense(entropy, dev, "float32", "entropy", rows, True), top,
