@@ -365,15 +365,18 @@ def kv8_views(cfg, cache):
 
 
 def pf_op_kv8_store(cfg, k, v, layer, start, m, k_cache, v_cache, blocks=None, status=None, stream=None):
-    """k, v: f16 [m, nkv, hd], any token and head strides (multiples of 8, the same for both)."""
+    """k, v: f16 [m, nkv, hd], any token and head strides (multiples of 8, the same for both; those of a
+    dimension of 1 do not count)."""
     dev, l, ref = _here(), lib(), ctypes.byref(cfg)
-    st = k.stride()
+    nkv = cfg.n_kv_heads
+    st, sv = k.stride(), v.stride()
     if (k.get_device() != dev or v.get_device() != dev or k.dtype is not _torch.float16 or v.dtype is not _torch.float16
-            or k.shape != (m, cfg.n_kv_heads, cfg.head_dim) or v.shape != k.shape or v.stride() != st or st[2] != 1):
-        raise PfError(1, f"K / V rows: need f16 {(m, cfg.n_kv_heads, cfg.head_dim)} of equal strides with contiguous elements "
+            or k.shape != (m, nkv, cfg.head_dim) or v.shape != k.shape or st[2] != 1 or sv[2] != 1
+            or (m > 1 and sv[0] != st[0]) or (nkv > 1 and sv[1] != st[1])):
+        raise PfError(1, f"K / V rows: need f16 {(m, nkv, cfg.head_dim)} of equal strides with contiguous elements "
                          f"on the current CUDA device, got {[(tuple(t.shape), t.dtype, t.stride(), str(t.device)) for t in (k, v)]}")
     n = l.pf_kv_bytes(ref)
-    check(l.pf_op_kv8_store(ref, k.data_ptr(), v.data_ptr(), st[0], st[1], layer, start, m, _table(cfg, dev, blocks),
+    check(l.pf_op_kv8_store(ref, k.data_ptr(), v.data_ptr(), st[0] if m > 1 else 0, st[1] if nkv > 1 else 0, layer, start, m, _table(cfg, dev, blocks),
                             _dense(k_cache, dev, "uint8", "K cache", n), _dense(v_cache, dev, "uint8", "V cache", n),
                             _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 

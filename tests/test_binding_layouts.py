@@ -61,6 +61,29 @@ def test_logits_as_a_view_of_wider_rows(lib):
     assert not lib.calls
 
 
+def test_strides_of_single_tokens_and_heads_do_not_count(lib):
+    def call(nkv, k, v):
+        cfg = pf.make_config(dataclasses.replace(synth.QWEN3_8B_LAYER, kv_dtype="int8", n_q_heads=8, n_kv_heads=nkv), 64, max_seq=64)
+        cache = pf.kv8_cache(cfg, device="cpu")
+        pf.pf_op_kv8_store(cfg, k, v, 0, 0, k.shape[0], cache, cache, stream=0)
+        name, a = lib.calls.pop()
+        assert name == "pf_op_kv8_store" and a[1:3] == (k.data_ptr(), v.data_ptr())
+        return a[3:5]
+
+    x = torch.zeros(9, 16, 128, dtype=torch.float16)  # 8 K heads, then 8 V heads
+    odd = torch.zeros(9 * 2048 + 4, dtype=torch.float16)
+    assert call(8, x[:, :8], x[:, 8:]) == (2048, 128)
+    assert call(8, x[:1, :8], torch.zeros(1, 8, 128, dtype=torch.float16))[1] == 128  # token strides 2048 and 1024
+    assert call(1, x[:, :1], odd.as_strided((9, 1, 128), (2048, 3, 1)))[0] == 2048     # head strides 128 and 3
+    assert call(1, odd.as_strided((1, 1, 128), (5, 3, 1)), x[:1, :1]) == (0, 0)
+    one = torch.zeros(9, 8, 128, dtype=torch.float16)
+    for k, v in [(x[:, :8], one), (one, one.transpose(0, 1).contiguous().transpose(0, 1)), (x[:, :8], x[:, 8:, :64]),
+                 (one.reshape(72, 128), one.reshape(72, 128)), (one.float(), one.float()),
+                 (x.as_strided((9, 8, 128), (2048, 128, 0)), one), (one, x.as_strided((9, 8, 128), (1024, 128, 0)))]:
+        refused(lambda: call(8, k, v))
+    assert not lib.calls
+
+
 @pytest.mark.gpu
 def test_views_give_what_the_buffers_give():
     buf = torch.randn(6, 4100, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
@@ -71,3 +94,10 @@ def test_views_give_what_the_buffers_give():
         pf.pf_op_logprobs(x, 6, 4001, 4100, tok, lp, None, 5, ids)
         got.append((lp, ids))
     assert all(torch.equal(a, b) for g in got[1:] for a, b in zip(g, got[0]))
+    cfg = pf.make_config(dataclasses.replace(synth.QWEN3_8B_LAYER, kv_dtype="e4m3"), 64, max_seq=64)
+    kv = torch.randn(9, 16, 128, device="cuda").half()
+    caches = []
+    for k, v in ((kv[4:5, :8], kv[4:5, 8:].contiguous()), (kv[4:5, :8].contiguous(), kv[4:5, 8:].contiguous())):
+        caches.append((pf.kv8_cache(cfg), pf.kv8_cache(cfg)))
+        pf.pf_op_kv8_store(cfg, k, v, 0, 0, 1, *caches[-1])
+    assert all(torch.equal(a, b) for a, b in zip(*caches)) and bool(caches[0][0].any())
