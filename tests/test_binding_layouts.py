@@ -85,6 +85,7 @@ def test_strides_of_single_tokens_and_heads_do_not_count(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")
 def test_views_give_what_the_buffers_give():
     buf = torch.randn(6, 4100, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
     tok = torch.arange(6, dtype=torch.int32, device="cuda") * 600

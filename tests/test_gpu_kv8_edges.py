@@ -173,3 +173,35 @@ def test_key_scales_at_the_ends_of_their_range(kind, m):
     c = given_cache(kind, nq, {"k": k, "v": v}, {"k": scale, "v": np.ones((1, nblk))}, L + 3)
     q = torch.from_numpy((rng.integers(-3, 4, (m, nq, hd)) * 2.0 ** -8).astype(np.float16)).cuda()
     check_scaled(c, q, T.attend(c, q, start, m), start, m)
+
+
+@pytest.mark.parametrize("rows,at", [(1, 300), (50, 300), (3, 383), (200, 200), (130, 250)])
+def test_store_through_a_bad_table_entry(rows, at):
+    """A store whose positions reach a page outside the pool: the status is the store's own (nothing else has run),
+    the positions of good pages are stored, every other byte stays."""
+    for bad in (-1, 7, 1 << 30, -(1 << 31)):
+        c = T.filled("int8", 2, 128, 600, True, 8)
+        assert c.pool == 7
+        t = c.table.copy()
+        t[2] = bad  # positions 256 .. 383
+        table = torch.from_numpy(t).cuda()
+        before = {w: c.dev[w].clone() for w in "kv"}
+        x = {w: c.rows(rows, False) for w in "kv"}
+        d = {w: torch.from_numpy(x[w]).cuda() for w in "kv"}
+        pf.pf_op_kv8_store(c.cfg, d["k"], d["v"], c.layer, at, rows, c.dev["k"], c.dev["v"], table, c.status)
+        with pytest.raises(pf.PfError) as e:
+            pf.pf_status_read(c.status)
+        assert e.value.status == 6
+        first = at // R.BLOCK * R.BLOCK  # a scale that grows takes its block's earlier codes along
+        p = np.arange(first, at + rows)
+        p = p[(p < 256) | (p >= 384)]
+        blk = np.unique(p // R.BLOCK)
+        slots = torch.from_numpy(c.slot_of(p)).cuda()
+        sblk = torch.from_numpy(c.slot_of(blk * R.BLOCK) // R.BLOCK).cuda()
+        for w in "kv":
+            R.store(c.kind, c.codes[w], c.scales[w], x[w], at)
+            want, scale = (t.clone() for t in pf.kv8_views(c.cfg, before[w]))
+            want[c.layer].view(torch.uint8)[:, slots] = torch.from_numpy(c.codes[w][:, p]).cuda()
+            scale[c.layer][:, sblk] = torch.from_numpy(c.scales[w][:, blk]).cuda()
+            got, got_scale = pf.kv8_views(c.cfg, c.dev[w])
+            assert torch.equal(got, want) and torch.equal(got_scale.view(torch.int32), scale.view(torch.int32))
