@@ -67,7 +67,10 @@ typedef enum { PF_W_Q1_G128 = 0, PF_W_INT4_AFFINE_G128 = 1 } pf_wformat;
 /* PF_KV_E4M3 / PF_KV_INT8: one byte per element and an f32 scale for each PF_KV8_BLOCK slots of
  * a (layer, kv head), see "8-bit cache" below. Linear and paged caches (no ring); q is f16. A
  * session rounds a chunk's K and V to f16, stores them in 8 bits and attends to what the cache then
- * holds, the chunk's own positions included; a K or V beyond f16 is recorded as PF_ERR_NONFINITE. */
+ * holds, the chunk's own positions included; a K or V beyond f16 is recorded as PF_ERR_NONFINITE. A
+ * position is read at the scale of its whole block, so results for a token depend on up to 31 later tokens
+ * of its chunk, as far as those raise the scale (int8: the steps of K and V grow with it; e4m3: values
+ * below 2^-6 of it only). */
 typedef enum { PF_KV_F32 = 0, PF_KV_BF16 = 1, PF_KV_F16 = 2, PF_KV_E4M3 = 3, PF_KV_INT8 = 4 } pf_kvdtype;
 
 /* Model configuration ([P1] LayerConfig + the tail's final_norm_eps / vocab). */
@@ -199,7 +202,9 @@ pf_status pf_session_create(const pf_model* model, void* k_cache_dev, void* v_ca
 pf_status pf_session_destroy(pf_session* s);
 int32_t pf_session_position(const pf_session* s); /* -1 for NULL */
 /* Sets the KV position (e.g. 0 to reuse the cache for a new prompt, or the length of a
- * cache the caller filled itself). Slots at or beyond the new position are stale. */
+ * cache the caller filled itself). Slots at or beyond the new position are stale. In an 8-bit cache the
+ * block of 32 that the position lies in keeps its scale, with those later slots in it, and the codes that
+ * were rounded for it, until it is stored from its first position again. */
 pf_status pf_session_set_position(pf_session* s, int32_t position);
 /* 1: record each chunk's launches once per (M, buffers) as a CUDA graph and replay it
  * (default); 0: launch kernels directly. */
@@ -304,7 +309,9 @@ pf_status pf_decode_step_greedy(pf_session* s, const int32_t* token_in_dev, int3
  * final RMSNorm and the LM head on EVERY position and the argmax of each position's logits.
  * logits_all_dev: f32 [M][vocab] (row t = logits after token t); ids_dev: int32 [M], the
  * greedy next token after each position (lowest index on ties). The KV position advances
- * by M. Needs an LM head and vocab % 8 == 0; PF_ERR_SHAPE for M > max_chunk. */
+ * by M. Needs an LM head and vocab % 8 == 0; PF_ERR_SHAPE for M > max_chunk. A rejected draft leaves its
+ * scales in an 8-bit cache: see pf_session_set_position; setting it to a multiple of PF_KV8_BLOCK and
+ * running the accepted tokens from there again takes them out. */
 pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M, int32_t start_pos,
                             float* logits_all_dev, int32_t* ids_dev, void* stream);
 
@@ -314,7 +321,8 @@ pf_status pf_prefill_verify(pf_session* s, const int32_t* tokens_dev, int32_t M,
  * (may be NULL), and with top > 0 the most likely tokens top_ids_dev [M][top] and their log
  * probabilities top_logprobs_dev [M][top] (may be NULL). Checks, errors and the KV position as
  * pf_prefill_verify; a target outside the vocabulary as in pf_op_logprobs, with the session's
- * status word. */
+ * status word. Over an 8-bit cache a score depends, through the blocks' scales, on later tokens of the
+ * chunk too, its target among them (see pf_kvdtype); a cache of 16 bits has no such dependence. */
 pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32_t* targets_dev, int32_t M,
                            int32_t start_pos, float* logits_all_dev, float* logprobs_dev, float* entropy_dev,
                            int32_t top, int32_t* top_ids_dev, float* top_logprobs_dev, void* stream);
@@ -470,7 +478,12 @@ pf_status pf_op_logprobs(const float* logits_dev, int32_t rows, int32_t n, int64
  *   must then have been stored by this call or lie at a power-of-two scale);
  *   if s > s_old, the earlier positions' codes become RNE(code * s_old / s);
  *   new codes = RNE(x / s), ties to even.
- * Positions past the chunk keep their bytes. A NaN is held as zero and an infinity as the largest
+ * Positions past the chunk keep their bytes. So a block's scale is that of the largest value that it has
+ * taken since it was stored from its first position, and later positions can move what earlier ones hold:
+ * a code that such a scale catches up with is rounded again. In all a value is then off by less than one
+ * step of the last scale (int8) where one chunk alone rounds by half a step; e4m3 moves only below 2^-6 of
+ * the scale, in steps of 2^-9. Storing a prompt in other chunks gives the same scales, int8 codes that differ by
+ * at most 1 and the same e4m3 codes above 2^-6. A NaN is held as zero and an infinity as the largest
  * code, neither counts for the maximum, and PF_ERR_NONFINITE is recorded in *status_dev.
  *
  * pf_op_kv8_load: out f32 [M][nkv][hd] = the values of positions start_pos .. +M-1 in `cache`

@@ -205,3 +205,57 @@ def test_store_through_a_bad_table_entry(rows, at):
             scale[c.layer][:, sblk] = torch.from_numpy(c.scales[w][:, blk]).cuda()
             got, got_scale = pf.kv8_views(c.cfg, c.dev[w])
             assert torch.equal(got, want) and torch.equal(got_scale.view(torch.int32), scale.view(torch.int32))
+
+
+def growing_rows(c, n):
+    """Rows whose largest value grows by about 2^6 within every block of 32: every chunk raises its scale."""
+    x = c.rng.standard_normal((n, c.nkv, c.hd)) * 2.0 ** (np.arange(n) % 32 / 5 - 3)[:, None, None]
+    return x.astype(np.float16)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hd,paged", [(128, False), (64, True)])
+def test_how_far_a_cut_prompt_is_from_one_chunk(kind, hd, paged):
+    """The scales are the same. A code that later chunks of its block scale down is rounded once for each: by at
+    most 1/2, then, in steps of the last scale, 1/4, 1/8, ... before it (each scale at most half of the next), less
+    than 1 in all where one chunk rounds by 1/2: int8 codes differ by at most 1. So do e4m3's below 2^-6, whose steps
+    are 2^-9; above, a power of two as the scale moves no rounding."""
+    a, b = T.Cache(kind, 2, hd, 300, paged, seed=5), T.Cache(kind, 2, hd, 300, paged, seed=5)
+    k, v = growing_rows(a, 300), growing_rows(a, 300)
+    a.store(k, v, 0)
+    at = 0
+    for m in (3, 50, 1, 1, 17, 100, 5, 81, 1, 1, 40):
+        b.store(k[at:at + m], v[at:at + m], at)
+        at += m
+    assert at == 300
+    a.check(300), b.check(300)
+    for w, x in (("k", k), ("v", v)):
+        assert np.array_equal(a.scales[w], b.scales[w])
+        one, cut = R.decode(kind, a.codes[w]), R.decode(kind, b.codes[w])
+        step = 1.0 if kind == "int8" else 2.0 ** -9
+        assert np.abs(one - cut).max() <= step
+        if kind == "e4m3":
+            assert np.array_equal(one[np.abs(one) > 2.0 ** -6], cut[np.abs(one) > 2.0 ** -6])
+        s = np.repeat(b.scales[w].astype(np.float64), R.BLOCK, axis=1)[:, :300, None]
+        err = np.abs(cut * s - x.astype(np.float64).transpose(1, 0, 2)) / s
+        if kind == "int8":
+            assert (one != cut).any()  # so it does differ
+            assert err.max() < 1 and np.abs(one * s - x.astype(np.float64).transpose(1, 0, 2)).max() <= 0.5 * s.max()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_a_rejected_draft_leaves_its_scale(kind):
+    """A draft of large rows is stored, all of it but the first token rejected, smaller rows stored in its place: the
+    block keeps the draft's scale, until it is stored again from its first position."""
+    c = T.Cache(kind, 2, 128, 128, True)
+    small = [c.rows(32, False) for _ in range(2)]
+    big = c.rows(5, False) * np.float16(64)
+    c.store(small[0][:10], small[1][:10], 0)
+    before = {w: c.scales[w][:, 0].copy() for w in "kv"}
+    c.store(big, big, 10)
+    c.store(small[0][11:20], small[1][11:20], 11)
+    c.check(20)
+    assert all((c.scales[w][:, 0] >= 32 * before[w]).all() for w in "kv")
+    c.store(*(x[:20] for x in small), 0)
+    c.check(20)
+    assert all((c.scales[w][:, 0] <= 2 * before[w]).all() for w in "kv")
