@@ -259,3 +259,72 @@ def test_a_rejected_draft_leaves_its_scale(kind):
     c.store(*(x[:20] for x in small), 0)
     c.check(20)
     assert all((c.scales[w][:, 0] <= 2 * before[w]).all() for w in "kv")
+
+
+@pytest.mark.parametrize("kind,nq,nkv,hd,start,m", [("e4m3", 4, 2, 128, 0, 8192), ("int8", 4, 1, 128, 777, 5000),
+                                                    ("int8", 2, 2, 64, 0, 8192), ("e4m3", 8, 1, 64, 100, 4100)])
+def test_the_longest_chunks(kind, nq, nkv, hd, start, m):
+    """As long as a session's chunk may be: row sets in several waves, of one to 64 key tiles."""
+    c, val = T.random_cache(kind, nq, nkv, hd, start + m, True, seed=m)
+    q = T.queries(c, m, nq, 1.0)
+    out = T.attend(c, q, start, m)
+    T.check_norms(c, val, q, out, start, m)
+    assert bool((out[m:] == 3).all())
+    pf.pf_status_read(c.status)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_offsets_past_32_bits(kind):
+    """A layer of more than 2^32 bytes: the last positions stored, read back and attended to by both forms. The
+    others hold zeros (score 0): the stored keys' scores of about 60 leave them a weight of 2^25 e^-60."""
+    hd, nq, n = 128, 4, 100
+    max_seq = (1 << 25) + 300
+    c = T.Cache.__new__(T.Cache)
+    c.kind, c.layer, c.nkv, c.hd, c.rng, c.table_dev = kind, 0, 1, hd, np.random.default_rng(1), None
+    c.cfg = T.config(kind, nq, 1, hd, max_seq, 0, n_layers=1)
+    c.status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    c.dev = {w: pf.kv8_cache(c.cfg) for w in "kv"}
+    at = max_seq - n
+    k, v = c.rows(n, False), c.rows(n, False)
+    k[:, :, :8] = np.abs(k[:, :, :8]) + np.float16(8)
+    kd, vd = torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda()
+    pf.pf_op_kv8_store(c.cfg, kd, vd, 0, at, n, c.dev["k"], c.dev["v"], None, c.status)
+    val = {}
+    for w in "kv":
+        back = torch.empty(n, 1, hd, device="cuda")
+        pf.pf_op_kv8_load(c.cfg, c.dev[w], 0, at, n, back, None, c.status)
+        val[w] = back.double()[:, 0]
+        codes, scales = np.zeros((1, 128, hd), np.uint8), np.zeros((1, 4), np.float32)
+        lo = at % R.BLOCK
+        scales[:, 0] = 2.0 ** -32  # the zeros before: a scale below any
+        R.store(kind, codes, scales, k if w == "k" else v, lo)
+        want = R.values(kind, codes, scales)[0, lo:lo + n]
+        assert np.array_equal(back[:, 0].cpu().numpy().astype(np.float64), want)
+        dev = pf.kv8_views(c.cfg, c.dev[w])[0]
+        assert not bool(dev[0, 0, :1 << 20].view(torch.uint8).any()) and not bool(dev[0, 0, at - 1000:at].view(torch.uint8).any())
+    for m in (1, 4, 40):
+        q = torch.from_numpy((0.3 * c.rng.standard_normal((m, nq, hd))).astype(np.float16)).cuda()
+        q[:, :, :8] = 10
+        out = T.attend(c, q, max_seq - m, m)[:m].double().view(m, nq, hd)
+        see = torch.arange(n, device="cuda")[None, :] <= n - m + torch.arange(m, device="cuda")[:, None]
+        for h in range(nq):
+            s = q[:, h].double() @ val["k"].T / hd ** 0.5
+            assert float(s.min()) > 50
+            p = torch.exp(s.masked_fill(~see, -float("inf")))
+            want = p @ val["v"] / (p.sum(1, keepdim=True) + at)
+            assert float((out[:, h] - want).norm() / want.norm()) <= 5e-4, (m, h)
+    pf.pf_status_read(c.status)
+
+
+def test_logits_rows_past_32_bits():
+    """Rows whose distance is 2^30 + 8 values: the third starts behind 2^33 bytes."""
+    ld, n = (1 << 30) + 8, 5000
+    buf = torch.empty(3 * ld, device="cuda")
+    x = buf.as_strided((3, n), (ld, 1))
+    x.copy_(torch.randn(3, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)))
+    lp, ids = torch.empty(3, device="cuda"), torch.empty(3, 4, dtype=torch.int32, device="cuda")
+    tok = torch.tensor([1, 4999, 77], dtype=torch.int32, device="cuda")
+    pf.pf_op_logprobs(x, 3, n, ld, tok, lp, None, 4, ids)
+    ref = torch.log_softmax(x.double(), 1)
+    assert float((lp.double() - ref.gather(1, tok.long()[:, None])[:, 0]).abs().max()) <= 2e-5
+    assert torch.equal(ids.long(), ref.topk(4, 1).indices)
