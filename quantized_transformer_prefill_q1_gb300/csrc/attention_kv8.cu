@@ -42,7 +42,8 @@ constexpr int UK = PF_KV8_BLOCK;      // keys per unit: one scale block
 constexpr int MAX_SPLIT = 64;         // parts per kv head (one kv head, 16 rows, 131,072 keys: 22.5 us; 128 parts 24.2,
                                       // since one CTA merges them)
 // Most rows per kv head of this kernel. 16 rows (four tokens of 32/8 heads of 128, int8) here and in the form
-// for chunks: 13.1 and 15.7 us over 8,192 keys, 20.5 and 35.3 over 32,768, 9.2 and 8.3 over 512.
+// for chunks: 13.1 and 15.6 us over 8,192 keys, 20.4 and 34.7 over 32,768, 9.1 and 8.2 over 512 (the rule does not
+// look at the length).
 constexpr int FEW_ROWS = 16;
 constexpr float RESCALE_LOG2 = 8.f;
 

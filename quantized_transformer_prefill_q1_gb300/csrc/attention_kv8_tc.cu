@@ -35,12 +35,12 @@
 // Rounding: P to f16 (the value codes' type in the product), the output to f16; all else f32.
 //
 // Bound (512 tokens of 32/8 heads of 128 over 32,768 int8 keys: 292 us = 0.93 PFLOP/s, 0.49 of the
-// measured burst peak on 128 of 152 SMs): a key tile takes 2,200 cycles (clock stamps in a copy). The two
-// products take about 1,000 each, for 512 of arithmetic: 128 columns do not hide the load of an A operand
-// (16 x 128 in about 93 cycles), and the conversions' shared-memory traffic adds to it. The softmax alone
-// would take 1,850. Without the conversions 265 us, without the exponentials and maxima 246, without the
-// products 250. Tried and slower: both row tiles in one CTA (340), one CTA a row tile (341), P through
-// shared memory (357). A chunk of 64 tokens at position 0, one tile and no cluster, takes 7.2 us (in
+// measured burst peak on 128 of 152 SMs): a key tile takes 2,200 cycles (clock stamps in a copy), 1.15 us,
+// where attention_tc.cu takes 0.85 for the same tile of a 16-bit cache. Without the conversions the case takes
+// 265 us (1.03 a tile), without the exponentials and maxima 246, without the products 250. So the conversions are
+// about a third of the difference; what the rest consists of (the hand-over between the CTAs of a pair,
+// the polling, the scales) was not measured apart. Tried and slower: both row tiles in one CTA (340), one CTA a
+// row tile (341), P through shared memory (357). A chunk of 64 tokens at position 0, one tile and no cluster, takes 7.0 us (in
 // a cluster, stamped, 10: 1 to set up, 1.5 to load, 1 to convert, 3 from the scores to O, 2 to merge). The MMA warp polls
 // without sleeping: with 20 ns between its looks the case above took 293 us.
 #include <algorithm>
@@ -126,7 +126,7 @@ __device__ __forceinline__ uint32_t f16x2t(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// mbar_wait with the hardware suspending the thread for up to 20 us a try: 20 warps that poll would take
+// mbar_wait with the hardware suspending the thread for up to 20 us a try: 16 warps that poll would take
 // issue slots from those that work.
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -779,13 +779,14 @@ cudaError_t launch(const Kv8AttnArgs& a, const Kv8Layer& l, cudaStream_t stream)
   p.status = a.status;
   const int sets = (a.M + W * BT - 1) / (W * BT);
   // As many CTAs on a set of rows as run at once: a second wave would cost more than the parts save
-  // (128 tokens of 32/8 heads over 8,192 keys: 56 us in 16 clusters of 8, of which 15 run at once, 42 in clusters of 6).
+  // (128 tokens of 32/8 heads over 8,192 keys took 56 us in 16 clusters of 8, of which 15 run at once, when clusters of 6
+  // took 42; they take 37 now).
   // And not more CTAs than the longest rows have key tiles. A start on the device is not known here: such
   // calls go by the longest sequence, and the kernel leaves out the CTAs that have no tile (a 12-layer session's
   // chunks of 8, 64 and 200 tokens at 0: 572, 985 and 1,358 us with room for 33,000 positions, 585, 984 and 1,365
   // with room for 512). (8 tokens of 32/8 heads, int8, before both: in clusters of 8
-  // 8.7 us over 8 keys, 19.0 over 8,200 and 47.6 over 32,008; now 6.0, 15.8 and 34.5. Parts up to the number of
-  // tiles are the rule's end, not always its best: 32 tokens of 32/4 heads over 1,032 keys take 11.4 in 9, 11.1 in 8.)
+  // 8.7 us over 8 keys, 19.0 over 8,200 and 47.6 over 32,008; now 5.7, 16.0 and 34.1. Parts up to the number of
+  // tiles are the rule's end, not always its best: 32 tokens of 32/4 heads over 1,032 keys took 11.4 in 9, 11.1 in 8.)
   const long long groups = static_cast<long long>(sets) * c.n_kv_heads;
   const int tiles = ((a.start_dev ? c.max_seq : a.start_host + a.M) + TK - 1) / TK;
   p.cs = 1;
