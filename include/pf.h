@@ -494,7 +494,7 @@ pf_status pf_op_logprobs(const float* logits_dev, int32_t rows, int32_t n, int64
  * in f32, each weight (probability times V scale, relative to the row's largest so far) rounded to f16
  * for its product with the value codes. Positions from start_pos + M on are not used, whatever their codes
  * and scales hold. Scales of earlier blocks are numbers from 0 to 2^16, of K and of V (the
- * store writes 2^-32 .. 2^8; a V scale below 2^-60 counts as 2^-60, whose values are far below what an f16
+ * store writes 2^-32 .. 2^10; a V scale below 2^-60 counts as 2^-60, whose values are far below what an f16
  * holds), and a NaN code (0x7f / 0xff of e4m3, which the store never writes) at a position below
  * start_pos + M may make any row's output NaN. scratch_dev:
  * device, 16-B aligned, at least pf_attention_kv8_scratch_bytes(cfg, M) bytes (which does not fall

@@ -105,6 +105,7 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > PF_WAIT_LIMIT_NS) return;
   }
 }
+// (bar.red wants its warps converged: __syncwarp() before it where they come from waits or branches of single threads)
 __device__ __forceinline__ bool bar_and(int id, int threads, bool pred) {
   uint32_t r;
   asm volatile(
@@ -607,6 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           sc[0].x = sc[1].x = 1.f;
           sc[0].y = sc[1].y = mm;
         }
+        __syncwarp();  // the warp-wide store of P follows
       }
       const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen no key: every weight 2^-inf = 0
       // P over the first half of S's columns, this thread's 32 of them
@@ -640,6 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // ---------------------------------------------------------------- O, m, l to shared memory
     if (ok) ok = !failed && mbar_wait_long(o_final, 0, abort_flag);
+    __syncwarp();
     all_ok = bar_and(1, SM_THREADS, ok);  // every MMA that reads the tiles is done
     if (all_ok) {
       tc_fence_after();
@@ -666,6 +669,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
+          __syncwarp();  // the warp-wide load of the next columns follows
         } else {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -707,6 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int s = 0; s < NP; ++s)
         if (s < parts) wts[my * parts + s] = __fdividef(ml[s].x, lr);
     }
+    __syncwarp();
     bar_and(1, SM_THREADS, true);
     constexpr int RPW = 128 / HD;  // rows a warp's 32 lanes cover
     constexpr int U = PAIR ? 2 : 1;
