@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(THREADS, 4)
       }
     }
   }
+  __syncwarp();  // the cluster's barrier takes converged warps
   if (cs > 1) cluster_sync_all();  // the first CTA has read the others' shared memory
 }
 
