@@ -28,21 +28,21 @@
 //   8..15    softmax, two threads per row (64 keys each; the maxima meet in shared memory, warp pair by
 //            warp pair): S from TMEM, running maximum raised only when exceeded by more than 2^8 (then O
 //            is rescaled in TMEM), P as f16 back. (Two groups of four warps on alternate key tiles, a
-//            whole row a thread, held each S buffer twice as long: 300 us where this takes 292 for 512
+//            whole row a thread, held each S buffer twice as long: 300 us where this took 292 for 512
 //            tokens of 32/8 heads at 32,256.)
 // Every wait is bounded; a timeout aborts the CTA and records PF_ERR_DEVICE_TIMEOUT.
 //
 // Rounding: P to f16 (the value codes' type in the product), the output to f16; all else f32.
 //
-// Bound (512 tokens of 32/8 heads of 128 over 32,768 int8 keys: 292 us = 0.93 PFLOP/s, 0.49 of the
+// Bound (512 tokens of 32/8 heads of 128 over 32,768 int8 keys: 293 us = 0.93 PFLOP/s, 0.49 of the
 // measured burst peak on 128 of 152 SMs): a key tile takes 2,200 cycles (clock stamps in a copy), 1.15 us,
-// where attention_tc.cu takes 0.85 for the same tile of a 16-bit cache. Without the conversions the case takes
-// 265 us (1.03 a tile), without the exponentials and maxima 246, without the products 250. So the conversions are
+// where attention_tc.cu takes 0.85 for the same tile of a 16-bit cache. Without the conversions the case took
+// 265 us (1.03 a tile) instead of 292, without the exponentials and maxima 246, without the products 250. So the conversions are
 // about a third of the difference; what the rest consists of (the hand-over between the CTAs of a pair,
 // the polling, the scales) was not measured apart. Tried and slower: both row tiles in one CTA (340), one CTA a
 // row tile (341), P through shared memory (357). A chunk of 64 tokens at position 0, one tile and no cluster, takes 7.0 us (in
 // a cluster, stamped, 10: 1 to set up, 1.5 to load, 1 to convert, 3 from the scores to O, 2 to merge). The MMA warp polls
-// without sleeping: with 20 ns between its looks the case above took 293 us.
+// without sleeping: with 20 ns between its looks the long case took 293 us where it took 291.8.
 #include <algorithm>
 #include <type_traits>
 
