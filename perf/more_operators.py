@@ -83,7 +83,7 @@ def draw(rng):
         c = adapters("", k, n, 8 * rng.choice([1, 2, 2, 3, 4, 8]), seqs, (lo, hi), rng.randint(1, 16))
     else:
         kv, paged = rng.choice(["bf16", "f16"]), rng.random() < 0.8
-        nq, nkv, hd = rng.choice([(32, 8, 128), (32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (32, 4, 128), (28, 4, 128)])
+        nq, nkv, hd = rng.choice([(32, 8, 128), (32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (32, 4, 128), (64, 8, 128)])
         seqs = _log(rng, 1, 48) if paged else 1
         hi = rng.choice([1, _log(rng, 2, 64), _log(rng, 2, 64)])
         lo = rng.randint(0 if seqs > 1 and hi > 1 else 1, hi)
