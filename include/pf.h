@@ -111,6 +111,9 @@ typedef struct {
 #define PF_KV_BLOCK 128 /* positions per paged KV block: one attention key tile */
 #define PF_KV8_BLOCK 32 /* slots that share one scale in an 8-bit cache */
 #define PF_MAX_TOP 32   /* most alternatives per row (pf_op_logprobs) */
+#define PF_MAX_SEQS 1024 /* most sequences of a batch (pf_batch) */
+#define PF_MAX_TREE 256  /* most rows of one sequence that has a tree, or that pf_op_attention_tree takes */
+#define PF_MAX_RANK 128  /* largest adapter rank (pf_op_adapters) */
 
 /* One layer's weights ([P1] LayerWeightRefs), all device pointers. Packed tensors
  * come from pf_pack_weights_host (gate_up with interleave_gate_up = 1). */
@@ -515,6 +518,79 @@ pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q_f16_dev, c
                               const void* v_cache_dev, int32_t layer, int32_t start_pos, int32_t M,
                               const int32_t* block_table_dev, uint16_t* out_f16_dev, void* scratch_dev,
                               size_t scratch_bytes, int32_t* status_dev, void* stream);
+/* ------------------------------------------------------------------ many sequences at once
+ * The rows of a step over n_seq sequences (requests): sequence b has rows row_begin_dev[b] ..
+ * row_begin_dev[b + 1] - 1 of the call's row arrays, none or as many as max_rows. Everything that changes
+ * from step to step is in device memory, so that a step can be captured once and replayed.
+ *   start_dev[b]   positions that the cache holds of sequence b before its rows; row i lies at position start + i.
+ *   parent_dev     NULL: the rows are a chain. Else row i of a sequence is a node of a tree of drafted tokens and
+ *                  parent_dev[row_begin + i] < i is the node before it, -1 the cached positions (several nodes
+ *                  may hang there): its depth (0 under the cache) takes i's place in the rotation, and it sees the
+ *                  cached positions, its ancestors and itself. A sequence then has at most PF_MAX_TREE rows.
+ *   block_table_dev  paged caches: [n_seq][ceil(max_seq / PF_KV_BLOCK)], the physical block of each position
+ *                  block; NULL for a linear cache, which holds one sequence (n_seq = 1).
+ * Numbers in device memory are checked by the kernels, which follow none that is out of range and record in
+ * *status_dev (may be NULL): row_begin that falls, passes n_rows or makes more than max_rows rows: PF_ERR_SHAPE;
+ * a start below 0 or rows past max_seq: PF_ERR_KV_CAPACITY; the sequence is then left out, its rows in the
+ * outputs stay as they were. A table entry outside the pool: PF_ERR_KV_CAPACITY, what would lie there is not
+ * written, and read as any block. A parent outside -1 .. i - 1: PF_ERR_INVALID_ARG, taken as -1. Table entries of
+ * the positions that a call writes are distinct. Rows behind the last sequence are neither read nor written.
+ * Errors of these calls: PF_ERR_INVALID_ARG (pointers, alignment, a table with a linear cache or none with a
+ * paged one), PF_ERR_EMPTY_CHUNK (n_rows 0), PF_ERR_SHAPE (counts, layer, rank, widths, strides),
+ * PF_ERR_UNSUPPORTED (a ring, a cache that is not bf16 or f16, a linear cache with several sequences),
+ * PF_ERR_WORKSPACE, PF_ERR_CUDA. */
+typedef struct {
+  int32_t n_seq;                  /* 1 .. PF_MAX_SEQS */
+  int32_t n_rows;                 /* rows that the row arrays hold */
+  int32_t max_rows;               /* most rows of one sequence */
+  const int32_t* row_begin_dev;   /* [n_seq + 1] */
+  const int32_t* start_dev;       /* [n_seq]; not used by pf_op_adapters */
+  const int32_t* parent_dev;      /* [n_rows] or NULL */
+  const int32_t* block_table_dev; /* [n_seq][ceil(max_seq / PF_KV_BLOCK)] or NULL */
+} pf_batch;
+
+/* Per-head QK RMSNorm (cfg->qk_norm) + RoPE + KV store of every sequence's rows, as pf_op_qk_norm_rope_kv: from
+ * qkv f32 [n_rows][(nq + 2 nkv) hd] to q_dev [n_rows][nq][hd] of the cache's type and the slots of positions
+ * start .. of `layer`. rope_dev: [max_seq][hd / 2] of (cos, sin). */
+pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const float* qkv_dev, const float* q_norm_dev,
+                             const float* k_norm_dev, const float* rope_dev, int32_t layer, void* q_dev,
+                             void* k_cache_dev, void* v_cache_dev, int32_t* status_dev, void* stream);
+/* Attention of every sequence's rows over its cached positions and its own rows, as far as each sees them: q
+ * [n_rows][nq][hd] of the cache's type, out f16 [n_rows][nq hd]. At most PF_MAX_TREE rows a sequence, trees or
+ * chains. Positions from start + rows on are not used, whatever their slots hold. scratch_dev: 16-B aligned,
+ * at least pf_attention_tree_scratch_bytes(cfg, n_seq, max_rows) bytes (which does not fall as either grows), zero before the first call;
+ * each call that completes leaves it ready for the next (after PF_ERR_DEVICE_TIMEOUT zero it again). Calls
+ * sharing one scratch must not overlap in time. */
+size_t pf_attention_tree_scratch_bytes(const pf_config* cfg, int32_t n_seq, int32_t max_rows);
+pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, const void* q_dev, const void* k_cache_dev,
+                               const void* v_cache_dev, int32_t layer, uint16_t* out_f16_dev, void* scratch_dev,
+                               size_t scratch_bytes, int32_t* status_dev, void* stream);
+/* Greedy acceptance. root_ids_dev[b]: the token that follows the cached positions of sequence b; tokens_dev
+ * [n_rows]: each node's token; ids_dev [n_rows]: the token that the model gives after each node. From the cached
+ * positions on, the child with the wanted token (the lowest among several) is accepted and its id is wanted next,
+ * until no child has it. path_dev [n_rows]: the accepted nodes of each sequence in order, then -1;
+ * n_accepted_dev [n_seq]: how many; next_dev [n_seq]: the wanted token that no node had (the next root id).
+ * The accepted nodes' K and V of every layer move up to positions start .. start + n_accepted - 1, where the next
+ * step's start is start + n_accepted; other slots stay. k_cache_dev and v_cache_dev both NULL: nothing is
+ * moved. The outputs overlap no input. A sequence that is left out gets n_accepted 0 and next = its root id. */
+pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const int32_t* tokens_dev, const int32_t* ids_dev,
+                            const int32_t* root_ids_dev, int32_t* path_dev, int32_t* n_accepted_dev, int32_t* next_dev,
+                            void* k_cache_dev, void* v_cache_dev, int32_t* status_dev, void* stream);
+/* Low-rank adapters of many sequences beside a shared projection (of pf_op_gemm, or a block of its columns):
+ *   out[m] = base[m] + scale[a] (x[m] A_a^T) B_a^T,  a = adapter_dev[b] of row m's sequence, -1: out[m] = base[m].
+ * x f16 [n_rows][K] (rows ldx apart), base and out f32 [n_rows][N] (ld_base, ld_out apart; out may be base itself
+ * with the same ld: the residual form, and rows without an adapter are then not touched), A f16 [n_adapters][rank][K], B f16
+ * [n_adapters][N][rank], scale f32 [n_adapters]. rank a multiple of 8 up to PF_MAX_RANK (adapters of lower rank:
+ * zero rows of A); K a multiple of 16, N of 8, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
+ * aligned. Products and sums in f32 (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
+ * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. batch: row_begin only; sequences of
+ * up to 8192 rows. scratch_dev: 16-B aligned, pf_adapters_scratch_bytes(n_rows, rank) bytes, zero before
+ * the first call and left zero by calls that complete; not shared by calls that overlap. */
+size_t pf_adapters_scratch_bytes(int32_t n_rows, int32_t rank);
+pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x_f16_dev, int64_t ldx, const float* base_dev, int64_t ld_base,
+                         float* out_dev, int64_t ld_out, int32_t K, int32_t N, int32_t rank, int32_t n_adapters,
+                         const int32_t* adapter_dev, const uint16_t* a_f16_dev, const uint16_t* b_f16_dev,
+                         const float* scale_dev, void* scratch_dev, size_t scratch_bytes, int32_t* status_dev, void* stream);
 /* Host RoPE table [max_seq][hd/2][2] = (cos, sin)(p * theta^(-2i/hd)), computed in
  * double and rounded to f32. */
 pf_status pf_rope_table_host(float theta, int32_t head_dim, int32_t max_seq, float* dst_host);

@@ -855,6 +855,9 @@ pf_status pf_timeline_set(uint64_t* buffer, int64_t capacity) {
   PF_CUDA(timeline_set_attention_kv8(b), "timeline");
   PF_CUDA(timeline_set_attention_kv8_tc(b), "timeline");
   PF_CUDA(timeline_set_logprobs(b), "timeline");
+  PF_CUDA(timeline_set_batch(b), "timeline");
+  PF_CUDA(timeline_set_attention_tree(b), "timeline");
+  PF_CUDA(timeline_set_adapters(b), "timeline");
   return PF_OK;
 }
 
@@ -873,6 +876,11 @@ const char* pf_timeline_kernel_name(int32_t id) {
       n[TL_GEMM_SMALL + e] = std::string("gemm_small_") + epi[e];
       n[TL_GEMV + e] = std::string("gemv_") + epi[e];
     }
+    n[TL_BATCH_APPEND] = "batch_append";
+    n[TL_TREE_ACCEPT] = "tree_accept";
+    n[TL_ATTENTION_TREE] = "attention_tree";
+    n[TL_ADAPTER_DOWN] = "adapter_down";
+    n[TL_ADAPTER_UP] = "adapter_up";
     return n;
   }();
   if (id < 1 || id >= 64 || names[id].empty()) return nullptr;
@@ -1447,6 +1455,114 @@ pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32
 }
 
 }  // extern "C"
+
+// What every call over a batch checks; `tree`: rows per sequence are bounded by PF_MAX_TREE.
+static pf_status check_batch_rows(const pf_batch* b, bool tree) {
+  if (!b) return fail(PF_ERR_INVALID_ARG, "batch is NULL");
+  if (b->n_seq < 1 || b->n_seq > PF_MAX_SEQS) return fail(PF_ERR_SHAPE, "n_seq %d: 1..%d", b->n_seq, PF_MAX_SEQS);
+  if (b->n_rows == 0) return fail(PF_ERR_EMPTY_CHUNK, "empty batch (n_rows = 0)");
+  if (b->n_rows < 0) return fail(PF_ERR_SHAPE, "n_rows %d", b->n_rows);
+  const int most = tree ? PF_MAX_TREE : 8192;
+  if (b->max_rows < 1 || b->max_rows > most) return fail(PF_ERR_SHAPE, "max_rows %d: 1..%d", b->max_rows, most);
+  if (!b->row_begin_dev) return fail(PF_ERR_INVALID_ARG, "row_begin is NULL");
+  return PF_OK;
+}
+
+// Calls over a batch that touch the caches.
+static pf_status check_batch(const pf_config* cfg, const pf_batch* b, int32_t layer, bool tree) {
+  PF_TRY(check_cfg(cfg));
+  if (cfg->ring_capacity > 0) return fail(PF_ERR_UNSUPPORTED, "batch calls: linear and paged caches only");
+  if (cfg->kv_dtype != PF_KV_BF16 && cfg->kv_dtype != PF_KV_F16)
+    return fail(PF_ERR_UNSUPPORTED, "batch calls: bf16 and f16 caches only (kv dtype %d)", cfg->kv_dtype);
+  PF_TRY(check_batch_rows(b, tree || (b && b->parent_dev != nullptr)));
+  if (cfg->max_seq > (1 << 30)) return fail(PF_ERR_SHAPE, "max_seq %d: at most 2^30", cfg->max_seq);
+  if (static_cast<int64_t>(cfg->n_layers) * cfg->n_kv_heads * cache_slots(*cfg) > 0x7fffffff)
+    return fail(PF_ERR_SHAPE, "layers x kv heads x slots: below 2^31");
+  if (static_cast<int64_t>(b->n_rows) * (cfg->n_q_heads + 2 * cfg->n_kv_heads) > 0x7fffffff)
+    return fail(PF_ERR_SHAPE, "n_rows x heads: below 2^31");
+  if (layer < 0 || layer >= cfg->n_layers) return fail(PF_ERR_SHAPE, "layer %d of %d", layer, cfg->n_layers);
+  if (!b->start_dev) return fail(PF_ERR_INVALID_ARG, "start is NULL");
+  if ((cfg->kv_block_pool > 0) != (b->block_table_dev != nullptr))
+    return fail(PF_ERR_INVALID_ARG, cfg->kv_block_pool > 0 ? "a paged cache needs a block table" : "a linear cache takes no block table");
+  if (cfg->kv_block_pool == 0 && b->n_seq != 1)
+    return fail(PF_ERR_UNSUPPORTED, "a linear cache holds one sequence (n_seq %d): use a paged one", b->n_seq);
+  return PF_OK;
+}
+
+pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const float* qkv, const float* qn, const float* kn,
+                             const float* rope, int32_t layer, void* q, void* kc, void* vc, int32_t* status, void* stream) {
+  PF_TRY(check_batch(cfg, batch, layer, false));
+  if (!qkv || !rope || !q || !kc || !vc || (cfg->qk_norm && (!qn || !kn))) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(qkv) || !aligned16(rope) || !aligned16(q) || !aligned16(kc) || !aligned16(vc) ||
+      (cfg->qk_norm && (!aligned16(qn) || !aligned16(kn))))
+    return fail(PF_ERR_INVALID_ARG, "qkv, norms, RoPE table, q and caches must be 16-B aligned");
+  PF_CUDA(launch_batch_append(*cfg, *batch, qkv, qn, kn, rope, layer, q, kc, vc, status, static_cast<cudaStream_t>(stream)),
+          "batch append");
+  return PF_OK;
+}
+
+size_t pf_attention_tree_scratch_bytes(const pf_config* cfg, int32_t n_seq, int32_t max_rows) {
+  if (check_cfg(cfg) != PF_OK || n_seq < 1 || n_seq > PF_MAX_SEQS || max_rows < 1 || max_rows > PF_MAX_TREE) return 0;
+  return attention_tree_scratch_bytes(*cfg, n_seq, max_rows);
+}
+
+pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, const void* q, const void* kc, const void* vc,
+                               int32_t layer, uint16_t* out, void* scratch, size_t scratch_bytes, int32_t* status,
+                               void* stream) {
+  PF_TRY(check_batch(cfg, batch, layer, true));
+  if (!q || !kc || !vc || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out))
+    return fail(PF_ERR_INVALID_ARG, "q, caches and out must be 16-B aligned");
+  const size_t need = attention_tree_scratch_bytes(*cfg, batch->n_seq, batch->max_rows);
+  if (scratch_bytes < need || !scratch)
+    return fail(PF_ERR_WORKSPACE, "tree attention scratch %zu bytes, need %zu", scratch_bytes, need);
+  if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  TreeAttnArgs a{cfg, batch, q, kc, vc, layer, out, scratch, status};
+  PF_CUDA(launch_attention_tree(a, static_cast<cudaStream_t>(stream)), "tree attention");
+  return PF_OK;
+}
+
+pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const int32_t* tokens, const int32_t* ids,
+                            const int32_t* root, int32_t* path, int32_t* n_accepted, int32_t* next, void* kc, void* vc,
+                            int32_t* status, void* stream) {
+  PF_TRY(check_batch(cfg, batch, 0, true));
+  if (!tokens || !ids || !root || !path || !n_accepted || !next) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (next == root) return fail(PF_ERR_INVALID_ARG, "next must not be the root ids");
+  if (!kc != !vc) return fail(PF_ERR_INVALID_ARG, "both caches or none");
+  if (kc && (!aligned16(kc) || !aligned16(vc))) return fail(PF_ERR_INVALID_ARG, "caches must be 16-B aligned");
+  PF_CUDA(launch_tree_accept(*cfg, *batch, tokens, ids, root, path, n_accepted, next, kc, vc, status,
+                             static_cast<cudaStream_t>(stream)),
+          "tree accept");
+  return PF_OK;
+}
+
+size_t pf_adapters_scratch_bytes(int32_t n_rows, int32_t rank) {
+  if (n_rows < 1 || rank < 8 || rank > PF_MAX_RANK || rank % 8) return 0;
+  return adapters_scratch_bytes(n_rows, rank);
+}
+
+pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, const float* base, int64_t ld_base, float* out,
+                         int64_t ld_out, int32_t K, int32_t N, int32_t rank, int32_t n_adapters, const int32_t* adapter,
+                         const uint16_t* wa, const uint16_t* wb, const float* scale, void* scratch, size_t scratch_bytes,
+                         int32_t* status, void* stream) {
+  PF_TRY(check_batch_rows(batch, false));
+  if (rank < 8 || rank > PF_MAX_RANK || rank % 8) return fail(PF_ERR_SHAPE, "rank %d: a multiple of 8 up to %d", rank, PF_MAX_RANK);
+  if (K < 16 || K % 16 || N < 8 || N % 8) return fail(PF_ERR_SHAPE, "K %d: a multiple of 16; N %d: of 8", K, N);
+  if (n_adapters < 1) return fail(PF_ERR_SHAPE, "n_adapters %d", n_adapters);
+  if (ldx < K || ldx % 8 || ld_base < N || ld_base % 4 || ld_out < N || ld_out % 4)
+    return fail(PF_ERR_SHAPE, "ldx %lld: at least K, a multiple of 8; ld_base %lld, ld_out %lld: at least N, multiples of 4",
+                (long long)ldx, (long long)ld_base, (long long)ld_out);
+  if (!x || !base || !out || !adapter || !wa || !wb || !scale) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(wa) || !aligned16(wb))
+    return fail(PF_ERR_INVALID_ARG, "x, base, out, A and B must be 16-B aligned");
+  if (base == out && ld_base != ld_out) return fail(PF_ERR_SHAPE, "out = base needs ld_out = ld_base");
+  const size_t need = adapters_scratch_bytes(batch->n_rows, rank);
+  if (scratch_bytes < need || !scratch) return fail(PF_ERR_WORKSPACE, "adapters scratch %zu bytes, need %zu", scratch_bytes, need);
+  if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  AdapterArgs a{batch, x, ldx, base, ld_base, out, ld_out, K, N, rank, n_adapters, adapter, wa, wb, scale, scratch, status};
+  PF_CUDA(launch_adapters(a, static_cast<cudaStream_t>(stream)), "adapters");
+  return PF_OK;
+}
 
 pf_status pf_streamk_plan_host(int32_t n_mt, int32_t n_nt, int32_t kbt, int32_t ctas, int32_t late_units,
                                int32_t late_kb, int64_t* begins, int32_t* segs, int32_t max_segs,

@@ -240,6 +240,70 @@ struct LogprobsArgs {
 };
 cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------------------------ many sequences at once (batch.cu, attention_tree*.cu, adapters.cu)
+// A pf_batch with what the kernels need of the configuration (device pointers).
+struct BatchDev {
+  int n_seq, n_rows, max_rows;
+  int max_seq;  // positions a sequence may have
+  int slots;    // per (layer, kv head)
+  int pages;    // entries of a sequence's block table
+  int pool;     // physical blocks (0: linear cache)
+  const int* row_begin;
+  const int* start;
+  const int* parent;
+  const int* table;
+};
+inline BatchDev batch_dev(const pf_config& c, const pf_batch& b) {
+  BatchDev d{};
+  d.n_seq = b.n_seq;
+  d.n_rows = b.n_rows;
+  d.max_rows = b.max_rows;
+  d.max_seq = c.max_seq;
+  d.slots = cache_slots(c);
+  d.pages = block_table_entries(c);
+  d.pool = c.kv_block_pool;
+  d.row_begin = b.row_begin_dev;
+  d.start = b.start_dev;
+  d.parent = b.parent_dev;
+  d.table = b.block_table_dev;
+  return d;
+}
+cudaError_t launch_batch_append(const pf_config& c, const pf_batch& b, const float* qkv, const float* qn, const float* kn,
+                                const float* rope, int layer, void* q, void* kc, void* vc, int* status, cudaStream_t stream);
+cudaError_t launch_tree_accept(const pf_config& c, const pf_batch& b, const int* tokens, const int* ids, const int* root, int* path,
+                               int* n_accepted, int* next, void* kc, void* vc, int* status, cudaStream_t stream);
+struct TreeAttnArgs {
+  const pf_config* c;
+  const pf_batch* b;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  int layer;
+  void* out;
+  void* scratch;  // attention_tree_scratch_bytes(c, n_seq, max_rows) bytes
+  int* status;
+};
+size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows);
+cudaError_t launch_attention_tree(const TreeAttnArgs& a, cudaStream_t stream);
+struct AdapterArgs {
+  const pf_batch* b;
+  const void* x;
+  int64_t ldx;
+  const float* base;
+  int64_t ld_base;
+  float* out;
+  int64_t ld_out;
+  int K, N, rank, n_adapters;
+  const int* adapter;
+  const void* wa;
+  const void* wb;
+  const float* scale;
+  void* scratch;
+  int* status;
+};
+size_t adapters_scratch_bytes(int n_rows, int rank);
+cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t stream);
+
 cudaError_t launch_embed(const float* E, const int* tokens, int M, int H, int vocab, float* x,
                          int* status, cudaStream_t stream);
 cudaError_t launch_lm_head(int wfmt, const float* x_row, const float* norm_w, float eps,
@@ -317,7 +381,8 @@ enum TimelineId : int {
   TL_KV8_STORE = 15, TL_KV8_LOAD = 16, TL_ATTENTION_KV8 = 17, TL_LOGPROBS = 18, TL_ATTENTION_KV8_TC = 19,
   TL_GEMM = 20,        // + epilogue (0 store, 1 residual, 2 SwiGLU) + 3 for the CTA-pair form
   TL_GEMM_SMALL = 30,  // + epilogue
-  TL_GEMV = 40         // + epilogue
+  TL_GEMV = 40,        // + epilogue
+  TL_BATCH_APPEND = 50, TL_TREE_ACCEPT = 51, TL_ATTENTION_TREE = 52, TL_ADAPTER_DOWN = 55, TL_ADAPTER_UP = 56
 };
 // Per translation unit: points its kernels' timeline buffer at `buf` (NULL: off).
 cudaError_t timeline_set_kernels(unsigned long long* buf);
@@ -329,6 +394,9 @@ cudaError_t timeline_set_attention_tc(unsigned long long* buf);
 cudaError_t timeline_set_kv8(unsigned long long* buf);
 cudaError_t timeline_set_attention_kv8(unsigned long long* buf);
 cudaError_t timeline_set_logprobs(unsigned long long* buf);
+cudaError_t timeline_set_batch(unsigned long long* buf);
+cudaError_t timeline_set_attention_tree(unsigned long long* buf);
+cudaError_t timeline_set_adapters(unsigned long long* buf);
 
 int device_sm_count();
 // Tiled tensor map over a 16-bit (bf16 if `bf16`, else f16) array of `rank` dims

@@ -50,6 +50,9 @@ class pf_config(ctypes.Structure):
 KV_BLOCK = 128  # PF_KV_BLOCK: positions per paged KV block
 KV8_BLOCK = 32  # PF_KV8_BLOCK: slots that share one scale in an 8-bit cache
 MAX_TOP = 32    # PF_MAX_TOP: most alternatives per row of pf_op_logprobs
+MAX_SEQS = 1024  # PF_MAX_SEQS: most sequences of a batch
+MAX_TREE = 256   # PF_MAX_TREE: most rows of one sequence with a tree
+MAX_RANK = 128   # PF_MAX_RANK: largest adapter rank
 
 
 class pf_layer_weights(ctypes.Structure):
@@ -61,6 +64,12 @@ class pf_model(ctypes.Structure):
     _fields_ = [("cfg", pf_config), ("layers", ctypes.POINTER(pf_layer_weights)),
                 ("embed", ctypes.c_void_p), ("final_norm", ctypes.c_void_p),
                 ("lm_head", ctypes.c_void_p)]
+
+
+class pf_batch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("row_begin_dev", ctypes.c_void_p), ("start_dev", ctypes.c_void_p),
+                ("parent_dev", ctypes.c_void_p), ("block_table_dev", ctypes.c_void_p)]
 
 
 _VP, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -121,6 +130,16 @@ _SIGS = {
     "pf_attention_kv8_scratch_bytes": ([ctypes.POINTER(pf_config), _I32], _SZ),
     "pf_op_attention_kv8": ([ctypes.POINTER(pf_config), _VP, _VP, _VP, _I32, _I32, _I32, _VP, _VP, _VP, _SZ, _VP,
                              _VP], _I32),
+    "pf_op_batch_append": ([ctypes.POINTER(pf_config), ctypes.POINTER(pf_batch), _VP, _VP, _VP, _VP, _I32, _VP, _VP,
+                            _VP, _VP, _VP], _I32),
+    "pf_attention_tree_scratch_bytes": ([ctypes.POINTER(pf_config), _I32, _I32], _SZ),
+    "pf_op_attention_tree": ([ctypes.POINTER(pf_config), ctypes.POINTER(pf_batch), _VP, _VP, _VP, _I32, _VP, _VP, _SZ,
+                              _VP, _VP], _I32),
+    "pf_op_tree_accept": ([ctypes.POINTER(pf_config), ctypes.POINTER(pf_batch), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                           _VP, _VP], _I32),
+    "pf_adapters_scratch_bytes": ([_I32, _I32], _SZ),
+    "pf_op_adapters": ([ctypes.POINTER(pf_batch), _VP, _I64, _VP, _I64, _VP, _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP,
+                        _VP, _VP, _SZ, _VP, _VP], _I32),
     "pf_status_read": ([_VP, _VP], _I32),
     "pf_selftest_bounded_wait": ([_VP, _I64, _I32, _VP], _I32),
 }
@@ -422,6 +441,137 @@ def pf_op_logprobs(logits, rows, n, ld, tokens, logprobs, entropy=None, top=0, t
                                _dense(entropy, dev, "float32", "entropy", rows, True), top,
                                _dense(top_ids, dev, "int32", "top_ids", rows * top, True),
                                _dense(top_logprobs, dev, "float32", "top_logprobs", rows * top, True),
+                               _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
+
+
+class Batch:
+    """The rows of a step over many sequences (pf_batch): row_begin int32 [n_seq + 1] on the device, start int32 [n_seq],
+    parent int32 [n_rows] (None: chains), blocks int32 [n_seq, pages] (paged caches). n_rows: rows that the row arrays
+    hold; max_rows: most rows of one sequence. The tensors' contents may change from step to step; the tensors
+    themselves are kept alive here and checked here, once."""
+
+    def __init__(self, row_begin, n_rows: int, max_rows: int, start=None, parent=None, blocks=None):
+        self.device = dev = _here()
+        if row_begin is None or row_begin.dim() != 1 or row_begin.shape[0] < 2:
+            raise PfError(1, "row_begin: need int32 [n_seq + 1]")
+        n_seq = row_begin.shape[0] - 1
+        if blocks is not None and (blocks.dim() != 2 or blocks.shape[0] != n_seq):
+            raise PfError(1, f"blocks: need int32 [{n_seq}, pages], got {tuple(blocks.shape)}")
+        self.pages = 0 if blocks is None else blocks.shape[1]
+        self.keep = (row_begin, start, parent, blocks)
+        self.n_seq, self.n_rows = n_seq, n_rows
+        self.c = pf_batch(n_seq=n_seq, n_rows=n_rows, max_rows=max_rows,
+                          row_begin_dev=_dense(row_begin, dev, "int32", "row_begin", n_seq + 1),
+                          start_dev=_dense(start, dev, "int32", "start", n_seq, True),
+                          parent_dev=_dense(parent, dev, "int32", "parent", n_rows, True),
+                          block_table_dev=_dense(blocks, dev, "int32", "blocks", n_seq, True))
+        self.ref = ctypes.byref(self.c)
+
+
+def _batch(batch, dev: int, cfg=None):
+    """The batch's struct for a call on CUDA device `dev` (with a configuration: over its caches)."""
+    if batch.device != dev:
+        raise PfError(1, f"the batch is on cuda:{batch.device}, not on the current CUDA device")
+    if cfg is not None and cfg.kv_block_pool > 0 and batch.pages and batch.pages != -(-cfg.max_seq // KV_BLOCK):
+        raise PfError(1, f"blocks: need {-(-cfg.max_seq // KV_BLOCK)} entries a sequence, got {batch.pages}")
+    return batch.ref
+
+
+def _cache16(cfg, dev: int, t, what: str) -> Optional[int]:
+    """Address of a 16-bit cache buffer of the configuration's type."""
+    slots = cfg.kv_block_pool * KV_BLOCK if cfg.kv_block_pool > 0 else cfg.max_seq
+    return _dense(t, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), what, cfg.n_layers * cfg.n_kv_heads * slots * cfg.head_dim)
+
+
+def pf_op_batch_append(cfg, batch, qkv, qn, kn, rope, layer, q, k_cache, v_cache, status=None, stream=None):
+    """QK-norm, RoPE and KV store of every sequence's rows: qkv f32 [n_rows, (nq + 2 nkv) hd], q of the cache's type
+    [n_rows, nq, hd], rope f32 [max_seq, hd / 2, 2] on the device (pf_rope_table_host)."""
+    dev, n, hd = _here(), batch.n_rows, cfg.head_dim
+    check(lib().pf_op_batch_append(ctypes.byref(cfg), _batch(batch, dev, cfg),
+                                   _dense(qkv, dev, "float32", "qkv", n * (cfg.n_q_heads + 2 * cfg.n_kv_heads) * hd),
+                                   _dense(qn, dev, "float32", "q_norm", hd, True), _dense(kn, dev, "float32", "k_norm", hd, True),
+                                   _dense(rope, dev, "float32", "rope", cfg.max_seq * hd), layer,
+                                   _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n * cfg.n_q_heads * hd),
+                                   _cache16(cfg, dev, k_cache, "K cache"), _cache16(cfg, dev, v_cache, "V cache"),
+                                   _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
+
+
+def pf_attention_tree_scratch_bytes(cfg, n_seq, max_rows):
+    return lib().pf_attention_tree_scratch_bytes(ctypes.byref(cfg), n_seq, max_rows)
+
+
+def attention_tree_scratch(cfg, n_seq, max_rows, device="cuda"):
+    """Zeroed scratch (uint8 tensor) for pf_op_attention_tree on up to n_seq sequences of up to max_rows rows."""
+    import torch
+    check(lib().pf_config_check(ctypes.byref(cfg)))
+    n = pf_attention_tree_scratch_bytes(cfg, n_seq, max_rows)
+    if n == 0:
+        raise PfError(2, f"n_seq {n_seq}: 1..{MAX_SEQS}; max_rows {max_rows}: 1..{MAX_TREE}")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def pf_op_attention_tree(cfg, batch, q, k_cache, v_cache, layer, out, scratch, status=None, stream=None):
+    """Attention of every sequence's rows over the cache: q of the cache's type [n_rows, nq, hd], out f16 [n_rows, nq * hd]."""
+    dev = _here()
+    n = batch.n_rows * cfg.n_q_heads * cfg.head_dim
+    check(lib().pf_op_attention_tree(ctypes.byref(cfg), _batch(batch, dev, cfg),
+                                     _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n),
+                                     _cache16(cfg, dev, k_cache, "K cache"), _cache16(cfg, dev, v_cache, "V cache"), layer,
+                                     _dense(out, dev, "float16", "out", n), _dense(scratch, dev, "uint8", "scratch", 0),
+                                     scratch.numel(), _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
+
+
+def pf_op_tree_accept(cfg, batch, tokens, ids, root_ids, path, n_accepted, next_ids, k_cache=None, v_cache=None, status=None,
+                      stream=None):
+    """Greedy acceptance of each sequence's tree (int32: tokens, ids, path [n_rows]; root_ids, n_accepted, next_ids
+    [n_seq]); the accepted nodes' K and V move up in every layer of the caches (None: nothing is moved)."""
+    dev, n, b = _here(), batch.n_rows, batch.n_seq
+    check(lib().pf_op_tree_accept(ctypes.byref(cfg), _batch(batch, dev, cfg), _dense(tokens, dev, "int32", "tokens", n),
+                                  _dense(ids, dev, "int32", "ids", n), _dense(root_ids, dev, "int32", "root_ids", b),
+                                  _dense(path, dev, "int32", "path", n), _dense(n_accepted, dev, "int32", "n_accepted", b),
+                                  _dense(next_ids, dev, "int32", "next_ids", b),
+                                  None if k_cache is None else _cache16(cfg, dev, k_cache, "K cache"),
+                                  None if v_cache is None else _cache16(cfg, dev, v_cache, "V cache"),
+                                  _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
+
+
+def adapters_scratch(n_rows, rank, device="cuda"):
+    """Zeroed scratch (uint8 tensor) for pf_op_adapters on up to n_rows rows with adapters of this rank."""
+    import torch
+    n = lib().pf_adapters_scratch_bytes(n_rows, rank)
+    if n == 0:
+        raise PfError(2, f"n_rows {n_rows}: at least 1; rank {rank}: a multiple of 8 up to {MAX_RANK}")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _strided(t, dev: int, dtype: str, what: str, rows: int):
+    """(address, elements between rows) of rows [>= rows, width] with contiguous elements."""
+    if t is None or t.dim() != 2 or t.shape[0] < rows:
+        raise PfError(1, f"{what}: need {dtype} [{rows}, width], got {None if t is None else tuple(t.shape)}")
+    st = t.stride()
+    if t.get_device() != dev or t.dtype is not getattr(_torch, dtype) or (st[1] != 1 and t.shape[1] != 1):
+        raise PfError(1, f"{what}: need {dtype} rows with contiguous elements on the current CUDA device, got {t.dtype} "
+                         f"of strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if rows > 1 else -(-t.shape[1] // 8) * 8
+
+
+def pf_op_adapters(batch, x, base, out, adapter, a, b, scale, scratch, status=None, stream=None):
+    """out[m] = base[m] + scale[i] (x[m] A_i^T) B_i^T with i = adapter[sequence of m], -1: none. x f16 [n_rows, K], base and
+    out f32 [n_rows, N] (views of wider rows; out may be base), a f16 [adapters, rank, K], b f16 [adapters, N, rank],
+    scale f32 [adapters], adapter int32 [n_seq]."""
+    dev = _here()
+    if a is None or b is None or a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+        raise PfError(1, "A: need f16 [adapters, rank, K], B: f16 [adapters, N, rank]")
+    (count, rank, k), n = a.shape, b.shape[1]
+    xp, ldx = _strided(x, dev, "float16", "x", batch.n_rows)
+    bp, ldb = _strided(base, dev, "float32", "base", batch.n_rows)
+    op, ldo = _strided(out, dev, "float32", "out", batch.n_rows)
+    if x.shape[1] != k or base.shape[1] != n or out.shape[1] != n:
+        raise PfError(1, f"widths: x {x.shape[1]} and A {k}, base {base.shape[1]}, out {out.shape[1]} and B {n}")
+    check(lib().pf_op_adapters(_batch(batch, dev), xp, ldx, bp, ldb, op, ldo, k, n, rank, count,
+                               _dense(adapter, dev, "int32", "adapter", batch.n_seq), _dense(a, dev, "float16", "A", count * rank * k),
+                               _dense(b, dev, "float16", "B", count * n * rank), _dense(scale, dev, "float32", "scale", count),
+                               _dense(scratch, dev, "uint8", "scratch", 0), scratch.numel(),
                                _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 

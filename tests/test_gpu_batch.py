@@ -1,0 +1,537 @@
+"""Calls over many sequences on the GPU: append, tree attention, acceptance and adapters against their definitions
+in float64, numbers in device memory that are out of range, a whole layer of several requests."""
+import dataclasses
+
+import numpy as np
+import pytest
+
+import batch_reference as R
+from quantized_transformer_prefill_q1_gb300 import pf, synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+class Step:
+    """A batch over a cache with NaN in every slot that no sequence holds."""
+
+    def __init__(self, kind, nq, nkv, hd, rows, start, paged=True, parents=None, norm=False, n_layers=2, layer=1, seed=0, spare=3):
+        self.rng = rng = np.random.default_rng(seed)
+        self.kind, self.dt, self.nq, self.nkv, self.hd, self.layer = kind, TYPES[kind], nq, nkv, hd, layer
+        self.rows, self.start, self.norm = list(rows), list(start), norm
+        self.begin = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        self.total = int(self.begin[-1])
+        self.n_rows = self.total + spare
+        self.max_seq = max(s + r for s, r in zip(start, rows)) + 5
+        self.pages = -(-self.max_seq // 128)
+        need = [-(-(s + r) // 128) for s, r in zip(start, rows)]
+        self.pool = sum(need) + 2 if paged else 0
+        shape = dataclasses.replace(synth.QWEN3_8B_LAYER, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, kv_dtype=kind, qk_norm=norm)
+        self.cfg = pf.make_config(shape, 256, n_layers=n_layers, max_seq=self.max_seq, kv_block_pool=self.pool)
+        self.slots = self.pool * 128 if paged else self.max_seq
+        self.parents = parents if parents is not None else [R.chain(n) for n in rows]
+        self.parent_dev = None if parents is None else ints(np.concatenate([*parents, [7] * spare]))
+        self.table = None
+        if paged:
+            order, at = rng.permutation(self.pool), 0
+            self.table = np.full((len(rows), self.pages), -1, np.int32)
+            for b, m in enumerate(need):
+                self.table[b, :m] = order[at:at + m]
+                at += m
+        self.table_dev = ints(self.table) if paged else None
+        self.begin_dev, self.start_dev = ints(self.begin), ints(self.start)
+        self.status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        self.k, self.v = (torch.full((n_layers, nkv, self.slots, hd), float("nan"), dtype=self.dt, device="cuda") for _ in "kv")
+        self.batch = self.make_batch()
+
+    def make_batch(self, max_rows=None):
+        return pf.Batch(self.begin_dev, n_rows=self.n_rows, max_rows=max_rows or max(1, *self.rows), start=self.start_dev,
+                        parent=self.parent_dev, blocks=self.table_dev)
+
+    def slot(self, b, p):
+        p = np.asarray(p)
+        return p if self.table is None else self.table[b][p // 128] * 128 + p % 128
+
+    def fill(self, own_rows=True, heavy=1.0):
+        """Cached positions (and the sequences' own rows) hold normal values."""
+        for b, n in enumerate(self.rows):
+            i = torch.from_numpy(np.asarray(self.slot(b, np.arange(self.start[b] + (n if own_rows else 0))), np.int64)).cuda()
+            for c in (self.k, self.v):
+                x = self.rng.standard_normal((c.shape[0], self.nkv, len(i), self.hd)) * (heavy if c is self.k else 1)
+                c[:, :, i] = torch.from_numpy(x).cuda().to(self.dt)
+
+    def held(self, c, b, layer=None):
+        """Sequence b's values of positions 0 .. start + rows - 1, float64 [nkv, positions, hd]."""
+        i = torch.from_numpy(np.asarray(self.slot(b, np.arange(self.start[b] + self.rows[b])), np.int64)).cuda()
+        return c[self.layer if layer is None else layer][:, i].double().cpu().numpy()
+
+    def scratch(self):
+        return pf.attention_tree_scratch(self.cfg, len(self.rows), max(1, *self.rows))
+
+    def q(self, scale=1.0):
+        return torch.from_numpy(self.rng.standard_normal((self.n_rows, self.nq, self.hd)) * scale).cuda().to(self.dt)
+
+    def attend(self, q, scratch=None):
+        out = torch.full((self.n_rows, self.nq * self.hd), 7.0, dtype=torch.float16, device="cuda")
+        pf.pf_op_attention_tree(self.cfg, self.batch, q, self.k, self.v, self.layer, out, self.scratch() if scratch is None else scratch,
+                                self.status)
+        return out
+
+    def check_attention(self, q, out):
+        got, qq = out.double().cpu().numpy().reshape(self.n_rows, self.nq, self.hd), q.double().cpu().numpy()
+        for b, n in enumerate(self.rows):
+            if n == 0:
+                continue
+            rows = slice(self.begin[b], self.begin[b + 1])
+            ref, bound = R.attention(qq[rows], self.held(self.k, b), self.held(self.v, b), self.start[b], self.parents[b], self.kind)
+            off = np.abs(got[rows] - ref)
+            assert (off <= bound).all(), (b, n, self.start[b], float((off / bound).max()), np.argwhere(~(off <= bound))[:3])
+        assert (got[self.total:] == 7).all()
+
+
+def trees(rng, rows):
+    return [R.random_tree(rng, n, roots=1 + (n > 5)) for n in rows]
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nkv,hd,norm", [(32, 8, 128, True), (4, 2, 64, True), (1, 1, 128, False), (64, 1, 64, False), (64, 8, 128, True)])
+@pytest.mark.parametrize("paged,tree", [(True, True), (True, False), (False, True)])
+def test_append(kind, nq, nkv, hd, norm, paged, tree):
+    rows, start = ([5, 0, 1, 40, 3, 130], [126, 9, 0, 250, 127, 1]) if paged else ([37], [11])
+    rng = np.random.default_rng(hd + nq)
+    s = Step(kind, nq, nkv, hd, rows, start, paged, trees(rng, rows) if tree else None, norm)
+    width = (nq + 2 * nkv) * hd
+    qkv = torch.from_numpy(rng.standard_normal((s.n_rows, width)) * 2).cuda().float()
+    qn, kn = ((1 + 0.1 * rng.standard_normal((2, hd))).astype(np.float32) if norm else (None, None))
+    qd, kd = (torch.from_numpy(x).cuda() if norm else None for x in (qn, kn))
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, hd, s.max_seq)).cuda()
+    q = torch.full((s.n_rows, nq, hd), 7.0, dtype=s.dt, device="cuda")
+    pf.pf_op_batch_append(s.cfg, s.batch, qkv, qd, kd, rope, s.layer, q, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    assert (q[s.total:] == 7).all()
+    want_k, want_v = (torch.full_like(c, float("nan")) for c in (s.k, s.v))
+    tiny = 2.0 ** -25 if kind == "f16" else 0.0
+    for b, n in enumerate(rows):
+        if n == 0:
+            continue
+        x = qkv[s.begin[b]:s.begin[b + 1]].cpu().numpy()
+        pos = start[b] + R.depths(s.parents[b])
+        rq, rk, rv, size = R.append(x, nq, nkv, hd, qn, kn, s.cfg.eps, s.cfg.rope_theta, pos)
+        i = torch.from_numpy(np.asarray(s.slot(b, start[b] + np.arange(n)), np.int64)).cuda()
+        got_q = q[s.begin[b]:s.begin[b + 1]].double().cpu().numpy()
+        got_k = s.k[s.layer][:, i].double().cpu().numpy().transpose(1, 0, 2)
+        # half a step of the type; f32: the norm (hd squares' sum, root, division, two products) and the rotation
+        # (table, two products, their sum) within 16 roundings of the products' sizes
+        for got, ref, sz in ((got_q, rq, size[:, :nq]), (got_k, rk, size[:, nq:])):
+            off = np.abs(got - ref)
+            bound = R.half_step(kind) * (np.abs(ref) + 16 * 2.0 ** -24 * sz) + 16 * 2.0 ** -24 * sz + tiny
+            assert (off <= bound).all(), (b, float((off - bound).max()))
+        want_k[s.layer][:, i] = s.k[s.layer][:, i]
+        want_v[s.layer][:, i] = torch.from_numpy(rv.transpose(1, 0, 2)).cuda().float().to(s.dt)
+    for got, want in ((s.k, want_k), (s.v, want_v)):
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nkv,hd", [(32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (64, 1, 64)])
+@pytest.mark.parametrize("top", [1, 3, 16, 64])
+def test_attention_ragged(kind, nq, nkv, hd, top):
+    """Sequences of none to `top` rows, lengths that end on, before and behind pages and tiles."""
+    rng = np.random.default_rng(top * 7 + hd + nq)
+    start = [0, 1, 31, 127, 128, 129, 300, 511, 640]
+    rows = [top, 1, max(1, top - 1), 1, top, 0, max(1, top // 2), top, 1]
+    s = Step(kind, nq, nkv, hd, rows, start, True, trees(rng, rows), seed=top)
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n,start,tree", [(1, 0, False), (1, 1000, False), (2, 2049, False), (26, 1021, True), (70, 130, False), (256, 100, True),
+                                          (256, 0, False)])
+def test_attention_linear(kind, n, start, tree):
+    rng = np.random.default_rng(n + start)
+    s = Step(kind, 8, 2, 128, [n], [start], False, [R.random_tree(rng, n)] if tree else None, seed=n)
+    s.fill()
+    q = s.q(2.0)
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("top", [1, 40])
+def test_attention_large_scores(kind, top):
+    """Scores of thousands: the running maximum rises and falls by hundreds; rows whose first tiles weigh nothing."""
+    rng = np.random.default_rng(5)
+    rows, start = [top, top, 1], [700, 5, 1500]
+    s = Step(kind, 8, 2, 128, rows, start, True, trees(rng, rows), seed=3)
+    s.fill(heavy=30.0)
+    q = s.q(10.0)
+    s.check_attention(q, s.attend(q))
+    pf.pf_status_read(s.status)
+
+
+def test_attention_deep_and_wide_trees():
+    """A chain given by parents, a star, all nodes under the cache, two of them in one batch."""
+    n = 256
+    parents = [R.chain(n), np.array([-1] + [0] * (n - 1), np.int32), np.full(n, -1, np.int32), np.arange(n, dtype=np.int32) // 2 - 1 + (np.arange(n) == 1)]
+    parents[3][0] = -1
+    for p in parents:
+        assert (p < np.arange(n)).all() and (p >= -1).all()
+    s = Step("f16", 4, 2, 64, [n] * 4, [3, 0, 130, 77], True, parents)
+    s.fill()
+    q = s.q()
+    s.check_attention(q, s.attend(q))
+    pf.pf_status_read(s.status)
+
+
+@pytest.mark.parametrize("top", [1, 64])
+def test_attention_repeats_and_streams(top):
+    """One scratch for call after call of other lengths, results equal bit for bit; a second stream; a captured call
+    whose lengths and tree change between replays."""
+    rng = np.random.default_rng(9)
+    rows, start = [top, max(1, top - 3), 1, top], [900, 40, 513, 1]  # every position that a replay below reads
+    s = Step("bf16", 32, 8, 128, rows, start, True, trees(rng, rows))
+    s.fill()
+    q, scratch = s.q(), s.scratch()
+    first = s.attend(q, scratch)
+    s.check_attention(q, first)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        again = s.attend(q, scratch)
+    other.synchronize()
+    assert torch.equal(first, again)
+    out = torch.full_like(first, 7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pf.pf_op_attention_tree(s.cfg, s.batch, q, s.k, s.v, s.layer, out, scratch, s.status)
+    graph.replay()
+    assert torch.equal(out, first)
+    # shorter rows and caches, other trees: the same addresses
+    s.rows = [max(1, top // 2), 0, 1, top]
+    s.start = [880, 41, 2, 1]
+    s.begin = np.concatenate([[0], np.cumsum(s.rows)]).astype(np.int32)
+    s.total = int(s.begin[-1])
+    s.parents = trees(rng, s.rows)
+    s.begin_dev.copy_(ints(s.begin))
+    s.start_dev.copy_(ints(s.start))
+    s.parent_dev[:s.total] = ints(np.concatenate(s.parents))
+    out.fill_(7.0)
+    graph.replay()
+    s.check_attention(q, out)
+    pf.pf_status_read(s.status)
+
+
+# ------------------------------------------------------------------ acceptance
+@pytest.mark.parametrize("kind,hd,paged", [("bf16", 128, True), ("f16", 64, True), ("f16", 128, False)])
+@pytest.mark.parametrize("tree", [True, False])
+def test_accept(kind, hd, paged, tree):
+    rng = np.random.default_rng(hd)
+    rows, start = ([1, 26, 0, 256, 61, 40], [5, 120, 3, 0, 127, 300]) if paged else ([33], [100])
+    s = Step(kind, 4, 2, hd, rows, start, paged, trees(rng, rows) if tree else None, n_layers=3)
+    for c in (s.k, s.v):
+        c.copy_(torch.from_numpy(rng.standard_normal(c.shape)).cuda())
+    before = s.k.clone(), s.v.clone()
+    tokens = rng.integers(0, 4, s.n_rows).astype(np.int32)  # few tokens: several children fit
+    ids = rng.integers(0, 4, s.n_rows).astype(np.int32)
+    root = rng.integers(0, 4, len(rows)).astype(np.int32)
+    for b, n in enumerate(rows):
+        if n:
+            root[b] = tokens[s.begin[b]]
+        for i in range(n):  # most ids lead on
+            kids = [j for j in range(n) if s.parents[b][j] == i]
+            if kids and rng.random() < 0.95:
+                ids[s.begin[b] + i] = tokens[s.begin[b] + kids[rng.integers(len(kids))]]
+    path, count, after = (torch.full((m,), 99, dtype=torch.int32, device="cuda") for m in (s.n_rows, len(rows), len(rows)))
+    pf.pf_op_tree_accept(s.cfg, s.batch, ints(tokens), ints(ids), ints(root), path, count, after, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    longest = 0
+    for b, n in enumerate(rows):
+        at = s.begin[b]
+        want, follow = R.accept(s.parents[b], tokens[at:at + n], ids[at:at + n], root[b])
+        assert path[at:at + n].tolist() == want + [-1] * (n - len(want))
+        assert int(count[b]) == len(want) and int(after[b]) == follow
+        longest = max(longest, len(want))
+        if want:
+            src = torch.from_numpy(np.asarray(s.slot(b, start[b] + np.array(want)), np.int64)).cuda()
+            dst = torch.from_numpy(np.asarray(s.slot(b, start[b] + np.arange(len(want))), np.int64)).cuda()
+            for old, now in zip(before, (s.k, s.v)):
+                moved = old[:, :, src].clone()
+                old[:, :, dst] = moved
+    assert longest > 2  # the inputs lead on
+    assert (path[s.total:] == 99).all()
+    for old, now in zip(before, (s.k, s.v)):
+        assert torch.equal(old, now)
+    # without caches: the same answer, nothing moved
+    p2, c2, a2 = (torch.full_like(t, 98) for t in (path, count, after))
+    pf.pf_op_tree_accept(s.cfg, s.batch, ints(tokens), ints(ids), ints(root), p2, c2, a2, status=s.status)
+    assert torch.equal(p2[:s.total], path[:s.total]) and torch.equal(c2, count) and torch.equal(a2, after)
+    assert torch.equal(before[0], s.k)
+
+
+# ------------------------------------------------------------------ adapters
+@pytest.mark.parametrize("k,n,rank", [(256, 128, 8), (4096, 512, 16), (272, 1000, 24), (1040, 264, 64), (512, 2056, 128), (16, 8, 8)])
+@pytest.mark.parametrize("top", [1, 5, 70, 300])
+def test_adapters(k, n, rank, top):
+    rng = np.random.default_rng(k + top)
+    rows = [top, 0, 1, max(1, top - 1), top, max(1, top // 3), 2 if top > 1 else 1]
+    which = np.array([1, 0, 2, -1, 1, 0, 3], np.int32)
+    begin = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    total, n_rows = int(begin[-1]), int(begin[-1]) + 2
+    batch = pf.Batch(ints(begin), n_rows=n_rows, max_rows=top if top > 1 else 1)
+    x = torch.from_numpy(rng.standard_normal((n_rows, k + 8))).cuda().half()[:, :k]
+    base = torch.from_numpy(rng.standard_normal((n_rows, n + 8))).cuda().float()[:, 4:n + 4]
+    a = torch.from_numpy(rng.standard_normal((4, rank, k)) * k ** -0.5).cuda().half()
+    b = torch.from_numpy(rng.standard_normal((4, n, rank)) * 0.1).cuda().half()
+    scale = torch.tensor([0.5, 2.0, 1.25, 16.0], device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    scratch = pf.adapters_scratch(n_rows, rank)
+    out = torch.full((n_rows, n), 7.0, device="cuda")
+    pf.pf_op_adapters(batch, x, base, out, ints(which), a, b, scale, scratch, status)
+    pf.pf_status_read(status)
+    got = out.double().cpu().numpy()
+    for i, w in enumerate(which):
+        rs = slice(begin[i], begin[i + 1])
+        bs = base[rs].cpu().numpy()
+        if w < 0:
+            assert np.array_equal(got[rs], bs.astype(np.float64))
+            continue
+        ref, bound = R.adapters(bs, x[rs].cpu().numpy(), a[w].cpu().numpy(), b[w].cpu().numpy(), float(scale[w]))
+        off = np.abs(got[rs] - ref)
+        assert (off <= bound).all(), (i, w, float((off / bound).max()))
+    assert (got[total:] == 7).all()
+    # in place over a block of wider rows: the same numbers, the columns beside it untouched
+    wide = torch.full((n_rows, n + 24), 3.0, device="cuda")
+    block = wide[:, 8:n + 8]
+    block.copy_(base)
+    pf.pf_op_adapters(batch, x, block, block, ints(which), a, b, scale, scratch, status)
+    assert torch.equal(block[:total], out[:total]) and torch.equal(block[total:], base[total:])
+    assert (wide[:, :8] == 3).all() and (wide[:, n + 8:] == 3).all()
+
+
+def test_adapters_range():
+    """Rows of 60,000s and of 1e-6: x A^T far beyond and below what an f16 holds."""
+    rng = np.random.default_rng(2)
+    k, n, rank = 2048, 256, 16
+    x = torch.ones(3, k, dtype=torch.float16, device="cuda") * torch.tensor([[60000.0], [1.0], [6e-8]], device="cuda").half()
+    a = torch.from_numpy(rng.standard_normal((1, rank, k)) * 8).cuda().half()
+    b = torch.from_numpy(rng.standard_normal((1, n, rank))).cuda().half()
+    scale, base = torch.ones(1, device="cuda"), torch.zeros(3, n, device="cuda")
+    out = torch.empty_like(base)
+    batch = pf.Batch(ints([0, 3]), n_rows=3, max_rows=3)
+    pf.pf_op_adapters(batch, x, base, out, ints([0]), a, b, scale, pf.adapters_scratch(3, rank))
+    ref, bound = R.adapters(base.cpu().numpy(), x.cpu().numpy(), a[0].cpu().numpy(), b[0].cpu().numpy(), 1.0)
+    off = np.abs(out.double().cpu().numpy() - ref)
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+# ------------------------------------------------------------------ numbers out of range
+def status_of(f):
+    with pytest.raises(pf.PfError) as e:
+        f()
+    return pf.STATUS[e.value.status]
+
+
+@pytest.mark.parametrize("top", [2, 40])
+def test_left_out_sequences(top):
+    """A sequence with impossible rows or start is recorded and left out; the others are as without it."""
+    rng = np.random.default_rng(4)
+    rows, start = [top, 1, top], [130, 60, 20]
+    for what, code in (("rows", "PF_ERR_SHAPE"), ("start", "PF_ERR_KV_CAPACITY"), ("negative", "PF_ERR_KV_CAPACITY"), ("far", "PF_ERR_KV_CAPACITY")):
+        s = Step("f16", 8, 2, 128, rows, start, True, trees(rng, rows))
+        s.fill()
+        q = s.q()
+        good = s.attend(q)
+        kc = s.k.clone()
+        if what == "rows":
+            s.begin_dev.copy_(ints([0, top, top - 1, 2 * top + 1]))  # the second falls; the third overlaps it and has too many
+        else:
+            s.start_dev[1] = {"start": s.max_seq, "negative": -1, "far": 2 ** 31 - 1}[what]
+        out = s.attend(q)
+        torch.cuda.synchronize()
+        assert status_of(lambda: pf.pf_status_read(s.status)) == code
+        assert torch.equal(out[:top], good[:top])
+        if what != "rows":
+            assert (out[top] == 7).all() and torch.equal(out[top + 1:], good[top + 1:])
+        else:
+            assert (out[top:] == 7).all()
+        # append and accept leave it out too
+        qkv = torch.randn(s.n_rows, 12 * 128, device="cuda")
+        rope = torch.from_numpy(pf.pf_rope_table_host(1e6, 128, s.max_seq)).cuda()
+        q2 = torch.full_like(q, 7.0)
+        pf.pf_op_batch_append(s.cfg, s.batch, qkv, None, None, rope, 0, q2, s.k, s.v, s.status)
+        assert status_of(lambda: pf.pf_status_read(s.status)) == code
+        assert (q2[top] == 7).all() and not (q2[:top] == 7).any()
+        assert torch.equal(s.k[1].view(torch.int16), kc[1].view(torch.int16))
+        path, count, after = (torch.full((m,), 99, dtype=torch.int32, device="cuda") for m in (s.n_rows, 3, 3))
+        one = torch.ones(s.n_rows, dtype=torch.int32, device="cuda")
+        pf.pf_op_tree_accept(s.cfg, s.batch, one, one, ints([1, 5, 1]), path, count, after, s.k, s.v, s.status)
+        assert status_of(lambda: pf.pf_status_read(s.status)) == code
+        assert count[1] == 0 and after[1] == 5 and path[top] == 99
+
+
+@pytest.mark.parametrize("top", [2, 40])
+def test_bad_parents_and_pages(top):
+    rng = np.random.default_rng(4)
+    rows, start = [top, 1, top], [130, 60, 20]
+    s = Step("f16", 8, 2, 128, rows, start, True, trees(rng, rows))
+    s.fill()
+    q = s.q()
+    # a parent that is no earlier node is the cache
+    for bad in (top - 1, top, -2, 2 ** 31 - 1, -2 ** 31):
+        p = [x.copy() for x in s.parents]
+        p[0][top - 1] = -1
+        s.parent_dev[:s.total] = ints(np.concatenate(p))
+        want = s.attend(q)
+        pf.pf_status_read(s.status)
+        s.parent_dev[top - 1] = bad
+        got = s.attend(q)
+        assert status_of(lambda: pf.pf_status_read(s.status)) == "PF_ERR_INVALID_ARG"
+        assert torch.equal(got, want)
+    s.parent_dev[:s.total] = ints(np.concatenate(s.parents))
+    # a page outside the pool: not written, read as any block, the other sequences unharmed
+    want = s.attend(q)
+    pf.pf_status_read(s.status)
+    for bad in (-1, s.pool, 2 ** 31 - 1, -2 ** 31):
+        s.table_dev[0, 1] = bad
+        got = s.attend(q)
+        assert status_of(lambda: pf.pf_status_read(s.status)) == "PF_ERR_KV_CAPACITY"
+        assert torch.equal(got[top:], want[top:])
+        before = s.k.clone()
+        qkv = torch.randn(s.n_rows, 12 * 128, device="cuda")
+        rope = torch.from_numpy(pf.pf_rope_table_host(1e6, 128, s.max_seq)).cuda()
+        pf.pf_op_batch_append(s.cfg, s.batch, qkv, None, None, rope, 0, torch.empty_like(q), s.k, s.v, s.status)
+        assert status_of(lambda: pf.pf_status_read(s.status)) == "PF_ERR_KV_CAPACITY"
+        changed = (s.k.view(torch.int16) != before.view(torch.int16)).any(-1)
+        mine = {int(s.slot(b, start[b] + i)) for b in (1, 2) for i in range(rows[b])}
+        assert not changed[1].any() and {int(x) for x in changed[0].nonzero()[:, 1]} <= mine
+
+
+def test_bad_adapters():
+    batch = pf.Batch(ints([0, 2, 3]), n_rows=3, max_rows=2)
+    x, base = torch.randn(3, 64, device="cuda").half(), torch.randn(3, 32, device="cuda")
+    a, b = torch.randn(2, 8, 64, device="cuda").half(), torch.randn(2, 32, 8, device="cuda").half()
+    scale, scratch, status = torch.ones(2, device="cuda"), pf.adapters_scratch(3, 8), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in (2, -2, 2 ** 31 - 1, -2 ** 31):
+        out = torch.full_like(base, 7.0)
+        pf.pf_op_adapters(batch, x, base, out, ints([bad, 1]), a, b, scale, scratch, status)
+        assert status_of(lambda: pf.pf_status_read(status)) == "PF_ERR_INVALID_ARG"
+        assert torch.equal(out[:2], base[:2]) and not torch.equal(out[2], base[2])
+
+
+# ------------------------------------------------------------------ together
+def test_layer_of_several_requests():
+    """What a layer's attention block does for five requests with trees and adapters: projection, adapters, append, attention,
+    output projection with the residual and its adapters; then the accepted paths move up and the next step reads them."""
+    rng = np.random.default_rng(17)
+    shape = dataclasses.replace(synth.QWEN3_8B_LAYER, hidden=512, intermediate=512, n_q_heads=8, n_kv_heads=2, head_dim=64, kv_dtype="f16")
+    nq, nkv, hd, h = 8, 2, 64, 512
+    rows, start = [7, 1, 30, 12, 20], [0, 200, 127, 60, 310]
+    s = Step("f16", nq, nkv, hd, rows, start, True, trees(rng, rows), norm=True, n_layers=1, layer=0, spare=0)
+    s.fill(own_rows=False)
+    width = (nq + 2 * nkv) * hd
+    w = {name: synth.q1_weight(rng, n, k) for name, n, k in (("qkv", width, h), ("o", h, nq * hd))}
+    dense = {}
+    packed = {}
+    for name, t in w.items():
+        sign = np.unpackbits(t["bits"], axis=1, bitorder="little").astype(np.float64) * 2 - 1
+        dense[name] = sign * np.repeat(t["scales"].astype(np.float64), 128, 1)
+        packed[name] = torch.from_numpy(pf.pf_pack_weights_host(t)).cuda()
+    x = torch.from_numpy(rng.standard_normal((s.total, h))).cuda().float()
+    norm_w = torch.ones(h, device="cuda")
+    qn, kn = (1 + 0.1 * rng.standard_normal((2, hd))).astype(np.float32)
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, hd, s.max_seq)).cuda()
+    which = np.array([0, -1, 1, 0, 1], np.int32)
+    ad = {name: (torch.from_numpy(rng.standard_normal((2, 16, k)) * k ** -0.5).cuda().half(), torch.from_numpy(rng.standard_normal((2, n, 16)) * 0.3).cuda().half())
+          for name, n, k in (("q", nq * hd, h), ("v", nkv * hd, h), ("o", h, nq * hd))}
+    scale = torch.tensor([1.0, 2.0], device="cuda")
+    y, qkv = torch.empty(s.total, h, dtype=torch.float16, device="cuda"), torch.empty(s.total, width, device="cuda")
+    q, attn = torch.empty(s.total, nq, hd, dtype=torch.float16, device="cuda"), torch.empty(s.total, nq * hd, dtype=torch.float16, device="cuda")
+    out, qn_dev, kn_dev = x.clone(), torch.from_numpy(qn).cuda(), torch.from_numpy(kn).cuda()
+    gs, ls = pf.gemm_scratch(s.total, max(width, h)), pf.adapters_scratch(s.total, 16)
+    scratch, which_dev = s.scratch(), ints(which)
+
+    def step():
+        pf.pf_op_rmsnorm(x, norm_w, 1e-6, y)
+        pf.pf_op_gemm(pf.W_Q1, pf.EPI_STORE_F32, y, packed["qkv"], s.total, width, h, qkv, gs, status=s.status)
+        for name, lo, hi in (("q", 0, nq * hd), ("v", (nq + nkv) * hd, width)):
+            pf.pf_op_adapters(s.batch, y, qkv[:, lo:hi], qkv[:, lo:hi], which_dev, *ad[name], scale, ls, s.status)
+        pf.pf_op_batch_append(s.cfg, s.batch, qkv, qn_dev, kn_dev, rope, 0, q, s.k, s.v, s.status)
+        pf.pf_op_attention_tree(s.cfg, s.batch, q, s.k, s.v, 0, attn, scratch, s.status)
+        pf.pf_op_gemm(pf.W_Q1, pf.EPI_RESID_ADD, attn, packed["o"], s.total, h, nq * hd, out, gs, status=s.status)
+        pf.pf_op_adapters(s.batch, attn, out, out, which_dev, *ad["o"], scale, ls, s.status)
+
+    step()
+    pf.pf_status_read(s.status)
+
+    def lora(name, i, v):
+        a, b = (t[i].double().cpu().numpy() for t in ad[name])
+        return float(scale[i]) * (v @ a.T) @ b.T
+
+    xn = x.double().cpu().numpy()
+    ref = np.empty((s.total, h))
+    kv = {}
+    for b, n in enumerate(rows):
+        xr = xn[s.begin[b]:s.begin[b + 1]]
+        yr = xr / np.sqrt((xr * xr).mean(1, keepdims=True) + 1e-6)
+        p = yr @ dense["qkv"].T
+        if which[b] >= 0:
+            p[:, :nq * hd] += lora("q", which[b], yr)
+            p[:, (nq + nkv) * hd:] += lora("v", which[b], yr)
+        rq, rk, rv, _ = R.append(p, nq, nkv, hd, qn, kn, s.cfg.eps, s.cfg.rope_theta, start[b] + R.depths(s.parents[b]))
+        k, v = s.held(s.k, b), s.held(s.v, b)
+        k[:, start[b]:], v[:, start[b]:] = rk.transpose(1, 0, 2), rv.transpose(1, 0, 2)
+        kv[b] = k, v
+        o = R.attention(rq, k, v, start[b], s.parents[b], "f16")[0].reshape(n, nq * hd)
+        r = xr + o @ dense["o"].T
+        ref[s.begin[b]:s.begin[b + 1]] = r + (lora("o", which[b], o) if which[b] >= 0 else 0)
+    got = out.double().cpu().numpy()
+    off = np.linalg.norm(got - ref, axis=1) / np.linalg.norm(ref, axis=1)
+    assert off.max() < 5e-3, off  # f16 operands throughout: about ten roundings of 2^-11
+
+    # the whole step captured and replayed
+    out.copy_(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    out.copy_(x)
+    graph.replay()
+    got2 = out.double().cpu().numpy()
+    assert (np.linalg.norm(got2 - ref, axis=1) / np.linalg.norm(ref, axis=1)).max() < 5e-3
+
+    # acceptance, then one more token on the accepted positions
+    tokens = rng.integers(0, 50, s.total).astype(np.int32)
+    ids = rng.integers(0, 50, s.total).astype(np.int32)
+    root = np.array([tokens[s.begin[b]] for b in range(5)], np.int32)
+    for b, n in enumerate(rows):
+        for i in range(n):
+            kids = [j for j in range(n) if s.parents[b][j] == i]
+            if kids:
+                ids[s.begin[b] + i] = tokens[s.begin[b] + kids[-1]]
+    path, count, after = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (s.total, 5, 5))
+    pf.pf_op_tree_accept(s.cfg, s.batch, ints(tokens), ints(ids), ints(root), path, count, after, s.k, s.v, s.status)
+    new_start = s.start_dev + count
+    one = pf.Batch(ints(np.arange(6)), n_rows=5, max_rows=1, start=new_start - 1, blocks=s.table_dev)  # each path's last node again
+    q1 = torch.stack([q[s.begin[b] + int(path[s.begin[b] + int(count[b]) - 1])] for b in range(5)])
+    o1 = torch.empty(5, nq * hd, dtype=torch.float16, device="cuda")
+    pf.pf_op_attention_tree(s.cfg, one, q1, s.k, s.v, 0, o1, pf.attention_tree_scratch(s.cfg, 5, 1), s.status)
+    pf.pf_status_read(s.status)
+    for b in range(5):
+        node = int(path[s.begin[b] + int(count[b]) - 1])
+        d = (o1[b].double() - attn[s.begin[b] + node].double()).abs().max()
+        assert float(d) <= 2.0 ** -9 * float(attn[s.begin[b] + node].double().abs().max()), (b, float(d))
