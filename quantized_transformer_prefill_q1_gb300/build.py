@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libpf.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["pf_host.cu", "gemm_q.cu", "gemm_small.cu", "gemv.cu", "attention.cu", "attention_tc.cu", "kernels.cu",
            "kv8.cu", "attention_kv8.cu", "attention_kv8_tc.cu", "logprobs.cu", "batch.cu",
-           "attention_tree.cu", "adapters.cu"]
+           "attention_tree.cu", "attention_tree_tc.cu", "adapters.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -1,107 +1,512 @@
-// attention_tree.cu — attention of many sequences' rows (trees of drafted tokens, single tokens) over the cache.
+// attention_tree.cu — attention of many sequences' rows (trees of drafted tokens, single tokens) over the cache,
+// few rows per kv head; more rows go to attention_tree_tc.cu.
 //
 // For row i of a sequence and its head h (kv head h / G) over the keys j that it sees (the cached positions, its
 // ancestors, itself): s_j = q . k_j / sqrt(hd), p = softmax_j(s), o = sum_j p_j v_j.
+//
+// The cache is read once and nothing else weighs, so the kernel streams it: all (sequence, kv head) tasks in one
+// line of units of 32 keys, cut evenly over the CTAs whatever the lengths are (batch.cuh). The units go round
+// the CTA's 4 warps in turn, each through its own ring of TMA stages that it refills itself, across task borders, so
+// that the copies never wait for a task's end, with its own running maximum m, sum l and O. At a task's end the
+// warps meet in shared memory; a task that lies in one CTA is done, parts of a cut one meet in scratch, where the CTA
+// that completes the task's count merges them.
+//
+// The rows of one kv head (row = node * G + head in the group, at most 8 NB) are the n side of warp-level MMAs
+// m16n8k16: S^T [keys x rows] = K [16 keys x 16 d] Q^T and O^T [d x rows] += V^T [16 d x 16 keys] P^T, K and V as A
+// operands by ldmatrix (V transposed on the way); P^T comes from S^T by a register transpose (movmatrix).
+// The running maximum is raised only when exceeded by more than 2^8.
+//
+// Rounding: P to the cache's type (what the product with V takes), the output to f16; all else f32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "batch.cuh"
 
 namespace pf {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int UK = 32;  // keys per unit
+constexpr float RESCALE_LOG2 = 8.f;
+constexpr int FEW_ROWS = 16;  // most rows per kv head of this form
 
-__device__ __forceinline__ float2 pair(__half2 x) { return __half22float2(x); }
-__device__ __forceinline__ float2 pair(__nv_bfloat162 x) { return __bfloat1622float2(x); }
+template <int HD, int NB>
+struct FSmem {
+  static constexpr int WS = HD == 64 ? 6 : 3;  // stages of a warp's ring: 192 KB in flight an SM
+  static constexpr int NS = WARPS * WS;
+  static constexpr int TILE = UK * HD * 2;                       // bytes of a K or V unit
+  static constexpr int RING = NS * 2 * TILE;
+  static constexpr int ROWS = 8 * NB;
+  static constexpr int OW = HD + 4;  // floats between rows of the warps' O
+  static constexpr int MERGE = WARPS * ROWS * (OW + 2) * 4;
+  static constexpr int BYTES = 1024 + RING + MERGE + NS * 8;
+  static_assert(BYTES <= 232448 - 384, "shared memory");  // beside the static arrays
+};
 
-// One CTA per (row, sequence, kv head), a warp per query head, keys one after the other.
-template <int HD, typename T2>
-__global__ void __launch_bounds__(THREADS) tree_rows_kernel(const BatchDev B, const T2* __restrict__ q, const T2* __restrict__ kc,
-                                                            const T2* __restrict__ vc, int nq, int nkv, int layer, float scale,
-                                                            __half* __restrict__ out, int* status) {
-  PF_TIMELINE(TL_ATTENTION_TREE);
-  constexpr int PER = HD / 64;  // pairs of elements a lane
-  __shared__ uint32_t see[PF_MAX_TREE / 32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int i = blockIdx.x, b = blockIdx.y, kvh = blockIdx.z;
-  const int G = nq / nkv, lane = threadIdx.x & 31;
-  const SeqRows s = batch_seq(B, b, true);
-  if (s.err != PF_OK && threadIdx.x == 0) batch_record(status, s.err);
-  if (i >= s.n) return;
-  if (threadIdx.x < PF_MAX_TREE / 32) see[threadIdx.x] = 0;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int j = i; j >= 0;) {
-      see[j >> 5] |= 1u << (j & 31);
-      bool bad = false;
-      const int p = B.parent != nullptr ? tree_parent(B.parent + s.at, j, bad) : j - 1;
-      if (bad) batch_record(status, PF_ERR_INVALID_ARG);
-      j = p;
-    }
+struct FewParams {
+  BatchDev B;
+  const uint16_t* q;
+  int nq, nkv, layer;
+  float scale_log2;
+  __half* out;
+  int* counters;  // one per (sequence, kv head)
+  float* part;    // two places a CTA: [rows][HD], then (m, l) per row
+  int* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  __syncthreads();
-  const size_t head = (static_cast<size_t>(layer) * nkv + kvh) * B.slots;
-  for (int h = kvh * G + (threadIdx.x >> 5); h < (kvh + 1) * G; h += THREADS / 32) {
-    float2 x[PER], o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      x[e] = pair(q[(static_cast<size_t>(s.at + i) * nq + h) * (HD / 2) + lane + 32 * e]);
-      o[e] = make_float2(0.f, 0.f);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// 16-byte chunk `chunk` of key `row` in a unit: boxes of 64 elements (128-byte rows, chunk ^ row % 8)
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int chunk) {
+  return tile + (chunk >> 3) * (UK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+template <int HD, int BF16, int NB>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_tree_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const FewParams P) {
+  PF_TIMELINE(TL_ATTENTION_TREE);
+  using L = FSmem<HD, NB>;
+  constexpr int KS = HD / 16, DT = HD / 16, NH = HD / 64, ROWS = L::ROWS, NS = L::NS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_s, last_s;
+  __shared__ int issued_s[NS];  // copies that each stage has taken (its own warp's lane 0 counts)
+  volatile int* abort_flag = &abort_s;
+  const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
+  float* os = reinterpret_cast<float*>(smem_raw + (ring - raw) + L::RING);  // the warps' O [warp][row][OW], then (m, l)
+  float2* mls = reinterpret_cast<float2*>(os + WARPS * ROWS * L::OW);
+  const uint32_t bars = ring + L::RING + L::MERGE;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const BatchDev& B = P.B;
+  const int G = P.nq / P.nkv;
+  griddep_launch_dependents();
+  if (threadIdx.x < NS) {
+    mbar_init(bars + 8 * threadIdx.x, 1);
+    issued_s[threadIdx.x] = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (threadIdx.x == 0) abort_s = 0;
+  griddep_wait();
+  auto work = [&](const SeqRows& s) -> SeqWork { return {P.nkv, s.n > 0 ? (s.start + s.n + UK - 1) / UK : 0}; };
+  // every CTA has a unit for each warp, as far as the work goes
+  auto ctas_of = [&](long long total) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (total + WARPS - 1) / WARPS)); };
+  const WorkStart ws = batch_scan<THREADS>(
+      B, work, [&](long long total) { return range_begin(total, blockIdx.x, max(1, ctas_of(total))); }, nullptr, P.status);
+  const int ctas = ctas_of(ws.total), cta = blockIdx.x;
+  if (cta >= ctas) return;
+  const long long ub = range_begin(ws.total, cta, ctas);
+  const long long count = range_begin(ws.total, cta + 1, ctas) - ub;
+
+  WorkCursor<decltype(work)> cur, iss;
+  cur.seek(B, work, ws.b, ub - ws.first);
+  // the warp's next copy: its place in the line, as a row of the cache (-1: none)
+  iss = cur;
+  long long iu = warp;  // unit of the range
+  int irow = 0;
+  auto locate = [&]() {
+    int slot = batch_slot(B, iss.b, iss.u * UK);
+    if (slot < 0) {
+      if (lane == 0) batch_record(P.status, PF_ERR_KV_CAPACITY);
+      slot = 0;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int p = 0; p <= s.start + i; ++p) {
-      const int j = p - s.start;
-      if (j >= 0 && !(see[j >> 5] >> (j & 31) & 1u)) continue;
-      int slot = batch_slot(B, b, p);
-      if (slot < 0) {
-        if (lane == 0) batch_record(status, PF_ERR_KV_CAPACITY);
-        slot = 0;
-      }
-      const size_t at = (head + slot) * (HD / 2) + lane;
-      float d = 0.f;
+    irow = (P.layer * P.nkv + iss.task) * B.slots + slot;
+  };
+  auto issue = [&](int st) {
+    if (lane == 0) {
+      const uint32_t dst = ring + st * (2 * L::TILE), bar = bars + 8 * st;
+      ++issued_s[st];
+      mbar_arrive_expect_tx(bar, 2 * L::TILE);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const float2 k = pair(kc[at + 32 * e]);
-        d = fmaf(x[e].x, k.x, fmaf(x[e].y, k.y, d));
-      }
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-      d *= scale;
-      const float mn = fmaxf(m, d), a = expf(m - mn), e2 = expf(d - mn);
-      m = mn;
-      l = l * a + e2;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const float2 v = pair(vc[at + 32 * e]);
-        o[e].x = o[e].x * a + e2 * v.x;
-        o[e].y = o[e].y * a + e2 * v.y;
+      for (int h = 0; h < NH; ++h) {
+        tma_load_2d(dst + h * (UK * 128), &tm_k, 64 * h, irow, bar);
+        tma_load_2d(dst + L::TILE + h * (UK * 128), &tm_v, 64 * h, irow, bar);
       }
     }
-    __half2* dst = reinterpret_cast<__half2*>(out) + (static_cast<size_t>(s.at + i) * nq + h) * (HD / 2) + lane;
+  };
+  auto ahead = [&](int d) {  // to the warp's next copy
+    iu += d;
+    if (iu < count) {
+      iss.advance(B, work, d);
+      locate();
+    }
+  };
+  if (iu < count) {
+    iss.advance(B, work, warp);
+    locate();
+  }
+#pragma unroll 1
+  for (int y = 0; y < L::WS; ++y) {
+    if (iu < count) issue(warp * L::WS + y);
+    ahead(WARPS);
+  }
+
+  const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;   // ldmatrix address of K: keys x chunks
+  const int vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;  // of V (transposed)
+  long long x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
+  int st = 0, ph = 0;         // the latter's stage of the warp's ring, and phase
+  bool failed = false;
+  while (x < count) {
+    const int u0 = cur.u, cnt = static_cast<int>(min(static_cast<long long>(cur.w.units - u0), count - x));
+    const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
+    float o[NB][DT][4], m[NB][2], l[NB][2];
+    uint32_t qf[NB][KS][2];  // Q^T as the B operand: row 8 b + g
 #pragma unroll
-    for (int e = 0; e < PER; ++e) dst[32 * e] = __floats2half2_rn(o[e].x / l, o[e].y / l);
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[b][d][e] = 0.f;
+      m[b][0] = m[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+      const int r = 8 * b + g;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(P.q + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD) + t;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qf[b][k][e] = r < R ? src[8 * k + 4 * e] : 0u;
+    }
+    uint32_t see[NB][2];  // nodes that the lane's rows (columns 2t, 2t + 1 of each block of 8) see
+    bool have_see = false;
+    for (; i < x + cnt && !failed; i += WARPS) {
+      const int unit = u0 + static_cast<int>(i - x), key0 = unit * UK;
+      const int stage = warp * L::WS + st;
+      const uint32_t kt = ring + stage * (2 * L::TILE), vt = kt + L::TILE;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, ph, abort_flag))) {
+        failed = true;
+        break;
+      }
+      const bool tail = key0 + UK > start;
+      if (key0 + UK > len) {  // values behind the sequence may be anything: a zero weight must not meet a NaN
+        for (int y = lane; y < UK * (HD / 8); y += 32) {
+          const int row = y / (HD / 8);
+          if (key0 + row >= len)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk_at(vt, row, y % (HD / 8))), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();  // before the copy that refills the stage
+        __syncwarp();
+      }
+      if (tail && !have_see) {
+        have_see = true;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * b + 2 * t + e, node = r / G;
+            see[b][e] = 0;
+            if (r >= R) continue;
+            if (B.parent == nullptr) {
+              see[b][e] = (2u << node) - 1u;
+            } else {
+              for (int j = node; j >= 0;) {
+                bool bad;
+                see[b][e] |= 1u << j;
+                j = tree_parent(B.parent + at, j, bad);
+                if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
+              }
+            }
+          }
+      }
+      // scores of 32 keys: two tiles of 16
+      float sc[NB][2][4];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[b][mt][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t a[4];
+          ldsm4(a, chunk_at(kt, 16 * mt + krow, 2 * k + kch));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<BF16>(sc[b][mt], a, qf[b][k][0], qf[b][k][1]);
+        }
+      if (tail) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = key0 + 16 * mt + 8 * (e >> 1) + g - start;  // node of the key
+              if (j >= 0 && (j >= n || !(see[b][e & 1] >> j & 1u))) sc[b][mt][e] = -INFINITY;
+            }
+      }
+      float mx[NB][2];
+      bool raise = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[b][e] = fmaxf(fmaxf(sc[b][0][e], sc[b][0][e + 2]), fmaxf(sc[b][1][e], sc[b][1][e + 2])) * P.scale_log2;
+          raise |= mx[b][e] > m[b][e] + RESCALE_LOG2;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = mx[b][e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+            const float mn = fmaxf(m[b][e], y);
+            const float alpha = mn == -INFINITY ? 1.f : ex2(m[b][e] - mn);
+            m[b][e] = mn;
+            l[b][e] *= alpha;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              o[b][d][e] *= alpha;
+              o[b][d][e + 2] *= alpha;
+            }
+          }
+      }
+      uint32_t pf[NB][2][2];  // P^T as the B operand: [16-key tile][register]
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float n0 = m[b][0] == -INFINITY ? 0.f : -m[b][0], n1 = m[b][1] == -INFINITY ? 0.f : -m[b][1];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float p0 = ex2(fmaf(sc[b][mt][2 * hh], P.scale_log2, n0)), p1 = ex2(fmaf(sc[b][mt][2 * hh + 1], P.scale_log2, n1));
+            l[b][0] += p0;
+            l[b][1] += p1;
+            pf[b][mt][hh] = transpose8x8(pack2<BF16>(p0, p1));
+          }
+      }
+#pragma unroll
+      for (int kt2 = 0; kt2 < 2; ++kt2)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint32_t a[4];
+          ldsm4_t(a, chunk_at(vt, 16 * kt2 + vrow, 2 * d + vch));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<BF16>(o[b][d], a, pf[b][kt2][0], pf[b][kt2][1]);
+        }
+      __syncwarp();  // every lane has read the stage
+      if (iu < count) {
+        issue(stage);
+        ahead(WARPS);
+      }
+      if (++st == L::WS) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    // the warps' parts of this task meet
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * b + 2 * t + e;
+        float y = l[b][e];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+        if (g == 0) mls[warp * ROWS + r] = make_float2(m[b][e], y);
+        float* dst = os + (warp * ROWS + r) * L::OW + g;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          dst[16 * d] = o[b][d][e];
+          dst[16 * d + 8] = o[b][d][e + 2];
+        }
+      }
+    failed = __syncthreads_or(failed) != 0;
+    if (failed) break;
+    constexpr int LPR = HD / 4;  // threads per row, four columns each
+    const int col = (threadIdx.x % LPR) * 4;
+    auto store_out = [&](int r, float4 v, float f) {
+      const __half2 a = __floats2half2_rn(v.x * f, v.y * f), c = __floats2half2_rn(v.z * f, v.w * f);
+      *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD + col) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+    };
+    const bool whole = cnt == cur.w.units;
+    const long long task_first = ub + x - u0;
+    constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
+    float* mine = P.part + part_place(ws.total, cta, ctas, task_first) * PLACE;
+    for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
+      float mw[WARPS], mr = -INFINITY, lr = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        mw[w] = mls[w * ROWS + r].x;
+        mr = fmaxf(mr, mw[w]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float a = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - mr);
+        const float4 v = *reinterpret_cast<const float4*>(os + (w * ROWS + r) * L::OW + col);
+        lr = fmaf(a, mls[w * ROWS + r].y, lr);
+        acc = make_float4(fmaf(a, v.x, acc.x), fmaf(a, v.y, acc.y), fmaf(a, v.z, acc.z), fmaf(a, v.w, acc.w));
+      }
+      if (whole) {
+        store_out(r, acc, 1.f / lr);
+      } else {
+        *reinterpret_cast<float4*>(mine + r * HD + col) = acc;
+        if (col == 0) reinterpret_cast<float2*>(mine + ROWS * HD)[r] = make_float2(mr, lr);
+      }
+    }
+    if (!whole) {
+      const int c0 = range_owner(ws.total, task_first, ctas), c1 = range_owner(ws.total, task_first + cur.w.units - 1, ctas);
+      int* ctr = P.counters + cur.b * P.nkv + kvh;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) last_s = atomicAdd(ctr, 1) == c1 - c0;
+      __syncthreads();
+      if (last_s) {
+        __threadfence();
+        // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c
+        for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float mr = -INFINITY, lr = 0.f;
+          for (int c = c0; c <= c1; c += 8) {
+            float4 v[8];
+            float2 ml[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const float* src = P.part + part_place(ws.total, min(c + y, c1), ctas, task_first) * PLACE;
+              v[y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
+              ml[y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              if (c + y > c1) break;
+              const float mn = fmaxf(mr, ml[y].x);
+              const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ml[y].x == -INFINITY ? 0.f : ex2(ml[y].x - mn);
+              mr = mn;
+              lr = lr * a + f * ml[y].y;
+              acc = make_float4(acc.x * a + f * v[y].x, acc.y * a + f * v[y].y, acc.z * a + f * v[y].z, acc.w * a + f * v[y].w);
+            }
+          }
+          store_out(r, acc, 1.f / lr);
+        }
+        if (threadIdx.x == 0) *ctr = 0;  // every part is in: ready for the next call
+      }
+    }
+    x += cnt;
+    if (x < count) cur.advance(B, work, cnt);
+    __syncthreads();  // the merge area is free
+  }
+  if (failed) {
+    __syncthreads();
+    // let the copies in flight land before shared memory is released
+    if (threadIdx.x < NS && issued_s[threadIdx.x] > 0) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bars + 8 * threadIdx.x, (issued_s[threadIdx.x] - 1) & 1) && global_timer_ns() - t0 < PF_WAIT_LIMIT_NS) {}
+    }
+    if (threadIdx.x == 0) batch_record(P.status, PF_ERR_DEVICE_TIMEOUT);
   }
 }
 
-template <int HD, typename T2>
-cudaError_t launch_rows(const TreeAttnArgs& a, cudaStream_t stream) {
+
+template <int HD, int BF16, int NB>
+cudaError_t launch_few(const TreeAttnArgs& a, cudaStream_t stream) {
+  using L = FSmem<HD, NB>;
   const pf_config& c = *a.c;
-  return launch_pdl(tree_rows_kernel<HD, T2>, dim3(a.b->max_rows, a.b->n_seq, c.n_kv_heads), dim3(THREADS), 0, stream,
-                    batch_dev(c, *a.b), static_cast<const T2*>(a.q), static_cast<const T2*>(a.k_cache),
-                    static_cast<const T2*>(a.v_cache), c.n_q_heads, c.n_kv_heads, a.layer, 1.f / sqrtf(static_cast<float>(HD)),
-                    static_cast<__half*>(a.out), a.status);
+  const int slots = cache_slots(c);
+  const uint64_t dims[2] = {HD, static_cast<uint64_t>(c.n_layers) * c.n_kv_heads * slots}, strides[1] = {HD * 2};
+  const uint32_t box[2] = {64, UK};
+  CUtensorMap tk, tv;
+  if (!encode_tmap_16(&tk, BF16, 2, a.k_cache, dims, strides, box) || !encode_tmap_16(&tv, BF16, 2, a.v_cache, dims, strides, box))
+    return cudaErrorInvalidValue;
+  FewParams p{};
+  p.B = batch_dev(c, *a.b);
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.nq = c.n_q_heads;
+  p.nkv = c.n_kv_heads;
+  p.layer = a.layer;
+  p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
+  p.out = static_cast<__half*>(a.out);
+  p.counters = static_cast<int*>(a.scratch);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c));
+  p.status = a.status;
+  const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
+  return launch_pdl(attn_tree_few_kernel<HD, BF16, NB>, dim3(ctas), dim3(THREADS), L::BYTES, stream, tk, tv, p);
+}
+
+template <int HD, int BF16>
+cudaError_t launch_rows(const TreeAttnArgs& a, cudaStream_t stream) {
+  const int R = std::min(a.b->max_rows, a.b->n_rows) * (a.c->n_q_heads / a.c->n_kv_heads);
+  if (R <= 8) return launch_few<HD, BF16, 1>(a, stream);
+  if (R <= FEW_ROWS) return launch_few<HD, BF16, 2>(a, stream);
+  return launch_attention_tree_tc(a, stream);
+}
+
+template <int HD, int BF16>
+cudaError_t set_attr_few() {
+  const cudaError_t e = cudaFuncSetAttribute(attn_tree_few_kernel<HD, BF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<HD, 1>::BYTES);
+  const cudaError_t f = cudaFuncSetAttribute(attn_tree_few_kernel<HD, BF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<HD, 2>::BYTES);
+  return e != cudaSuccess ? e : f;
 }
 
 }  // namespace
 
-size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows) { return 256; }
+size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows) {
+  // either form: a call with fewer rows than max_rows may take the other
+  const int rows = std::min(FEW_ROWS, (max_rows * (c.n_q_heads / c.n_kv_heads) + 7) / 8 * 8);
+  const size_t few = tree_counter_bytes(c) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * rows * (c.head_dim + 2) * sizeof(float);
+  return std::max(few, attention_tree_tc_scratch_bytes(c, n_seq, max_rows));
+}
+
+cudaError_t prepare_attention_tree_kernels() {
+  cudaError_t e = cudaSuccess, r;
+  if ((r = set_attr_few<128, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr_few<128, 0>()) != cudaSuccess) e = r;
+  if ((r = set_attr_few<64, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr_few<64, 0>()) != cudaSuccess) e = r;
+  return e;
+}
 
 cudaError_t launch_attention_tree(const TreeAttnArgs& a, cudaStream_t stream) {
   const bool bf = a.c->kv_dtype == PF_KV_BF16;
-  if (a.c->head_dim == 128) return bf ? launch_rows<128, __nv_bfloat162>(a, stream) : launch_rows<128, __half2>(a, stream);
-  return bf ? launch_rows<64, __nv_bfloat162>(a, stream) : launch_rows<64, __half2>(a, stream);
+  if (a.c->head_dim == 128) return bf ? launch_rows<128, 1>(a, stream) : launch_rows<128, 0>(a, stream);
+  return bf ? launch_rows<64, 1>(a, stream) : launch_rows<64, 0>(a, stream);
 }
 
 }  // namespace pf

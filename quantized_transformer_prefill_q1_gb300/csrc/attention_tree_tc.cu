@@ -1,0 +1,680 @@
+// attention_tree_tc.cu — attention of many sequences' rows (trees of drafted tokens) over the cache on the
+// 5th-generation tensor cores, for more rows per kv head than attention_tree.cu takes.
+//
+// The rows of one sequence and kv head (row = node * G + head in the group) in blocks of 256 are a task; its key
+// units are tiles of 128 positions (a page). All tasks lie in one line, cut evenly over persistent CTAs whatever the
+// lengths are (batch.cuh). A CTA holds two slots, each with 128 rows in the MMA's M side, its own S / P and O in tensor
+// memory and 128 softmax threads, one a row: while one slot's softmax runs, the other's products do.
+//   more than 128 rows: slot s takes rows 128 s .. +127 of every tile: K and V are read once for 256 rows;
+//   128 rows or fewer:  both slots hold the same rows and take the tiles in turn; at the end slot 1's
+//                       (m, l, O) join slot 0's through shared memory.
+//
+// Warp roles:
+//   warp 0      TMA: Q (3-D map over q[rows][nq][hd]), K and V tiles into one ring in the order the products need them,
+//               across task borders (the next task's first tiles come before its Q);
+//   warp 1      the MMAs, one elected lane issuing: S = Q K^T, O += P V with P from tensor memory over S's columns, V
+//               MN-major as it lies in the cache. Products run in the order of issue, so the next S of a slot follows the
+//               product that reads its P without a wait;
+//   warps 2..5  softmax of slot 0 (tensor memory lane quarter = warp % 4), warps 6..9 of slot 1: a thread reads its row's
+//               128 scores, hides the keys that the row does not see, exponentials in the exp2 domain, P back; the
+//               running maximum is raised only when exceeded by more than 2^8 (then O is scaled in tensor memory).
+// A task that lies in one CTA is written by it; parts of a cut one go to scratch as f32 and a second kernel merges
+// them, a thread per row and eight columns.
+//
+// Rounding: P to the cache's type (the product's operand), the output to f16; all else f32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "batch.cuh"
+
+namespace pf {
+namespace {
+
+constexpr int TM = 128;      // rows of a slot
+constexpr int BLOCK = 256;   // rows of a task
+constexpr int TK = 128;      // keys per tile
+constexpr int THREADS = 320;
+constexpr int SM_THREADS = 256;
+constexpr float RESCALE_LOG2 = 8.f;
+static_assert(TK == PF_KV_BLOCK, "a key tile is a page");
+
+template <int HD>
+struct TSmem {
+  static constexpr int QT = TM * HD * 2;   // a slot's Q
+  static constexpr int KV = TK * HD * 2;   // a K or V tile
+  static constexpr int NS = HD == 128 ? 5 : 10;
+  static constexpr int BYTES = 1024 + 2 * QT + NS * KV + 512;
+  static_assert(BYTES <= 232448 - TM * 8 - 256, "shared memory");  // beside the static arrays
+};
+
+struct TcParams {
+  BatchDev B;
+  int nq, nkv, layer;
+  float scale_log2;
+  __half* out;
+  long long* plan;  // [0] total units, [1] CTAs, then the first unit of every sequence
+  float* part;      // two places a CTA: [HD / 4][rows] float4, then (m, l) per row
+  int part_rows;
+  int* status;
+};
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < PF_WAIT_LIMIT_NS) {}
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ bool bar_and(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Bits [0, n) set (n clamped to [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// A CTA's part of a task, as every role sees it.
+struct Part {
+  int kvh, rb, at, n, start;  // kv head, row block, the sequence's rows and start
+  int rows;                   // rows of the task (of this block)
+  int slots;                  // 2: the slots share the rows; 1: they share the tiles
+  int u0, cnt;                // key tiles
+};
+
+template <int HD, int BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const TcParams P) {
+  PF_TIMELINE(TL_ATTENTION_TREE_TC);
+  using L = TSmem<HD>;
+  constexpr int NH = HD / 64, NS = L::NS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_s;
+  __shared__ float2 ml_s[TM];  // slot 1's (m, l)
+  volatile int* abort_flag = &abort_s;
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t q_s = base, kv_s = q_s + 2 * L::QT, bar0 = kv_s + NS * L::KV;
+  float* xbuf = reinterpret_cast<float*>(smem_raw + (base - raw) + L::QT);  // slot 1's Q, idle where the slots share the rows
+  auto kv_full = [&](int s) { return bar0 + 8u * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (NS + s); };
+  auto s_full = [&](int s) { return bar0 + 8u * (2 * NS + s); };
+  auto p_full = [&](int s) { return bar0 + 8u * (2 * NS + 2 + s); };
+  auto o_done = [&](int s) { return bar0 + 8u * (2 * NS + 4 + s); };
+  auto o_empty = [&](int s) { return bar0 + 8u * (2 * NS + 6 + s); };
+  const uint32_t q_full = bar0 + 8u * (2 * NS + 8), q_empty = q_full + 8, drain_bar = q_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (q_full + 24 - raw));
+  static_assert(8 * (2 * NS + 12) <= 512, "barrier area");
+  const BatchDev& B = P.B;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = P.nq / P.nkv;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), TM);
+      mbar_init(o_done(s), 1);
+      mbar_init(o_empty(s), TM);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(drain_bar, 1);
+    abort_s = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  auto work = [&](const SeqRows& s) -> SeqWork {
+    return {P.nkv * ((s.n * G + BLOCK - 1) / BLOCK), s.n > 0 ? (s.start + s.n + TK - 1) / TK : 0};
+  };
+  // a tile for each slot, as far as the work goes
+  auto ctas_of = [&](long long total) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 1) / 2)); };
+  const int cta = blockIdx.x;
+  const WorkStart ws = batch_scan<THREADS>(
+      B, work, [&](long long total) { return range_begin(total, cta, max(1, ctas_of(total))); }, cta == 0 ? P.plan + 2 : nullptr,
+      P.status);
+  const int ctas = ctas_of(ws.total);
+  if (cta == 0 && threadIdx.x == 0) {
+    P.plan[0] = ws.total;
+    P.plan[1] = ctas;
+  }
+  const long long ub = range_begin(ws.total, cta, max(1, ctas));
+  const long long count = cta < ctas ? range_begin(ws.total, cta + 1, ctas) - ub : 0;
+  WorkCursor<decltype(work)> cur;
+  if (count > 0) cur.seek(B, work, ws.b, ub - ws.first);
+  // the part of the task at the cursor that lies in this CTA's range, x units of which are done
+  auto part = [&](long long x) -> Part {
+    Part p;
+    const int blocks = cur.w.tasks / P.nkv;
+    p.kvh = cur.task / blocks;
+    p.rb = cur.task - p.kvh * blocks;
+    p.at = cur.s.at;
+    p.n = cur.s.n;
+    p.start = cur.s.start;
+    p.rows = min(BLOCK, p.n * G - p.rb * BLOCK);
+    p.slots = p.rows > TM ? 2 : 1;
+    p.u0 = cur.u;
+    p.cnt = static_cast<int>(min(static_cast<long long>(cur.w.units - cur.u), count - x));
+    return p;
+  };
+  // Order of a part's tiles in the ring: slots == 2: K0 V0 K1 V1 ..; slots == 1: K0 K1 V0 K2 V1 .. (the other
+  // slot's scores come before the first slot's product).
+  auto place_k = [](const Part& p, int j) { return p.slots == 2 ? 2 * j : max(0, 2 * j - 1); };
+  auto place_v = [](const Part& p, int j) { return p.slots == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.cnt - 1); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      int c = 0, seg = 0, last_slots = 0, q_issued = 0;
+      bool ok = true;
+      for (long long x = 0; x < count && ok; ++seg) {
+        const Part p = part(x);
+        const int row0 = (P.layer * P.nkv + p.kvh) * B.slots;
+        auto tile_row = [&](int j) {
+          int slot = batch_slot(B, cur.b, (p.u0 + j) * TK);
+          if (slot < 0) {
+            batch_record(P.status, PF_ERR_KV_CAPACITY);
+            slot = 0;
+          }
+          return row0 + slot;
+        };
+        auto load = [&](const CUtensorMap* map, int row) {
+          const int s = c % NS;
+          if (!mbar_wait(kv_empty(s), ((c / NS) & 1) ^ 1, abort_flag)) return false;
+          mbar_arrive_expect_tx(kv_full(s), L::KV);
+          for (int h = 0; h < NH; ++h) tma_load_2d(kv_s + s * L::KV + h * (TK * 128), map, h * 64, row, kv_full(s));
+          ++c;
+          return true;
+        };
+        auto load_q = [&]() {
+          if (seg > 0 && !mbar_wait(q_empty, (seg - 1) & 1, abort_flag)) return false;
+          // slot 1's Q may still be the exchange buffer of the part before
+          if (seg > 0 && p.slots == 2 && last_slots == 1 &&
+              !(mbar_wait(o_empty(0), (seg - 1) & 1, abort_flag) && mbar_wait(o_empty(1), (seg - 1) & 1, abort_flag)))
+            return false;
+          mbar_arrive_expect_tx(q_full, p.slots * L::QT);
+          for (int s = 0; s < p.slots; ++s)
+            for (int h = 0; h < NH; ++h)
+              tma_load_3d(q_s + s * L::QT + h * (TM * 128), &tm_q, h * 64, p.kvh * G, p.at + (p.rb * BLOCK + s * TM) / G, q_full);
+          ++q_issued;
+          return true;
+        };
+        const int lag = p.slots == 2 ? 0 : 1;  // V follows K by so many tiles
+        int rk = tile_row(0), rv = rk;
+        for (int j = 0; j < p.cnt + lag && ok; ++j) {
+          const int next = j + 1 < p.cnt ? tile_row(j + 1) : 0;  // a tile ahead: its table entry's latency lies behind the waits
+          if (j < p.cnt) ok = load(&tm_k, rk);
+          if (ok && j >= lag) ok = load(&tm_v, lag ? rv : rk);
+          rv = rk;
+          rk = next;
+          // at most four tiles before Q: the ring takes them without this part's products
+          if (ok && j == min(1, p.cnt + lag - 1)) ok = load_q();
+        }
+        last_slots = p.slots;
+        x += p.cnt;
+        if (x < count) cur.advance(B, work, p.cnt);
+      }
+      if (*abort_flag) {  // let copies in flight land before shared memory is released
+        if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
+        for (int k = max(0, c - NS); k < c; ++k) drain(kv_full(k % NS), (k / NS) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ products
+    constexpr uint32_t idesc_s = idesc_f16(TM, TK, BF16, 0), idesc_o = idesc_f16(TM, HD, BF16, 1);
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
+    auto wait_kv = [&](int c) { return wait(kv_full(c % NS), (c / NS) & 1); };
+    auto scores = [&](int slot, int q_slot, int c) {
+      tc_fence_after();
+      const uint32_t k = kv_s + (c % NS) * L::KV, q = q_s + q_slot * L::QT;
+#pragma unroll
+      for (int kc = 0; kc < HD / 16; ++kc)
+        umma_f16_ss_warp(tmem + slot * TK, sdesc_kmajor_sw128(q + (kc >> 2) * (TM * 128) + (kc & 3) * 32),
+                         sdesc_kmajor_sw128(k + (kc >> 2) * (TK * 128) + (kc & 3) * 32), idesc_s, kc > 0);
+      umma_commit_warp(s_full(slot));
+    };
+    auto values = [&](int slot, int c, bool add) {
+      tc_fence_after();
+      const uint32_t v = kv_s + (c % NS) * L::KV;
+#pragma unroll
+      for (int kc = 0; kc < TK / 16; ++kc)
+        umma_f16_ts_warp(tmem + 256 + slot * TK, tmem + slot * TK + (kc >> 2) * 64 + (kc & 3) * 8, sdesc_mnmajor_sw128(v + kc * 2048, TK * 128), idesc_o,
+                         add || kc > 0);
+      umma_commit_warp(o_done(slot));
+    };
+    int c0 = 0, seg = 0;
+    int pc[2] = {0, 0};  // P tiles taken of each slot
+    bool ok = true;
+    for (long long x = 0; x < count && ok; ++seg) {
+      const Part p = part(x);
+      auto free_kv = [&](int c) { umma_commit_warp(kv_empty(c % NS)); };
+      if (!(ok = wait(q_full, seg & 1))) break;
+      if (p.slots == 2) {
+        if (!(ok = wait_kv(c0))) break;
+        scores(0, 0, c0);
+        scores(1, 1, c0);
+        free_kv(c0);
+        if (p.cnt == 1) umma_commit_warp(q_empty);
+        if (seg > 0 && !(ok = wait(o_empty(0), (seg - 1) & 1) && wait(o_empty(1), (seg - 1) & 1))) break;
+        for (int j = 0; j < p.cnt && ok; ++j) {
+          const int v = c0 + place_v(p, j), k = c0 + place_k(p, j + 1);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!(ok = ok && wait(p_full(s), pc[s] & 1) && wait_kv(v))) break;
+            ++pc[s];
+            values(s, v, j > 0);
+            if (s == 1) free_kv(v);
+            if (j + 1 < p.cnt) {
+              if (!(ok = wait_kv(k))) break;
+              scores(s, s, k);
+              if (s == 1) {
+                free_kv(k);
+                if (j + 2 == p.cnt) umma_commit_warp(q_empty);
+              }
+            }
+          }
+        }
+      } else {
+        for (int j = 0; j < min(2, p.cnt) && ok; ++j) {
+          const int k = c0 + place_k(p, j);
+          if (!(ok = wait_kv(k))) break;
+          scores(j, 0, k);
+          free_kv(k);
+        }
+        if (!ok) break;
+        if (p.cnt <= 2) umma_commit_warp(q_empty);
+        if (seg > 0 && !(ok = wait(o_empty(0), (seg - 1) & 1) && wait(o_empty(1), (seg - 1) & 1))) break;
+        for (int j = 0; j < p.cnt && ok; ++j) {
+          const int s = j & 1, v = c0 + place_v(p, j), k = c0 + place_k(p, j + 2);
+          if (!(ok = wait(p_full(s), pc[s] & 1) && wait_kv(v))) break;
+          ++pc[s];
+          values(s, v, j >= 2);
+          free_kv(v);
+          if (j + 2 < p.cnt) {
+            if (!(ok = wait_kv(k))) break;
+            scores(s, 0, k);
+            free_kv(k);
+            if (j + 3 == p.cnt) umma_commit_warp(q_empty);
+          }
+        }
+      }
+      c0 += 2 * p.cnt;
+      x += p.cnt;
+      if (x < count) cur.advance(B, work, p.cnt);
+    }
+    if (!ok) {
+      umma_commit_warp(drain_bar);
+      drain(drain_bar, 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax rows
+    const int slot = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t sbuf = tmem + lane_off + slot * TK, obuf = tmem + lane_off + 256 + slot * TK;
+    const float sl2 = P.scale_log2;
+    int c0 = 0, done = 0;  // tiles of the parts before; tiles of this slot
+    bool ok = true;
+    // tcgen05.ld / st are warp-collective: every branch around them is warp-uniform
+    for (long long x = 0; x < count; ) {
+      const Part p = part(x);
+      const int row = p.rb * BLOCK + (p.slots == 2 ? slot * TM : 0) + r;  // row of the sequence and kv head
+      const int node = row / G;
+      const bool mine = r < p.rows - (p.slots == 2 ? slot * TM : 0);
+      float m = -INFINITY, l = 0.f;
+      const int step = p.slots == 2 ? 1 : 2, j0 = p.slots == 2 ? 0 : slot;
+      for (int j = j0; j < p.cnt; j += step) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(slot), done & 1, abort_flag)))) break;
+        tc_fence_after();
+        const int key0 = (p.u0 + j) * TK, nvalid = p.start + p.n - key0;
+        const bool tail = key0 + TK > p.start;  // the tile holds rows of the sequence itself, or what lies behind them
+        uint32_t vis[4];                        // the keys of such a tile that the row sees
+        if (tail) {
+          const int n0 = key0 - p.start;  // node of the tile's first key (negative: cached)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] = low_bits((mine && B.parent == nullptr ? node + 1 : 0) - (n0 + 32 * w));
+          if (mine && B.parent != nullptr) {
+            for (int a = node; a >= 0 && a >= n0;) {  // ancestors come before their children
+              const int e = a - n0;
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if ((e >> 5) == w) vis[w] |= 1u << (e & 31);
+              bool bad;
+              a = tree_parent(B.parent + p.at, a, bad);
+              if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
+            }
+          }
+        }
+        // the scores of 64 keys; hidden ones -inf: they add nothing to the maximum and get weight 0
+        uint32_t v[64];
+        auto load = [&](int h) {
+          tmem_ld_32x32b_x32(sbuf + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld_32x32b_x32(sbuf + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_wait();
+          if (tail) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (!(((h == 0 ? vis[e >> 5] : vis[2 + (e >> 5)]) >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+          }
+        };
+        // The first half is read twice: 128 scores at once do not fit the registers beside the rest. P takes the first
+        // 32 columns of its own half's scores.
+        float mp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load(h);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) mp[e & 7] = fmaxf(mp[e & 7], __uint_as_float(v[e]));
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])), fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+        const bool need = mx > m + RESCALE_LOG2;
+        if (j == j0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2(m - mx) : 1.f;
+          l *= alpha;
+          // O holds the tiles so far: wait for the last of them, then scale it in place
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_done(slot), (done - 1) & 1, abort_flag)))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(obuf + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st_32x32b_x32(obuf + 32 * c, o);
+          }
+          if (need) m = mx;
+        }
+        const float neg_m = m == -INFINITY ? 0.f : -m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          if (h == 0) load(0);
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), sl2, neg_m));
+            const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), sl2, neg_m));
+            ls[e & 3] += p0 + p1;
+            pk[e] = pack2<BF16>(p0, p1);
+          }
+          tmem_st_32x32b_x32(sbuf + 64 * h, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if (r >= nvalid) {
+          // key r of the tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN.
+          // Each slot clears it before its own product.
+          const int c = c0 + place_v(p, j);
+          const uint32_t vt = kv_s + (c % NS) * L::KV + r * 128;
+          ok = mbar_wait(kv_full(c % NS), (c / NS) & 1, abort_flag);
+          for (int y = 0; y < NH * 8; ++y)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (y >> 3) * (TK * 128) + (y & 7) * 16), "r"(0) : "memory");
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_before();
+        mbar_arrive(p_full(slot));
+        ++done;
+      }
+      // ------------------------------------------------------------------ the part's end
+      const int tiles = p.slots == 2 ? p.cnt : (p.cnt - slot + 1) / 2;
+      if (ok && tiles > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done(slot), (done - 1) & 1, abort_flag));
+      if (!bar_and(1, SM_THREADS, ok)) break;
+      tc_fence_after();
+      const bool whole = p.cnt == cur.w.units;
+      const long long task_first = ub + x - p.u0;
+      float* place = P.part + part_place(ws.total, cta, max(1, ctas), task_first) * (static_cast<size_t>(P.part_rows) * (HD + 2));
+      __half* dst = P.out + (static_cast<size_t>(p.at + node) * P.nq + p.kvh * G + (row - node * G)) * HD;
+      const int pr = row - p.rb * BLOCK;  // row of the place
+      // 32 columns of the row's O: to the output, or as they are to the part's place
+      auto put = [&](int c, const float* o, float inv) {
+        if (!mine) return;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const __half2 a = __floats2half2_rn(o[e + 2 * y] * inv, o[e + 2 * y + 1] * inv);
+              h[y] = *reinterpret_cast<const uint32_t*>(&a);
+            }
+            *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            reinterpret_cast<float4*>(place)[static_cast<size_t>(8 * c + e / 4) * P.part_rows + pr] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      };
+      auto put_ml = [&](float mm, float ll) {
+        if (mine && !whole) reinterpret_cast<float2*>(place + static_cast<size_t>(P.part_rows) * HD)[pr] = make_float2(mm, ll);
+      };
+      if (p.slots == 2) {
+        put_ml(m, l);
+        const float inv = 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(obuf + 32 * c, o);
+          tmem_ld_wait();
+          put(c, reinterpret_cast<const float*>(o), inv);
+        }
+      } else {
+        // slot 1's sums join slot 0's: half of the columns at a time through slot 1's Q, [column][row]
+        float a0 = 1.f, a1 = 0.f, inv = 1.f;
+        if (slot == 1) ml_s[r] = make_float2(m, l);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (slot == 1) {
+#pragma unroll 1
+            for (int c = 0; c < HD / 64; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(obuf + h * (HD / 2) + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) xbuf[(32 * c + e) * TM + r] = __uint_as_float(o[e]);
+            }
+          }
+          bar_sync(1, SM_THREADS);
+          if (slot == 0) {
+            if (h == 0) {
+              const float2 y = ml_s[r];
+              const float mm = fmaxf(m, y.x);
+              a0 = m == -INFINITY ? 0.f : ex2(m - mm);
+              a1 = y.x == -INFINITY ? 0.f : ex2(y.x - mm);
+              const float ll = a0 * l + a1 * y.y;
+              inv = 1.f / ll;
+              put_ml(mm, ll);
+            }
+#pragma unroll 1
+            for (int c = 0; c < HD / 64; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(obuf + h * (HD / 2) + 32 * c, o);
+              tmem_ld_wait();
+              float f[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {  // a slot that saw nothing may hold anything
+                const float u = a0 == 0.f ? 0.f : a0 * __uint_as_float(o[e]);
+                f[e] = a1 == 0.f ? u : fmaf(a1, xbuf[(32 * c + e) * TM + r], u);
+              }
+              put(h * (HD / 64) + c, f, inv);
+            }
+          }
+          bar_sync(1, SM_THREADS);
+        }
+        fence_proxy_async_smem();  // before a later part's Q
+      }
+      tc_fence_before();
+      mbar_arrive(o_empty(slot));
+      c0 += 2 * p.cnt;
+      x += p.cnt;
+      if (x < count) cur.advance(B, work, p.cnt);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) batch_record(P.status, PF_ERR_DEVICE_TIMEOUT);
+}
+
+// Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
+// CTA = 32 rows of a (sequence, kv head), a thread per row and eight columns; parts that saw no key of a row hold no O.
+constexpr int MERGE_ROWS = 32;
+
+template <int HD>
+__global__ void __launch_bounds__(MERGE_ROWS* HD / 8) tree_merge_kernel(const BatchDev B, int nq, int nkv, const long long* plan,
+                                                                        const float* part, int part_rows, __half* out) {
+  PF_TIMELINE(TL_TREE_MERGE);
+  griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.z, kvh = blockIdx.y, G = nq / nkv;
+  const SeqRows s = batch_seq(B, b, true);
+  const int row = blockIdx.x * MERGE_ROWS + (threadIdx.x & 31), oct = threadIdx.x >> 5;
+  if (static_cast<int>(blockIdx.x) * MERGE_ROWS >= s.n * G) return;
+  const long long total = plan[0], seq_first = plan[2 + b];
+  const int ctas = static_cast<int>(plan[1]);
+  const int rb = row / BLOCK, blocks = (s.n * G + BLOCK - 1) / BLOCK, units = (s.start + s.n + TK - 1) / TK;
+  const long long first = seq_first + static_cast<long long>(kvh * blocks + rb) * units;
+  const int c0 = range_owner(total, first, ctas), c1 = range_owner(total, first + units - 1, ctas);
+  if (c0 == c1 || row >= s.n * G) return;
+  const int pr = row - rb * BLOCK;
+  float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int Q = 4;  // parts in flight
+  for (int c = c0; c <= c1; c += Q) {
+    float4 v[Q][2];
+    float2 ml[Q];
+#pragma unroll
+    for (int y = 0; y < Q; ++y) {
+      const float* src = part + part_place(total, min(c + y, c1), ctas, first) * (static_cast<size_t>(part_rows) * (HD + 2));
+      ml[y] = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(part_rows) * HD) + pr);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) v[y][u] = __ldcg(reinterpret_cast<const float4*>(src) + static_cast<size_t>(2 * oct + u) * part_rows + pr);
+    }
+#pragma unroll
+    for (int y = 0; y < Q; ++y) {
+      if (c + y > c1 || ml[y].x == -INFINITY) continue;
+      const float mn = fmaxf(mr, ml[y].x);
+      const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ex2(ml[y].x - mn);
+      mr = mn;
+      lr = lr * a + f * ml[y].y;
+      const float* w = reinterpret_cast<const float*>(v[y]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + f * w[e];
+    }
+  }
+  const float inv = 1.f / lr;
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 x = __floats2half2_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    h[e] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  const int node = row / G;
+  *reinterpret_cast<uint4*>(out + (static_cast<size_t>(s.at + node) * nq + kvh * G + row - node * G) * HD + 8 * oct) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+size_t plan_bytes(int n_seq) { return (static_cast<size_t>(n_seq) + 2 + 31) / 32 * 32 * sizeof(long long); }
+int place_rows(const pf_config& c, int max_rows) { return std::min(BLOCK, (max_rows * (c.n_q_heads / c.n_kv_heads) + 31) / 32 * 32); }
+
+template <int HD, int BF16>
+cudaError_t launch_tc(const TreeAttnArgs& a, cudaStream_t stream) {
+  const pf_config& c = *a.c;
+  const int G = c.n_q_heads / c.n_kv_heads;
+  const uint64_t dims[2] = {HD, static_cast<uint64_t>(c.n_layers) * c.n_kv_heads * cache_slots(c)}, strides[1] = {HD * 2};
+  const uint32_t box[2] = {64, TK};
+  const uint64_t qd[3] = {HD, static_cast<uint64_t>(c.n_q_heads), static_cast<uint64_t>(a.b->n_rows)};
+  const uint64_t qs[2] = {HD * 2, static_cast<uint64_t>(c.n_q_heads) * HD * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(TM / G)};
+  CUtensorMap tq, tk, tv;
+  if (!encode_tmap_16(&tq, BF16, 3, a.q, qd, qs, qb) || !encode_tmap_16(&tk, BF16, 2, a.k_cache, dims, strides, box) ||
+      !encode_tmap_16(&tv, BF16, 2, a.v_cache, dims, strides, box))
+    return cudaErrorInvalidValue;
+  const int max_rows = std::min(a.b->max_rows, a.b->n_rows);
+  TcParams p{};
+  p.B = batch_dev(c, *a.b);
+  p.nq = c.n_q_heads;
+  p.nkv = c.n_kv_heads;
+  p.layer = a.layer;
+  p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
+  p.out = static_cast<__half*>(a.out);
+  uint8_t* at = static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c);
+  p.plan = reinterpret_cast<long long*>(at);
+  p.part = reinterpret_cast<float*>(at + plan_bytes(a.b->n_seq));
+  p.part_rows = place_rows(c, max_rows);
+  p.status = a.status;
+  const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
+  const cudaError_t e = launch_pdl(attn_tree_tc_kernel<HD, BF16>, dim3(ctas), dim3(THREADS), TSmem<HD>::BYTES, stream, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_merge_kernel<HD>, dim3((max_rows * G + MERGE_ROWS - 1) / MERGE_ROWS, c.n_kv_heads, a.b->n_seq),
+                    dim3(MERGE_ROWS * HD / 8), 0, stream, p.B, p.nq, p.nkv, static_cast<const long long*>(p.plan),
+                    static_cast<const float*>(p.part), p.part_rows, p.out);
+}
+
+template <int HD, int BF16>
+cudaError_t set_attr_tc() {
+  return cudaFuncSetAttribute(attn_tree_tc_kernel<HD, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TSmem<HD>::BYTES);
+}
+
+}  // namespace
+
+size_t attention_tree_tc_scratch_bytes(const pf_config& c, int n_seq, int max_rows) {
+  return tree_counter_bytes(c) + plan_bytes(n_seq) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * place_rows(c, max_rows) * (c.head_dim + 2) * sizeof(float);
+}
+
+cudaError_t prepare_attention_tree_tc_kernels() {
+  cudaError_t e = cudaSuccess, r;
+  if ((r = set_attr_tc<128, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr_tc<128, 0>()) != cudaSuccess) e = r;
+  if ((r = set_attr_tc<64, 1>()) != cudaSuccess) e = r;
+  if ((r = set_attr_tc<64, 0>()) != cudaSuccess) e = r;
+  return e;
+}
+
+cudaError_t launch_attention_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
+  const bool bf = a.c->kv_dtype == PF_KV_BF16;
+  if (a.c->head_dim == 128) return bf ? launch_tc<128, 1>(a, stream) : launch_tc<128, 0>(a, stream);
+  return bf ? launch_tc<64, 1>(a, stream) : launch_tc<64, 0>(a, stream);
+}
+
+}  // namespace pf
+
+PF_TIMELINE_SETTER(attention_tree_tc)

@@ -34,7 +34,7 @@ __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* dst, float a,
 }
 
 template <int HD, typename T, int SLOTS>
-__global__ void __launch_bounds__(AP_THREADS) batch_append_kernel(const BatchDev B, const float* __restrict__ qkv,
+__global__ void __launch_bounds__(AP_THREADS) batch_append_kernel(const BatchDev B, const float* qkv,
                                                                   const float* __restrict__ qn, const float* __restrict__ kn,
                                                                   const float* __restrict__ rope, int nq, int nkv, int layer,
                                                                   float eps, int qk_norm, T* __restrict__ q_out,
@@ -139,10 +139,8 @@ cudaError_t append(const pf_config& c, const pf_batch& b, const float* qkv, cons
 // reads none that was written.
 constexpr int AC_THREADS = 256;
 
-__global__ void __launch_bounds__(AC_THREADS) tree_accept_kernel(const BatchDev B, const int* __restrict__ tokens,
-                                                                 const int* __restrict__ ids, const int* __restrict__ root,
-                                                                 int* __restrict__ path_out, int* __restrict__ n_out,
-                                                                 int* __restrict__ next_out, uint4* kc, uint4* vc, int heads,
+__global__ void __launch_bounds__(AC_THREADS) tree_accept_kernel(const BatchDev B, const int* tokens, const int* ids, const int* root,
+                                                                 int* path_out, int* n_out, int* next_out, uint4* kc, uint4* vc, int heads,
                                                                  int vec, int* status) {
   PF_TIMELINE(TL_TREE_ACCEPT);
   __shared__ int path[PF_MAX_TREE], id_s[PF_MAX_TREE], from[PF_MAX_TREE], to[PF_MAX_TREE];

@@ -857,6 +857,7 @@ pf_status pf_timeline_set(uint64_t* buffer, int64_t capacity) {
   PF_CUDA(timeline_set_logprobs(b), "timeline");
   PF_CUDA(timeline_set_batch(b), "timeline");
   PF_CUDA(timeline_set_attention_tree(b), "timeline");
+  PF_CUDA(timeline_set_attention_tree_tc(b), "timeline");
   PF_CUDA(timeline_set_adapters(b), "timeline");
   return PF_OK;
 }
@@ -879,6 +880,8 @@ const char* pf_timeline_kernel_name(int32_t id) {
     n[TL_BATCH_APPEND] = "batch_append";
     n[TL_TREE_ACCEPT] = "tree_accept";
     n[TL_ATTENTION_TREE] = "attention_tree";
+    n[TL_ATTENTION_TREE_TC] = "attention_tree_tc";
+    n[TL_TREE_MERGE] = "attention_tree_merge";
     n[TL_ADAPTER_DOWN] = "adapter_down";
     n[TL_ADAPTER_UP] = "adapter_up";
     return n;
@@ -1456,6 +1459,17 @@ pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32
 
 }  // extern "C"
 
+// Raises the tree attention's dynamic shared-memory limits once on each device.
+static void prepare_tree() {
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  std::call_once(once[dev], [] {
+    prepare_attention_tree_kernels();
+    prepare_attention_tree_tc_kernels();
+  });
+}
+
 // What every call over a batch checks; `tree`: rows per sequence are bounded by PF_MAX_TREE.
 static pf_status check_batch_rows(const pf_batch* b, bool tree) {
   if (!b) return fail(PF_ERR_INVALID_ARG, "batch is NULL");
@@ -1517,6 +1531,7 @@ pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, cons
   if (scratch_bytes < need || !scratch)
     return fail(PF_ERR_WORKSPACE, "tree attention scratch %zu bytes, need %zu", scratch_bytes, need);
   if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  prepare_tree();
   TreeAttnArgs a{cfg, batch, q, kc, vc, layer, out, scratch, status};
   PF_CUDA(launch_attention_tree(a, static_cast<cudaStream_t>(stream)), "tree attention");
   return PF_OK;

@@ -283,7 +283,16 @@ struct TreeAttnArgs {
   void* scratch;  // attention_tree_scratch_bytes(c, n_seq, max_rows) bytes
   int* status;
 };
+// The scratch begins with an arrival counter per (sequence, kv head), as many as any batch has, zero before the
+// first launch and after every one that completes; behind them what a launch writes before it reads it.
+inline size_t tree_counter_bytes(const pf_config& c) { return (static_cast<size_t>(PF_MAX_SEQS) * c.n_kv_heads * sizeof(int) + 255) / 256 * 256; }
 size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows);
+cudaError_t prepare_attention_tree_kernels();
+// the form for more rows per kv head than the few-row kernel takes (attention_tree_tc.cu)
+size_t attention_tree_tc_scratch_bytes(const pf_config& c, int n_seq, int max_rows);
+cudaError_t prepare_attention_tree_tc_kernels();
+cudaError_t launch_attention_tree_tc(const TreeAttnArgs& a, cudaStream_t stream);
+cudaError_t timeline_set_attention_tree_tc(unsigned long long* buf);
 cudaError_t launch_attention_tree(const TreeAttnArgs& a, cudaStream_t stream);
 struct AdapterArgs {
   const pf_batch* b;
@@ -382,7 +391,8 @@ enum TimelineId : int {
   TL_GEMM = 20,        // + epilogue (0 store, 1 residual, 2 SwiGLU) + 3 for the CTA-pair form
   TL_GEMM_SMALL = 30,  // + epilogue
   TL_GEMV = 40,        // + epilogue
-  TL_BATCH_APPEND = 50, TL_TREE_ACCEPT = 51, TL_ATTENTION_TREE = 52, TL_ADAPTER_DOWN = 55, TL_ADAPTER_UP = 56
+  TL_BATCH_APPEND = 50, TL_TREE_ACCEPT = 51, TL_ATTENTION_TREE = 52, TL_ATTENTION_TREE_TC = 53, TL_TREE_MERGE = 54,
+  TL_ADAPTER_DOWN = 55, TL_ADAPTER_UP = 56
 };
 // Per translation unit: points its kernels' timeline buffer at `buf` (NULL: off).
 cudaError_t timeline_set_kernels(unsigned long long* buf);

@@ -185,6 +185,21 @@ def test_attention_large_scores(kind, top):
     pf.pf_status_read(s.status)
 
 
+@pytest.mark.parametrize("kind,nq,nkv,hd", [("bf16", 8, 2, 128), ("f16", 4, 2, 64)])
+@pytest.mark.parametrize("top", [1, 4, 33, 64])
+def test_attention_long_ragged(kind, nq, nkv, hd, top):
+    """Many units a CTA, borders of ranges and tasks in every place: each ring goes round many times."""
+    rng = np.random.default_rng(21)
+    rows = [top - (i % 2) if top > 1 else 1 for i in range(40)]
+    start = [int(x) for x in rng.integers(200, 9000, 40)]
+    s = Step(kind, nq, nkv, hd, rows, start, True, trees(rng, rows), n_layers=1, layer=0)
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
 def test_attention_deep_and_wide_trees():
     """A chain given by parents, a star, all nodes under the cache, two of them in one batch."""
     n = 256
