@@ -882,8 +882,7 @@ const char* pf_timeline_kernel_name(int32_t id) {
     n[TL_ATTENTION_TREE] = "attention_tree";
     n[TL_ATTENTION_TREE_TC] = "attention_tree_tc";
     n[TL_TREE_MERGE] = "attention_tree_merge";
-    n[TL_ADAPTER_DOWN] = "adapter_down";
-    n[TL_ADAPTER_UP] = "adapter_up";
+    n[TL_ADAPTERS] = "adapters";
     return n;
   }();
   if (id < 1 || id >= 64 || names[id].empty()) return nullptr;
@@ -1459,14 +1458,15 @@ pf_status pf_prefill_score(pf_session* s, const int32_t* tokens_dev, const int32
 
 }  // extern "C"
 
-// Raises the tree attention's dynamic shared-memory limits once on each device.
-static void prepare_tree() {
+// Raises the batch kernels' dynamic shared-memory limits once on each device.
+static void prepare_batch() {
   static std::once_flag once[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
   std::call_once(once[dev], [] {
     prepare_attention_tree_kernels();
     prepare_attention_tree_tc_kernels();
+    prepare_adapters_kernels();
   });
 }
 
@@ -1531,7 +1531,7 @@ pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, cons
   if (scratch_bytes < need || !scratch)
     return fail(PF_ERR_WORKSPACE, "tree attention scratch %zu bytes, need %zu", scratch_bytes, need);
   if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
-  prepare_tree();
+  prepare_batch();
   TreeAttnArgs a{cfg, batch, q, kc, vc, layer, out, scratch, status};
   PF_CUDA(launch_attention_tree(a, static_cast<cudaStream_t>(stream)), "tree attention");
   return PF_OK;
@@ -1574,6 +1574,7 @@ pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, 
   const size_t need = adapters_scratch_bytes(batch->n_rows, rank);
   if (scratch_bytes < need || !scratch) return fail(PF_ERR_WORKSPACE, "adapters scratch %zu bytes, need %zu", scratch_bytes, need);
   if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  prepare_batch();
   AdapterArgs a{batch, x, ldx, base, ld_base, out, ld_out, K, N, rank, n_adapters, adapter, wa, wb, scale, scratch, status};
   PF_CUDA(launch_adapters(a, static_cast<cudaStream_t>(stream)), "adapters");
   return PF_OK;

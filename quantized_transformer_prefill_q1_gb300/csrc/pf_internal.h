@@ -311,6 +311,7 @@ struct AdapterArgs {
   int* status;
 };
 size_t adapters_scratch_bytes(int n_rows, int rank);
+cudaError_t prepare_adapters_kernels();
 cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t stream);
 
 cudaError_t launch_embed(const float* E, const int* tokens, int M, int H, int vocab, float* x,
@@ -392,7 +393,7 @@ enum TimelineId : int {
   TL_GEMM_SMALL = 30,  // + epilogue
   TL_GEMV = 40,        // + epilogue
   TL_BATCH_APPEND = 50, TL_TREE_ACCEPT = 51, TL_ATTENTION_TREE = 52, TL_ATTENTION_TREE_TC = 53, TL_TREE_MERGE = 54,
-  TL_ADAPTER_DOWN = 55, TL_ADAPTER_UP = 56
+  TL_ADAPTERS = 55
 };
 // Per translation unit: points its kernels' timeline buffer at `buf` (NULL: off).
 cudaError_t timeline_set_kernels(unsigned long long* buf);
