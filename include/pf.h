@@ -584,13 +584,11 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
  * zero rows of A); K a multiple of 16, N of 8, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
  * aligned. Products and sums in f32 (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
  * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. batch: row_begin only; sequences of
- * up to 8192 rows. scratch_dev: 16-B aligned, pf_adapters_scratch_bytes(n_rows, rank) bytes, zero before
- * the first call and left zero by calls that complete; not shared by calls that overlap. */
-size_t pf_adapters_scratch_bytes(int32_t n_rows, int32_t rank);
+ * up to 8192 rows. No scratch. */
 pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x_f16_dev, int64_t ldx, const float* base_dev, int64_t ld_base,
                          float* out_dev, int64_t ld_out, int32_t K, int32_t N, int32_t rank, int32_t n_adapters,
                          const int32_t* adapter_dev, const uint16_t* a_f16_dev, const uint16_t* b_f16_dev,
-                         const float* scale_dev, void* scratch_dev, size_t scratch_bytes, int32_t* status_dev, void* stream);
+                         const float* scale_dev, int32_t* status_dev, void* stream);
 /* Host RoPE table [max_seq][hd/2][2] = (cos, sin)(p * theta^(-2i/hd)), computed in
  * double and rounded to f32. */
 pf_status pf_rope_table_host(float theta, int32_t head_dim, int32_t max_seq, float* dst_host);

@@ -375,8 +375,6 @@ cudaError_t set_attr() {
 
 }  // namespace
 
-size_t adapters_scratch_bytes(int n_rows, int rank) { return (static_cast<size_t>(n_rows) * rank * 4 + 15) / 16 * 16; }
-
 cudaError_t prepare_adapters_kernels() {
   cudaError_t e = cudaSuccess, r;
   if ((r = set_attr<16, 1>()) != cudaSuccess) e = r;

@@ -1551,15 +1551,10 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
   return PF_OK;
 }
 
-size_t pf_adapters_scratch_bytes(int32_t n_rows, int32_t rank) {
-  if (n_rows < 1 || rank < 8 || rank > PF_MAX_RANK || rank % 8) return 0;
-  return adapters_scratch_bytes(n_rows, rank);
-}
-
 pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, const float* base, int64_t ld_base, float* out,
                          int64_t ld_out, int32_t K, int32_t N, int32_t rank, int32_t n_adapters, const int32_t* adapter,
-                         const uint16_t* wa, const uint16_t* wb, const float* scale, void* scratch, size_t scratch_bytes,
-                         int32_t* status, void* stream) {
+                         const uint16_t* wa, const uint16_t* wb, const float* scale, int32_t* status,
+                         void* stream) {
   PF_TRY(check_batch_rows(batch, false));
   if (rank < 8 || rank > PF_MAX_RANK || rank % 8) return fail(PF_ERR_SHAPE, "rank %d: a multiple of 8 up to %d", rank, PF_MAX_RANK);
   if (K < 16 || K % 16 || N < 8 || N % 8) return fail(PF_ERR_SHAPE, "K %d: a multiple of 16; N %d: of 8", K, N);
@@ -1571,11 +1566,8 @@ pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, 
   if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(wa) || !aligned16(wb))
     return fail(PF_ERR_INVALID_ARG, "x, base, out, A and B must be 16-B aligned");
   if (base == out && ld_base != ld_out) return fail(PF_ERR_SHAPE, "out = base needs ld_out = ld_base");
-  const size_t need = adapters_scratch_bytes(batch->n_rows, rank);
-  if (scratch_bytes < need || !scratch) return fail(PF_ERR_WORKSPACE, "adapters scratch %zu bytes, need %zu", scratch_bytes, need);
-  if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
   prepare_batch();
-  AdapterArgs a{batch, x, ldx, base, ld_base, out, ld_out, K, N, rank, n_adapters, adapter, wa, wb, scale, scratch, status};
+  AdapterArgs a{batch, x, ldx, base, ld_base, out, ld_out, K, N, rank, n_adapters, adapter, wa, wb, scale, status};
   PF_CUDA(launch_adapters(a, static_cast<cudaStream_t>(stream)), "adapters");
   return PF_OK;
 }

@@ -307,10 +307,8 @@ struct AdapterArgs {
   const void* wa;
   const void* wb;
   const float* scale;
-  void* scratch;
   int* status;
 };
-size_t adapters_scratch_bytes(int n_rows, int rank);
 cudaError_t prepare_adapters_kernels();
 cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t stream);
 

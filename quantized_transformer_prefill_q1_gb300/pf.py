@@ -137,9 +137,8 @@ _SIGS = {
                               _VP, _VP], _I32),
     "pf_op_tree_accept": ([ctypes.POINTER(pf_config), ctypes.POINTER(pf_batch), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                            _VP, _VP], _I32),
-    "pf_adapters_scratch_bytes": ([_I32, _I32], _SZ),
     "pf_op_adapters": ([ctypes.POINTER(pf_batch), _VP, _I64, _VP, _I64, _VP, _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP,
-                        _VP, _VP, _SZ, _VP, _VP], _I32),
+                        _VP, _VP, _VP], _I32),
     "pf_status_read": ([_VP, _VP], _I32),
     "pf_selftest_bounded_wait": ([_VP, _I64, _I32, _VP], _I32),
 }
@@ -535,15 +534,6 @@ def pf_op_tree_accept(cfg, batch, tokens, ids, root_ids, path, n_accepted, next_
                                   _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
-def adapters_scratch(n_rows, rank, device="cuda"):
-    """Zeroed scratch (uint8 tensor) for pf_op_adapters on up to n_rows rows with adapters of this rank."""
-    import torch
-    n = lib().pf_adapters_scratch_bytes(n_rows, rank)
-    if n == 0:
-        raise PfError(2, f"n_rows {n_rows}: at least 1; rank {rank}: a multiple of 8 up to {MAX_RANK}")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
-
-
 def _strided(t, dev: int, dtype: str, what: str, rows: int):
     """(address, elements between rows) of rows [>= rows, width] with contiguous elements."""
     if t is None or t.dim() != 2 or t.shape[0] < rows:
@@ -555,7 +545,7 @@ def _strided(t, dev: int, dtype: str, what: str, rows: int):
     return t.data_ptr(), st[0] if rows > 1 else -(-t.shape[1] // 8) * 8
 
 
-def pf_op_adapters(batch, x, base, out, adapter, a, b, scale, scratch, status=None, stream=None):
+def pf_op_adapters(batch, x, base, out, adapter, a, b, scale, status=None, stream=None):
     """out[m] = base[m] + scale[i] (x[m] A_i^T) B_i^T with i = adapter[sequence of m], -1: none. x f16 [n_rows, K], base and
     out f32 [n_rows, N] (views of wider rows; out may be base), a f16 [adapters, rank, K], b f16 [adapters, N, rank],
     scale f32 [adapters], adapter int32 [n_seq]."""
@@ -571,7 +561,6 @@ def pf_op_adapters(batch, x, base, out, adapter, a, b, scale, scratch, status=No
     check(lib().pf_op_adapters(_batch(batch, dev), xp, ldx, bp, ldb, op, ldo, k, n, rank, count,
                                _dense(adapter, dev, "int32", "adapter", batch.n_seq), _dense(a, dev, "float16", "A", count * rank * k),
                                _dense(b, dev, "float16", "B", count * n * rank), _dense(scale, dev, "float32", "scale", count),
-                               _dense(scratch, dev, "uint8", "scratch", 0), scratch.numel(),
                                _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 

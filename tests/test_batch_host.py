@@ -43,11 +43,10 @@ def accept(lib, c=None, b=None, tokens=P, ids=P, root=P, path=P, count=P, after=
     return name(lib.pf_op_tree_accept(ctypes.byref(c), ctypes.byref(b) if b else None, tokens, ids, root, path, count, after, kc, vc, None, None))
 
 
-def adapters(lib, b=None, x=P, ldx=64, base=P, ldb=32, out=2 * P, ldo=32, k=64, n=32, rank=8, count=2, adapter=P, wa=P, wb=P, scale=P,
-             scratch=P, nbytes=1 << 40):
+def adapters(lib, b=None, x=P, ldx=64, base=P, ldb=32, out=2 * P, ldo=32, k=64, n=32, rank=8, count=2, adapter=P, wa=P, wb=P, scale=P):
     b = b if b is not None else batch()
-    return name(lib.pf_op_adapters(ctypes.byref(b) if b else None, x, ldx, base, ldb, out, ldo, k, n, rank, count, adapter, wa, wb, scale, scratch,
-                                   nbytes, None, None))
+    return name(lib.pf_op_adapters(ctypes.byref(b) if b else None, x, ldx, base, ldb, out, ldo, k, n, rank, count, adapter, wa, wb, scale,
+                                   None, None))
 
 
 @pytest.mark.parametrize("call", [append, attend, accept])
@@ -96,9 +95,6 @@ def test_adapter_refusals(lib):
                dict(ldb=28), dict(ldb=34), dict(ldo=28), dict(ldo=33), dict(out=P, ldo=36), dict(b=batch(max_rows=8193)), dict(b=batch(n_seq=2000))):
         assert adapters(lib, **kw) == "PF_ERR_SHAPE", kw
     assert adapters(lib, b=batch(n_rows=0)) == "PF_ERR_EMPTY_CHUNK"
-    assert adapters(lib, scratch=None) == "PF_ERR_WORKSPACE"
-    assert adapters(lib, scratch=P + 4) == "PF_ERR_INVALID_ARG"
-    assert adapters(lib, nbytes=lib.pf_adapters_scratch_bytes(10, 8) - 1) == "PF_ERR_WORKSPACE"
 
 
 def test_sizes(lib):
@@ -110,9 +106,6 @@ def test_sizes(lib):
         row = [lib.pf_attention_tree_scratch_bytes(c, n_seq, r) for r in (1, 2, 4, 5, 16, 33, 64, 65, 256)]
         assert row == sorted(row) and row[0] >= last > -1
         last = row[0]
-    for rows, rank in ((0, 8), (1, 0), (1, 4), (1, 136)):
-        assert lib.pf_adapters_scratch_bytes(rows, rank) == 0
-    assert lib.pf_adapters_scratch_bytes(5, 16) >= 5 * 16 * 4
 
 
 def test_binding_refuses_host_tensors():

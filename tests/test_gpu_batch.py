@@ -315,9 +315,8 @@ def test_adapters(k, n, rank, top):
     b = torch.from_numpy(rng.standard_normal((4, n, rank)) * 0.1).cuda().half()
     scale = torch.tensor([0.5, 2.0, 1.25, 16.0], device="cuda")
     status = torch.zeros(4, dtype=torch.int32, device="cuda")
-    scratch = pf.adapters_scratch(n_rows, rank)
     out = torch.full((n_rows, n), 7.0, device="cuda")
-    pf.pf_op_adapters(batch, x, base, out, ints(which), a, b, scale, scratch, status)
+    pf.pf_op_adapters(batch, x, base, out, ints(which), a, b, scale, status)
     pf.pf_status_read(status)
     got = out.double().cpu().numpy()
     for i, w in enumerate(which):
@@ -334,7 +333,7 @@ def test_adapters(k, n, rank, top):
     wide = torch.full((n_rows, n + 24), 3.0, device="cuda")
     block = wide[:, 8:n + 8]
     block.copy_(base)
-    pf.pf_op_adapters(batch, x, block, block, ints(which), a, b, scale, scratch, status)
+    pf.pf_op_adapters(batch, x, block, block, ints(which), a, b, scale, status)
     assert torch.equal(block[:total], out[:total]) and torch.equal(block[total:], base[total:])
     assert (wide[:, :8] == 3).all() and (wide[:, n + 8:] == 3).all()
 
@@ -349,7 +348,7 @@ def test_adapters_range():
     scale, base = torch.ones(1, device="cuda"), torch.zeros(3, n, device="cuda")
     out = torch.empty_like(base)
     batch = pf.Batch(ints([0, 3]), n_rows=3, max_rows=3)
-    pf.pf_op_adapters(batch, x, base, out, ints([0]), a, b, scale, pf.adapters_scratch(3, rank))
+    pf.pf_op_adapters(batch, x, base, out, ints([0]), a, b, scale)
     ref, bound = R.adapters(base.cpu().numpy(), x.cpu().numpy(), a[0].cpu().numpy(), b[0].cpu().numpy(), 1.0)
     off = np.abs(out.double().cpu().numpy() - ref)
     assert (off <= bound).all(), float((off / bound).max())
@@ -441,10 +440,10 @@ def test_bad_adapters():
     batch = pf.Batch(ints([0, 2, 3]), n_rows=3, max_rows=2)
     x, base = torch.randn(3, 64, device="cuda").half(), torch.randn(3, 32, device="cuda")
     a, b = torch.randn(2, 8, 64, device="cuda").half(), torch.randn(2, 32, 8, device="cuda").half()
-    scale, scratch, status = torch.ones(2, device="cuda"), pf.adapters_scratch(3, 8), torch.zeros(1, dtype=torch.int32, device="cuda")
+    scale, status = torch.ones(2, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     for bad in (2, -2, 2 ** 31 - 1, -2 ** 31):
         out = torch.full_like(base, 7.0)
-        pf.pf_op_adapters(batch, x, base, out, ints([bad, 1]), a, b, scale, scratch, status)
+        pf.pf_op_adapters(batch, x, base, out, ints([bad, 1]), a, b, scale, status)
         assert status_of(lambda: pf.pf_status_read(status)) == "PF_ERR_INVALID_ARG"
         assert torch.equal(out[:2], base[:2]) and not torch.equal(out[2], base[2])
 
@@ -478,18 +477,18 @@ def test_layer_of_several_requests():
     y, qkv = torch.empty(s.total, h, dtype=torch.float16, device="cuda"), torch.empty(s.total, width, device="cuda")
     q, attn = torch.empty(s.total, nq, hd, dtype=torch.float16, device="cuda"), torch.empty(s.total, nq * hd, dtype=torch.float16, device="cuda")
     out, qn_dev, kn_dev = x.clone(), torch.from_numpy(qn).cuda(), torch.from_numpy(kn).cuda()
-    gs, ls = pf.gemm_scratch(s.total, max(width, h)), pf.adapters_scratch(s.total, 16)
+    gs = pf.gemm_scratch(s.total, max(width, h))
     scratch, which_dev = s.scratch(), ints(which)
 
     def step():
         pf.pf_op_rmsnorm(x, norm_w, 1e-6, y)
         pf.pf_op_gemm(pf.W_Q1, pf.EPI_STORE_F32, y, packed["qkv"], s.total, width, h, qkv, gs, status=s.status)
         for name, lo, hi in (("q", 0, nq * hd), ("v", (nq + nkv) * hd, width)):
-            pf.pf_op_adapters(s.batch, y, qkv[:, lo:hi], qkv[:, lo:hi], which_dev, *ad[name], scale, ls, s.status)
+            pf.pf_op_adapters(s.batch, y, qkv[:, lo:hi], qkv[:, lo:hi], which_dev, *ad[name], scale, s.status)
         pf.pf_op_batch_append(s.cfg, s.batch, qkv, qn_dev, kn_dev, rope, 0, q, s.k, s.v, s.status)
         pf.pf_op_attention_tree(s.cfg, s.batch, q, s.k, s.v, 0, attn, scratch, s.status)
         pf.pf_op_gemm(pf.W_Q1, pf.EPI_RESID_ADD, attn, packed["o"], s.total, h, nq * hd, out, gs, status=s.status)
-        pf.pf_op_adapters(s.batch, attn, out, out, which_dev, *ad["o"], scale, ls, s.status)
+        pf.pf_op_adapters(s.batch, attn, out, out, which_dev, *ad["o"], scale, s.status)
 
     step()
     pf.pf_status_read(s.status)
