@@ -226,7 +226,7 @@ def _plan(c, s):
     if key not in _plans:
         status = torch.zeros(4, dtype=torch.int32, device="cuda")
         if c["op"] == "adapters":
-            _plans[key] = pf, None, pf.adapters_scratch(s["x"].shape[0], c["rank"]), status
+            _plans[key] = pf, None, None, status
         else:
             max_seq, _, pool, _ = _geometry(c)
             cfg = pf.pf_config(hidden=128, intermediate=128, n_q_heads=c["nq"], n_kv_heads=c["nkv"], head_dim=c["hd"], n_layers=N_LAYERS,
@@ -356,9 +356,9 @@ def run_accept(c, s):
 
 def run_adapters(c, s):
     if own:
-        pf, _, batch, scratch, status = _plan(c, s)
+        pf, _, batch, _, status = _plan(c, s)
         out = torch.empty_like(s["base"])
-        pf.pf_op_adapters(batch, s["x"], s["base"], out, s["adapter_dev"], s["a"], s["b"], s["scale"], scratch, status)
+        pf.pf_op_adapters(batch, s["x"], s["base"], out, s["adapter_dev"], s["a"], s["b"], s["scale"], status)
         return out
     out = s["base"].clone()
     for b, a in enumerate(s["adapter"]):
