@@ -124,6 +124,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const BatchDev& B = P.B;
   const int G = P.nq / P.nkv;
   griddep_launch_dependents();
+  if (threadIdx.x == 32) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
   if (threadIdx.x < NS) {
     mbar_init(bars + 8 * threadIdx.x, 1);
     issued_s[threadIdx.x] = 0;
@@ -131,22 +135,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) abort_s = 0;
+  __syncthreads();
   griddep_wait();
   auto work = [&](const SeqRows& s) -> SeqWork { return {P.nkv, s.n > 0 ? (s.start + s.n + UK - 1) / UK : 0}; };
   // every CTA has a unit for each warp, as far as the work goes
-  auto ctas_of = [&](long long total) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (total + WARPS - 1) / WARPS)); };
-  const WorkStart ws = batch_scan<THREADS>(
-      B, work, [&](long long total) { return range_begin(total, blockIdx.x, max(1, ctas_of(total))); }, nullptr, P.status);
-  const int ctas = ctas_of(ws.total), cta = blockIdx.x;
-  if (cta >= ctas) return;
-  const long long ub = range_begin(ws.total, cta, ctas);
-  const long long count = range_begin(ws.total, cta + 1, ctas) - ub;
+  const WorkStart ws = batch_scan<THREADS>(B, work, WARPS, nullptr, P.status);
+  const Line& line = ws.line;
+  const int cta = blockIdx.x;
+  if (cta >= line.ctas) return;
+  const int ub = line.begin(cta), count = line.begin(cta + 1) - ub;
 
   WorkCursor<decltype(work)> cur, iss;
   cur.seek(B, work, ws.b, ub - ws.first);
   // the warp's next copy: its place in the line, as a row of the cache (-1: none)
   iss = cur;
-  long long iu = warp;  // unit of the range
+  int iu = warp;  // unit of the range
   int irow = 0;
   auto locate = [&]() {
     int slot = batch_slot(B, iss.b, iss.u * UK);
@@ -187,11 +190,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;   // ldmatrix address of K: keys x chunks
   const int vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;  // of V (transposed)
-  long long x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
+  int x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
   int st = 0, ph = 0;         // the latter's stage of the warp's ring, and phase
   bool failed = false;
   while (x < count) {
-    const int u0 = cur.u, cnt = static_cast<int>(min(static_cast<long long>(cur.w.units - u0), count - x));
+    const int u0 = cur.u, cnt = min(cur.w.units - u0, count - x);
     const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
     float o[NB][DT][4], m[NB][2], l[NB][2];
     uint32_t qf[NB][KS][2];  // Q^T as the B operand: row 8 b + g
@@ -210,10 +213,29 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) qf[b][k][e] = r < R ? src[8 * k + 4 * e] : 0u;
     }
-    uint32_t see[NB][2];  // nodes that the lane's rows (columns 2t, 2t + 1 of each block of 8) see
-    bool have_see = false;
+    // nodes that the lane's rows (columns 2t, 2t + 1 of each block of 8) see, while the first unit is on its way
+    uint32_t see[NB][2];
+    const bool own_keys = (u0 + cnt) * UK > start;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * b + 2 * t + e, node = r / G;
+        see[b][e] = 0;
+        if (r >= R || !own_keys) continue;
+        if (B.parent == nullptr) {
+          see[b][e] = (2u << node) - 1u;
+        } else {
+          for (int j = node; j >= 0;) {
+            bool bad;
+            see[b][e] |= 1u << j;
+            j = tree_parent(B.parent + at, j, bad);
+            if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
+          }
+        }
+      }
     for (; i < x + cnt && !failed; i += WARPS) {
-      const int unit = u0 + static_cast<int>(i - x), key0 = unit * UK;
+      const int unit = u0 + i - x, key0 = unit * UK;
       const int stage = warp * L::WS + st;
       const uint32_t kt = ring + stage * (2 * L::TILE), vt = kt + L::TILE;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, ph, abort_flag))) {
@@ -229,27 +251,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();  // before the copy that refills the stage
         __syncwarp();
-      }
-      if (tail && !have_see) {
-        have_see = true;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 8 * b + 2 * t + e, node = r / G;
-            see[b][e] = 0;
-            if (r >= R) continue;
-            if (B.parent == nullptr) {
-              see[b][e] = (2u << node) - 1u;
-            } else {
-              for (int j = node; j >= 0;) {
-                bool bad;
-                see[b][e] |= 1u << j;
-                j = tree_parent(B.parent + at, j, bad);
-                if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
-              }
-            }
-          }
       }
       // scores of 32 keys: two tiles of 16
       float sc[NB][2][4];
@@ -367,9 +368,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
     };
     const bool whole = cnt == cur.w.units;
-    const long long task_first = ub + x - u0;
+    const int task_first = ub + x - u0;
     constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
-    float* mine = P.part + part_place(ws.total, cta, ctas, task_first) * PLACE;
+    float* mine = P.part + line.place(cta, task_first) * PLACE;
     for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
       float mw[WARPS], mr = -INFINITY, lr = 0.f;
 #pragma unroll
@@ -393,14 +394,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     if (!whole) {
-      const int c0 = range_owner(ws.total, task_first, ctas), c1 = range_owner(ws.total, task_first + cur.w.units - 1, ctas);
+      const int c0 = line.owner(task_first), c1 = line.owner(task_first + cur.w.units - 1);
       int* ctr = P.counters + cur.b * P.nkv + kvh;
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) last_s = atomicAdd(ctr, 1) == c1 - c0;
+      if (threadIdx.x == 0) {
+        __threadfence();  // the CTA's part, before the count
+        last_s = atomicAdd(ctr, 1) == c1 - c0;
+        __threadfence();  // the count, before the other parts
+      }
       __syncthreads();
       if (last_s) {
-        __threadfence();
+        const int place0 = line.place(c0, task_first);
         // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c
         for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float2 ml[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
-              const float* src = P.part + part_place(ws.total, min(c + y, c1), ctas, task_first) * PLACE;
+              const float* src = P.part + static_cast<size_t>(c + y == c0 ? place0 : 2 * min(c + y, c1)) * PLACE;
               v[y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
               ml[y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
             }

@@ -35,6 +35,7 @@ namespace {
 constexpr int TM = 128;      // rows of a slot
 constexpr int BLOCK = 256;   // rows of a task
 constexpr int TK = 128;      // keys per tile
+constexpr int HK = TK / 2;   // keys that a softmax thread holds at once
 constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;
 constexpr float RESCALE_LOG2 = 8.f;
@@ -54,7 +55,8 @@ struct TcParams {
   int nq, nkv, layer;
   float scale_log2;
   __half* out;
-  long long* plan;  // [0] total units, [1] CTAs, then the first unit of every sequence
+  Line* line;       // the launch's line, for the merge
+  int* prefix;      // the first unit of every sequence
   float* part;      // two places a CTA: [HD / 4][rows] float4, then (m, l) per row
   int part_rows;
   int* status;
@@ -116,17 +118,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto kv_full = [&](int s) { return bar0 + 8u * s; };
   auto kv_empty = [&](int s) { return bar0 + 8u * (NS + s); };
   auto s_full = [&](int s) { return bar0 + 8u * (2 * NS + s); };
-  auto p_full = [&](int s) { return bar0 + 8u * (2 * NS + 2 + s); };
-  auto o_done = [&](int s) { return bar0 + 8u * (2 * NS + 4 + s); };
-  auto o_empty = [&](int s) { return bar0 + 8u * (2 * NS + 6 + s); };
-  const uint32_t q_full = bar0 + 8u * (2 * NS + 8), q_empty = q_full + 8, drain_bar = q_full + 16;
+  auto p_full = [&](int s, int h) { return bar0 + 8u * (2 * NS + 2 + 2 * s + h); };
+  auto o_done = [&](int s) { return bar0 + 8u * (2 * NS + 6 + s); };
+  auto o_empty = [&](int s) { return bar0 + 8u * (2 * NS + 10 + s); };
+  const uint32_t q_full = bar0 + 8u * (2 * NS + 12), q_empty = q_full + 8, drain_bar = q_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (q_full + 24 - raw));
-  static_assert(8 * (2 * NS + 12) <= 512, "barrier area");
+  static_assert(8 * (2 * NS + 16) <= 512, "barrier area");
   const BatchDev& B = P.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = P.nq / P.nkv;
 
-  griddep_launch_dependents();
+  if (threadIdx.x == 64) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(kv_full(s), 1);
@@ -134,7 +140,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), TM);
+      mbar_init(p_full(s, 0), TM);
+      mbar_init(p_full(s, 1), TM);
       mbar_init(o_done(s), 1);
       mbar_init(o_empty(s), TM);
     }
@@ -158,22 +165,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     return {P.nkv * ((s.n * G + BLOCK - 1) / BLOCK), s.n > 0 ? (s.start + s.n + TK - 1) / TK : 0};
   };
   // a tile for each slot, as far as the work goes
-  auto ctas_of = [&](long long total) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (total + 1) / 2)); };
   const int cta = blockIdx.x;
-  const WorkStart ws = batch_scan<THREADS>(
-      B, work, [&](long long total) { return range_begin(total, cta, max(1, ctas_of(total))); }, cta == 0 ? P.plan + 2 : nullptr,
-      P.status);
-  const int ctas = ctas_of(ws.total);
-  if (cta == 0 && threadIdx.x == 0) {
-    P.plan[0] = ws.total;
-    P.plan[1] = ctas;
-  }
-  const long long ub = range_begin(ws.total, cta, max(1, ctas));
-  const long long count = cta < ctas ? range_begin(ws.total, cta + 1, ctas) - ub : 0;
+  const WorkStart ws = batch_scan<THREADS>(B, work, 2, cta == 0 ? P.prefix : nullptr, P.status);
+  const Line& line = ws.line;
+  if (cta == 0 && threadIdx.x == 0) *P.line = line;
+  const int ub = cta < line.ctas ? line.begin(cta) : 0;
+  const int count = cta < line.ctas ? line.begin(cta + 1) - ub : 0;
   WorkCursor<decltype(work)> cur;
   if (count > 0) cur.seek(B, work, ws.b, ub - ws.first);
   // the part of the task at the cursor that lies in this CTA's range, x units of which are done
-  auto part = [&](long long x) -> Part {
+  auto part = [&](int x) -> Part {
     Part p;
     const int blocks = cur.w.tasks / P.nkv;
     p.kvh = cur.task / blocks;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     p.rows = min(BLOCK, p.n * G - p.rb * BLOCK);
     p.slots = p.rows > TM ? 2 : 1;
     p.u0 = cur.u;
-    p.cnt = static_cast<int>(min(static_cast<long long>(cur.w.units - cur.u), count - x));
+    p.cnt = min(cur.w.units - cur.u, count - x);
     return p;
   };
   // Order of a part's tiles in the ring: slots == 2: K0 V0 K1 V1 ..; slots == 1: K0 K1 V0 K2 V1 .. (the other
@@ -193,61 +194,73 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto place_v = [](const Part& p, int j) { return p.slots == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.cnt - 1); };
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      int c = 0, seg = 0, last_slots = 0, q_issued = 0;
-      bool ok = true;
-      for (long long x = 0; x < count && ok; ++seg) {
-        const Part p = part(x);
-        const int row0 = (P.layer * P.nkv + p.kvh) * B.slots;
-        auto tile_row = [&](int j) {
-          int slot = batch_slot(B, cur.b, (p.u0 + j) * TK);
+    // ------------------------------------------------------------------ copies (lane 0; a lane each looks up the tiles' pages)
+    int c = 0, seg = 0, last_slots = 0, q_issued = 0;
+    bool ok = true;
+    for (int x = 0; x < count && ok; ++seg) {
+      const Part p = part(x);
+      const int row0 = (P.layer * P.nkv + p.kvh) * B.slots;
+      auto tile_row = [&](int j) {  // of tile j + lane
+        int slot = 0;
+        if (j + lane < p.cnt) {
+          slot = batch_slot(B, cur.b, (p.u0 + j + lane) * TK);
           if (slot < 0) {
             batch_record(P.status, PF_ERR_KV_CAPACITY);
             slot = 0;
           }
-          return row0 + slot;
-        };
-        auto load = [&](const CUtensorMap* map, int row) {
-          const int s = c % NS;
-          if (!mbar_wait(kv_empty(s), ((c / NS) & 1) ^ 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(kv_full(s), L::KV);
-          for (int h = 0; h < NH; ++h) tma_load_2d(kv_s + s * L::KV + h * (TK * 128), map, h * 64, row, kv_full(s));
-          ++c;
-          return true;
-        };
-        auto load_q = [&]() {
-          if (seg > 0 && !mbar_wait(q_empty, (seg - 1) & 1, abort_flag)) return false;
-          // slot 1's Q may still be the exchange buffer of the part before
-          if (seg > 0 && p.slots == 2 && last_slots == 1 &&
-              !(mbar_wait(o_empty(0), (seg - 1) & 1, abort_flag) && mbar_wait(o_empty(1), (seg - 1) & 1, abort_flag)))
-            return false;
-          mbar_arrive_expect_tx(q_full, p.slots * L::QT);
-          for (int s = 0; s < p.slots; ++s)
-            for (int h = 0; h < NH; ++h)
-              tma_load_3d(q_s + s * L::QT + h * (TM * 128), &tm_q, h * 64, p.kvh * G, p.at + (p.rb * BLOCK + s * TM) / G, q_full);
-          ++q_issued;
-          return true;
-        };
-        const int lag = p.slots == 2 ? 0 : 1;  // V follows K by so many tiles
-        int rk = tile_row(0), rv = rk;
-        for (int j = 0; j < p.cnt + lag && ok; ++j) {
-          const int next = j + 1 < p.cnt ? tile_row(j + 1) : 0;  // a tile ahead: its table entry's latency lies behind the waits
-          if (j < p.cnt) ok = load(&tm_k, rk);
-          if (ok && j >= lag) ok = load(&tm_v, lag ? rv : rk);
-          rv = rk;
-          rk = next;
-          // at most four tiles before Q: the ring takes them without this part's products
-          if (ok && j == min(1, p.cnt + lag - 1)) ok = load_q();
         }
-        last_slots = p.slots;
-        x += p.cnt;
-        if (x < count) cur.advance(B, work, p.cnt);
+        return row0 + slot;
+      };
+      auto load = [&](const CUtensorMap* map, int row) {
+        const int s = c % NS;
+        if (ok && lane == 0) {
+          ok = mbar_wait(kv_empty(s), ((c / NS) & 1) ^ 1, abort_flag);
+          if (ok) {
+            mbar_arrive_expect_tx(kv_full(s), L::KV);
+            for (int h = 0; h < NH; ++h) tma_load_2d(kv_s + s * L::KV + h * (TK * 128), map, h * 64, row, kv_full(s));
+            ++c;
+          }
+        }
+      };
+      auto load_q = [&]() {
+        if (ok && lane == 0) {
+          if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, abort_flag);
+          // slot 1's Q may still be the exchange buffer of the part before
+          if (ok && seg > 0 && p.slots == 2 && last_slots == 1)
+            ok = mbar_wait(o_empty(0), (seg - 1) & 1, abort_flag) && mbar_wait(o_empty(1), (seg - 1) & 1, abort_flag);
+          if (ok) {
+            mbar_arrive_expect_tx(q_full, p.slots * L::QT);
+            for (int s = 0; s < p.slots; ++s)
+              for (int h = 0; h < NH; ++h)
+                tma_load_3d(q_s + s * L::QT + h * (TM * 128), &tm_q, h * 64, p.kvh * G, p.at + (p.rb * BLOCK + s * TM) / G, q_full);
+            ++q_issued;
+          }
+        }
+      };
+      int rows = tile_row(0), rows_next = tile_row(32);  // 32 tiles, and the 32 after them
+      if (seg == 0) load_q();
+      const int lag = p.slots == 2 ? 0 : 1;  // V follows K by so many tiles
+      int rv = 0;
+      for (int j = 0; j < p.cnt + lag && ok; ++j) {
+        if (j > 0 && (j & 31) == 0) {
+          rows = rows_next;
+          rows_next = tile_row(j + 32);
+        }
+        const int rk = __shfl_sync(0xffffffffu, rows, j & 31);
+        if (j < p.cnt) load(&tm_k, rk);
+        if (j >= lag) load(&tm_v, lag ? rv : rk);
+        rv = rk;
+        // at most four tiles before a later part's Q: the ring takes them without this part's products
+        if (seg > 0 && j == min(1, p.cnt + lag - 1)) load_q();
+        ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
       }
-      if (*abort_flag) {  // let copies in flight land before shared memory is released
-        if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
-        for (int k = max(0, c - NS); k < c; ++k) drain(kv_full(k % NS), (k / NS) & 1);
-      }
+      last_slots = p.slots;
+      x += p.cnt;
+      if (x < count) cur.advance(B, work, p.cnt);
+    }
+    if (lane == 0 && *abort_flag) {  // let copies in flight land before shared memory is released
+      if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
+      for (int k = max(0, c - NS); k < c; ++k) drain(kv_full(k % NS), (k / NS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
@@ -263,19 +276,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                          sdesc_kmajor_sw128(k + (kc >> 2) * (TK * 128) + (kc & 3) * 32), idesc_s, kc > 0);
       umma_commit_warp(s_full(slot));
     };
-    auto values = [&](int slot, int c, bool add) {
+    // the product with the V rows of a half of the tile's keys
+    auto values = [&](int slot, int h, int c, bool add) {
       tc_fence_after();
-      const uint32_t v = kv_s + (c % NS) * L::KV;
+      const uint32_t v = kv_s + (c % NS) * L::KV + h * (HK * 128);
 #pragma unroll
-      for (int kc = 0; kc < TK / 16; ++kc)
-        umma_f16_ts_warp(tmem + 256 + slot * TK, tmem + slot * TK + (kc >> 2) * 64 + (kc & 3) * 8, sdesc_mnmajor_sw128(v + kc * 2048, TK * 128), idesc_o,
+      for (int kc = 0; kc < HK / 16; ++kc)
+        umma_f16_ts_warp(tmem + 256 + slot * TK, tmem + slot * TK + h * HK + kc * 8, sdesc_mnmajor_sw128(v + kc * 2048, TK * 128), idesc_o,
                          add || kc > 0);
-      umma_commit_warp(o_done(slot));
     };
     int c0 = 0, seg = 0;
     int pc[2] = {0, 0};  // P tiles taken of each slot
     bool ok = true;
-    for (long long x = 0; x < count && ok; ++seg) {
+    for (int x = 0; x < count && ok; ++seg) {
       const Part p = part(x);
       auto free_kv = [&](int c) { umma_commit_warp(kv_empty(c % NS)); };
       if (!(ok = wait(q_full, seg & 1))) break;
@@ -290,9 +303,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int v = c0 + place_v(p, j), k = c0 + place_k(p, j + 1);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (!(ok = ok && wait(p_full(s), pc[s] & 1) && wait_kv(v))) break;
+            if (!(ok = ok && wait(p_full(s, 1), pc[s] & 1) && wait_kv(v))) break;
+            values(s, 1, v, j > 0);
+            if (!(ok = wait(p_full(s, 0), pc[s] & 1))) break;
+            values(s, 0, v, true);
+            umma_commit_warp(o_done(s));
             ++pc[s];
-            values(s, v, j > 0);
             if (s == 1) free_kv(v);
             if (j + 1 < p.cnt) {
               if (!(ok = wait_kv(k))) break;
@@ -316,9 +332,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (seg > 0 && !(ok = wait(o_empty(0), (seg - 1) & 1) && wait(o_empty(1), (seg - 1) & 1))) break;
         for (int j = 0; j < p.cnt && ok; ++j) {
           const int s = j & 1, v = c0 + place_v(p, j), k = c0 + place_k(p, j + 2);
-          if (!(ok = wait(p_full(s), pc[s] & 1) && wait_kv(v))) break;
+          if (!(ok = wait(p_full(s, 1), pc[s] & 1) && wait_kv(v))) break;
+          values(s, 1, v, j >= 2);
+          if (!(ok = wait(p_full(s, 0), pc[s] & 1))) break;
+          values(s, 0, v, true);
+          umma_commit_warp(o_done(s));
           ++pc[s];
-          values(s, v, j >= 2);
           free_kv(v);
           if (j + 2 < p.cnt) {
             if (!(ok = wait_kv(k))) break;
@@ -345,13 +364,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     int c0 = 0, done = 0;  // tiles of the parts before; tiles of this slot
     bool ok = true;
     // tcgen05.ld / st are warp-collective: every branch around them is warp-uniform
-    for (long long x = 0; x < count; ) {
+    for (int x = 0; x < count; ) {
       const Part p = part(x);
       const int row = p.rb * BLOCK + (p.slots == 2 ? slot * TM : 0) + r;  // row of the sequence and kv head
       const int node = row / G;
       const bool mine = r < p.rows - (p.slots == 2 ? slot * TM : 0);
       float m = -INFINITY, l = 0.f;
       const int step = p.slots == 2 ? 1 : 2, j0 = p.slots == 2 ? 0 : slot;
+      // key r of a tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN. Each slot
+      // clears it before its own product.
+      auto clear_v = [&](int j) {
+        const int c = c0 + place_v(p, j);
+        const uint32_t vt = kv_s + (c % NS) * L::KV + r * 128;
+        ok = mbar_wait(kv_full(c % NS), (c / NS) & 1, abort_flag);
+        for (int y = 0; y < NH * 8; ++y)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (y >> 3) * (TK * 128) + (y & 7) * 16), "r"(0) : "memory");
+        fence_proxy_async_smem();
+      };
       for (int j = j0; j < p.cnt; j += step) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(slot), done & 1, abort_flag)))) break;
         tc_fence_after();
@@ -432,22 +461,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             pk[e] = pack2<BF16>(p0, p1);
           }
           tmem_st_32x32b_x32(sbuf + 64 * h, pk);
+          if (h == 1) {  // the second half's product starts while the first half's weights are formed
+            if (r >= nvalid && r >= 64) clear_v(j);
+            tmem_st_wait();
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_before();
+            mbar_arrive(p_full(slot, 1));
+          }
         }
+        if (!ok) break;
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        if (r >= nvalid) {
-          // key r of the tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN.
-          // Each slot clears it before its own product.
-          const int c = c0 + place_v(p, j);
-          const uint32_t vt = kv_s + (c % NS) * L::KV + r * 128;
-          ok = mbar_wait(kv_full(c % NS), (c / NS) & 1, abort_flag);
-          for (int y = 0; y < NH * 8; ++y)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (y >> 3) * (TK * 128) + (y & 7) * 16), "r"(0) : "memory");
-          fence_proxy_async_smem();
-        }
+        if (r >= nvalid && r < 64) clear_v(j);
         tmem_st_wait();
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_before();
-        mbar_arrive(p_full(slot));
+        mbar_arrive(p_full(slot, 0));
         ++done;
       }
       // ------------------------------------------------------------------ the part's end
@@ -456,8 +484,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!bar_and(1, SM_THREADS, ok)) break;
       tc_fence_after();
       const bool whole = p.cnt == cur.w.units;
-      const long long task_first = ub + x - p.u0;
-      float* place = P.part + part_place(ws.total, cta, max(1, ctas), task_first) * (static_cast<size_t>(P.part_rows) * (HD + 2));
+      const int task_first = ub + x - p.u0;
+      float* place = P.part + line.place(cta, task_first) * (static_cast<size_t>(P.part_rows) * (HD + 2));
       __half* dst = P.out + (static_cast<size_t>(p.at + node) * P.nq + p.kvh * G + (row - node * G)) * HD;
       const int pr = row - p.rb * BLOCK;  // row of the place
       // 32 columns of the row's O: to the output, or as they are to the part's place
@@ -548,6 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  griddep_launch_dependents();  // not earlier: a merge that starts while few SMs are free gathers on those
   if (warp == 1) {
     tc_fence_after();
     __syncwarp();
@@ -557,34 +586,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
-// CTA = 32 rows of a (sequence, kv head), a thread per row and eight columns; parts that saw no key of a row hold no O.
-constexpr int MERGE_ROWS = 32;
-
-template <int HD>
-__global__ void __launch_bounds__(MERGE_ROWS* HD / 8) tree_merge_kernel(const BatchDev B, int nq, int nkv, const long long* plan,
+// CTA = MERGE_ROWS rows of a (sequence, kv head), a thread per row and eight columns; parts that saw no key of a row hold
+// no O. Eight rows a CTA spread few rows with many parts over the SMs (one tree of 26 nodes at 8,189: 18.5 us with the
+// attention, 23 with 32 rows); many rows take 32, since CTAs start at about 200 a microsecond.
+template <int HD, int MERGE_ROWS>
+__global__ void __launch_bounds__(MERGE_ROWS* HD / 8) tree_merge_kernel(const BatchDev B, int nq, int nkv, const Line* line_p, const int* prefix,
                                                                         const float* part, int part_rows, __half* out) {
   PF_TIMELINE(TL_TREE_MERGE);
   griddep_launch_dependents();
   griddep_wait();
   const int b = blockIdx.z, kvh = blockIdx.y, G = nq / nkv;
   const SeqRows s = batch_seq(B, b, true);
-  const int row = blockIdx.x * MERGE_ROWS + (threadIdx.x & 31), oct = threadIdx.x >> 5;
+  const int row = blockIdx.x * MERGE_ROWS + threadIdx.x % MERGE_ROWS, oct = threadIdx.x / MERGE_ROWS;
   if (static_cast<int>(blockIdx.x) * MERGE_ROWS >= s.n * G) return;
-  const long long total = plan[0], seq_first = plan[2 + b];
-  const int ctas = static_cast<int>(plan[1]);
+  const Line line = *line_p;
   const int rb = row / BLOCK, blocks = (s.n * G + BLOCK - 1) / BLOCK, units = (s.start + s.n + TK - 1) / TK;
-  const long long first = seq_first + static_cast<long long>(kvh * blocks + rb) * units;
-  const int c0 = range_owner(total, first, ctas), c1 = range_owner(total, first + units - 1, ctas);
+  const int first = prefix[b] + (kvh * blocks + rb) * units;
+  const int c0 = line.owner(first), c1 = line.owner(first + units - 1);
   if (c0 == c1 || row >= s.n * G) return;
-  const int pr = row - rb * BLOCK;
+  const int pr = row - rb * BLOCK, place0 = line.place(c0, first);
   float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  constexpr int Q = 4;  // parts in flight
+  constexpr int Q = 8;  // parts in flight
   for (int c = c0; c <= c1; c += Q) {
     float4 v[Q][2];
     float2 ml[Q];
 #pragma unroll
     for (int y = 0; y < Q; ++y) {
-      const float* src = part + part_place(total, min(c + y, c1), ctas, first) * (static_cast<size_t>(part_rows) * (HD + 2));
+      const float* src = part + (c + y == c0 ? place0 : 2 * min(c + y, c1)) * (static_cast<size_t>(part_rows) * (HD + 2));
       ml[y] = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(part_rows) * HD) + pr);
 #pragma unroll
       for (int u = 0; u < 2; ++u) v[y][u] = __ldcg(reinterpret_cast<const float4*>(src) + static_cast<size_t>(2 * oct + u) * part_rows + pr);
@@ -612,7 +640,9 @@ __global__ void __launch_bounds__(MERGE_ROWS* HD / 8) tree_merge_kernel(const Ba
   *reinterpret_cast<uint4*>(out + (static_cast<size_t>(s.at + node) * nq + kvh * G + row - node * G) * HD + 8 * oct) = make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-size_t plan_bytes(int n_seq) { return (static_cast<size_t>(n_seq) + 2 + 31) / 32 * 32 * sizeof(long long); }
+constexpr size_t LINE_BYTES = 64;
+static_assert(sizeof(Line) <= LINE_BYTES, "the line's place in the scratch");
+size_t plan_bytes(int n_seq) { return LINE_BYTES + (static_cast<size_t>(n_seq) + 63) / 64 * 64 * sizeof(int); }
 int place_rows(const pf_config& c, int max_rows) { return std::min(BLOCK, (max_rows * (c.n_q_heads / c.n_kv_heads) + 31) / 32 * 32); }
 
 template <int HD, int BF16>
@@ -637,16 +667,22 @@ cudaError_t launch_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   p.out = static_cast<__half*>(a.out);
   uint8_t* at = static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c);
-  p.plan = reinterpret_cast<long long*>(at);
+  p.line = reinterpret_cast<Line*>(at);
+  p.prefix = reinterpret_cast<int*>(at + LINE_BYTES);
   p.part = reinterpret_cast<float*>(at + plan_bytes(a.b->n_seq));
   p.part_rows = place_rows(c, max_rows);
   p.status = a.status;
   const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
   const cudaError_t e = launch_pdl(attn_tree_tc_kernel<HD, BF16>, dim3(ctas), dim3(THREADS), TSmem<HD>::BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_merge_kernel<HD>, dim3((max_rows * G + MERGE_ROWS - 1) / MERGE_ROWS, c.n_kv_heads, a.b->n_seq),
-                    dim3(MERGE_ROWS * HD / 8), 0, stream, p.B, p.nq, p.nkv, static_cast<const long long*>(p.plan),
-                    static_cast<const float*>(p.part), p.part_rows, p.out);
+  const int rows = max_rows * G;
+  auto merge = [&](auto kernel, int per) {
+    return launch_pdl(kernel, dim3((rows + per - 1) / per, c.n_kv_heads, a.b->n_seq), dim3(per * HD / 8), 0, stream, p.B, p.nq, p.nkv,
+                      static_cast<const Line*>(p.line), static_cast<const int*>(p.prefix), static_cast<const float*>(p.part),
+                      p.part_rows, p.out);
+  };
+  const int64_t small = static_cast<int64_t>((rows + 7) / 8) * c.n_kv_heads * a.b->n_seq;
+  return small <= 4 * ctas ? merge(tree_merge_kernel<HD, 8>, 8) : merge(tree_merge_kernel<HD, 32>, 32);
 }
 
 template <int HD, int BF16>

@@ -52,54 +52,122 @@ __device__ __forceinline__ int tree_parent(const int* parent, int i, bool& bad) 
 }
 
 // ------------------------------------------------------------------ work of a batch cut into even ranges
-// The attention kernels lay the work of all sequences in one line: sequence b has `tasks` tasks (a kv head, or a kv
-// head and a block of rows) of `units` key units each, one after the other. CTA c of C takes units [W c / C, W (c + 1) / C),
-// however the lengths lie; a task that a border cuts has one part per CTA.
+// The attention kernels lay the work of all sequences in one line of fewer than 2^31 units: sequence b has `tasks` tasks
+// (a kv head, or a kv head and a block of rows) of `units` key units each, one after the other. CTA c takes
+// units [begin(c), begin(c + 1)), however the lengths lie; a task that a border cuts has one part per CTA.
 struct SeqWork {
   int tasks, units;
 };
 
-// First unit of sequence b0 that unit `at` lies in, and W, from a scan over all sequences (all threads of the CTA;
-// `work` gives a sequence's SeqWork). `prefix` (may be NULL): receives the first unit of every sequence.
-struct WorkStart {
-  long long total, first;  // W; first unit of sequence b
-  int b;
+struct Line {
+  int total, ctas;  // units; CTAs that have any
+  int q, rem;       // the first `rem` of a run of CTAs take q + 1 units, the others q
+  int parts, task;  // one sequence, no more tasks than CTAs: each task is a run of `parts` CTAs and of `task` units; else 0
+  // `fill`: units that keep a CTA busy at once
+  __device__ __forceinline__ void cut(int total_, int n_seq, const SeqWork& w, int grid, int fill) {
+    total = total_;
+    parts = 0;
+    if (n_seq == 1 && w.tasks > 0 && w.tasks <= grid && total > 0) {
+      task = w.units;
+      parts = min(grid / w.tasks, (w.units + fill - 1) / fill);
+      ctas = parts * w.tasks;
+      q = task / parts;
+      rem = task - q * parts;
+    } else {
+      ctas = min(grid, (total + fill - 1) / fill);
+      q = ctas > 0 ? total / ctas : 0;
+      rem = total - q * ctas;
+    }
+  }
+  __device__ __forceinline__ int begin(int c) const {
+    if (parts == 0) return c * q + min(c, rem);
+    const int t = c / parts, p = c - t * parts;
+    return t * task + p * q + min(p, rem);
+  }
+  // the CTA whose range holds `unit`
+  __device__ __forceinline__ int owner(int unit) const {
+    int run = 0;
+    if (parts != 0) {
+      const int t = unit / task;
+      run = t * parts;
+      unit -= t * task;
+    }
+    const int wide = rem * (q + 1);
+    return run + (unit < wide ? unit / (q + 1) : rem + (unit - wide) / q);
+  }
+  // Parts of a cut task lie in scratch by CTA: a task that began before the CTA's range (or with it) in its place 0, one
+  // that begins inside it in place 1 (only the task's first part may).
+  __device__ __forceinline__ int place(int c, int task_first) const { return 2 * c + (task_first > begin(c) ? 1 : 0); }
 };
-template <int THREADS, typename Work, typename At>
-__device__ __forceinline__ WorkStart batch_scan(const BatchDev& B, Work work, At at, long long* prefix, int* status) {
+
+// The line of a batch, and the first unit of the sequence b that this CTA's range begins in (all threads of the CTA;
+// work(s): a sequence's SeqWork). `prefix` (may be NULL) receives the first unit of every sequence.
+struct WorkStart {
+  Line line;
+  int first, b;
+};
+template <int THREADS, typename Work>
+__device__ __forceinline__ WorkStart batch_scan(const BatchDev& B, Work work, int fill, int* prefix, int* status) {
   constexpr int NW = THREADS / 32, PER = (PF_MAX_SEQS + THREADS - 1) / THREADS;
-  __shared__ long long warp_sum[NW];
-  __shared__ long long first_s;
-  __shared__ int b_s;
-  const int per = (B.n_seq + THREADS - 1) / THREADS, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
+  WorkStart r;
+  if (B.n_seq <= 32) {  // every warp by itself, a sequence a lane
+    SeqWork w{0, 0};
+    if (lane < B.n_seq) {
+      const SeqRows s = batch_seq(B, lane, true);
+      if (s.err != PF_OK && cta == 0 && warp == 0) batch_record(status, s.err);
+      w = work(s);
+    }
+    const int mine = w.tasks * w.units;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, inc, 31);
+    w.tasks = __shfl_sync(0xffffffffu, w.tasks, 0);
+    w.units = __shfl_sync(0xffffffffu, w.units, 0);
+    r.line.cut(total, B.n_seq, w, gridDim.x, fill);
+    const int before = inc - mine, unit = cta < r.line.ctas ? r.line.begin(cta) : 0;
+    if (prefix != nullptr && warp == 0 && lane < B.n_seq) prefix[lane] = before;
+    const unsigned here = __ballot_sync(0xffffffffu, unit >= before && unit < inc);
+    r.b = here != 0 ? __ffs(here) - 1 : 0;
+    r.first = __shfl_sync(0xffffffffu, before, r.b);
+    return r;
+  }
+  __shared__ int warp_sum[NW];
+  __shared__ int first_s, b_s;
+  const int per = (B.n_seq + THREADS - 1) / THREADS;
   const int b0 = threadIdx.x * per;
-  long long mine[PER], sum = 0;
+  int mine[PER], sum = 0;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
     mine[x] = 0;
     if (x < per && b0 + x < B.n_seq) {
       const SeqRows s = batch_seq(B, b0 + x, true);
-      if (s.err != PF_OK && blockIdx.x == 0) batch_record(status, s.err);
+      if (s.err != PF_OK && cta == 0) batch_record(status, s.err);
       const SeqWork w = work(s);
-      mine[x] = static_cast<long long>(w.tasks) * w.units;
+      mine[x] = w.tasks * w.units;
     }
     sum += mine[x];
   }
-  long long inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  long long before = inc - sum, total = 0;
+  int before = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const long long unit = at(total);
+  r.line.cut(total, B.n_seq, SeqWork{0, 0}, gridDim.x, fill);
+  const int unit = cta < r.line.ctas ? r.line.begin(cta) : 0;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
     if (x < per && b0 + x < B.n_seq) {
@@ -112,21 +180,23 @@ __device__ __forceinline__ WorkStart batch_scan(const BatchDev& B, Work work, At
     }
   }
   __syncthreads();
-  return {total, first_s, b_s};
+  r.first = first_s;
+  r.b = b_s;
+  return r;
 }
 
-// A place in that line, walked forward.
+// A place in the line, walked forward.
 template <typename Work>
 struct WorkCursor {
   int b, task, u;
   SeqRows s;
   SeqWork w;
-  __device__ __forceinline__ void seek(const BatchDev& B, Work work, int b_, long long off) {
+  __device__ __forceinline__ void seek(const BatchDev& B, Work work, int b_, int off) {
     b = b_;
     s = batch_seq(B, b, true);
     w = work(s);
-    task = static_cast<int>(off / w.units);
-    u = static_cast<int>(off - static_cast<long long>(task) * w.units);
+    task = off / w.units;
+    u = off - task * w.units;
   }
   // d units on; the caller knows that the line reaches that far
   __device__ __forceinline__ void advance(const BatchDev& B, Work work, int d) {
@@ -136,7 +206,7 @@ struct WorkCursor {
       if (++task == w.tasks) {
         task = 0;
         do {
-          if (++b >= B.n_seq) {  // past the end: only after the last unit
+          if (++b >= B.n_seq) {  // never, as long as the caller is right
             b = B.n_seq - 1;
             w = {1, 0x7fffffff};
             return;
@@ -149,14 +219,8 @@ struct WorkCursor {
   }
 };
 
-__device__ __forceinline__ long long range_begin(long long total, int c, int ctas) { return total * c / ctas; }
-// The CTA whose range holds `unit`.
-__device__ __forceinline__ int range_owner(long long total, long long unit, int ctas) {
-  return static_cast<int>(((unit + 1) * ctas - 1) / total);
-}
-// Parts of a cut task lie in scratch by CTA: a task that began before the CTA's range in its place 0, one that begins in it in place 1.
-__device__ __forceinline__ int part_place(long long total, int c, int ctas, long long task_first) {
-  return 2 * c + (task_first > range_begin(total, c, ctas) ? 1 : 0);
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 }  // namespace pf

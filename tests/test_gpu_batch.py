@@ -525,6 +525,7 @@ def test_layer_of_several_requests():
         step()
     out.copy_(x)
     graph.replay()
+    pf.pf_status_read(s.status)
     got2 = out.double().cpu().numpy()
     assert (np.linalg.norm(got2 - ref, axis=1) / np.linalg.norm(ref, axis=1)).max() < 5e-3
 
