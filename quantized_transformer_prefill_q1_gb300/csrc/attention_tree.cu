@@ -41,8 +41,9 @@ struct FSmem {
   static constexpr int RING = NS * 2 * TILE;
   static constexpr int ROWS = 8 * NB;
   static constexpr int OW = HD + 4;  // floats between rows of the warps' O
+  static constexpr int NM = NB == 1 ? 2 : 1;  // merge buffers
   static constexpr int MERGE = WARPS * ROWS * (OW + 2) * 4;
-  static constexpr int BYTES = 1024 + RING + MERGE + NS * 8;
+  static constexpr int BYTES = 1024 + RING + NM * MERGE + NS * 8;
   static_assert(BYTES <= 232448 - 384, "shared memory");  // beside the static arrays
 };
 
@@ -84,6 +85,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -114,12 +116,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int KS = HD / 16, DT = HD / 16, NH = HD / 64, ROWS = L::ROWS, NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_s, last_s;
+  __shared__ int arrived_s[L::NM], turn_s[L::NM];  // of each merge buffer: warps whose part is in, tasks it has served
   __shared__ int issued_s[NS];  // copies that each stage has taken (its own warp's lane 0 counts)
   volatile int* abort_flag = &abort_s;
   const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
-  float* os = reinterpret_cast<float*>(smem_raw + (ring - raw) + L::RING);  // the warps' O [warp][row][OW], then (m, l)
-  float2* mls = reinterpret_cast<float2*>(os + WARPS * ROWS * L::OW);
-  const uint32_t bars = ring + L::RING + L::MERGE;
+  const uint32_t bars = ring + L::RING + L::NM * L::MERGE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const BatchDev& B = P.B;
   const int G = P.nq / P.nkv;
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) abort_s = 0;
+  if (threadIdx.x < L::NM) arrived_s[threadIdx.x] = turn_s[threadIdx.x] = 0;
   __syncthreads();
   griddep_wait();
   auto work = [&](const SeqRows& s) -> SeqWork { return {P.nkv, s.n > 0 ? (s.start + s.n + UK - 1) / UK : 0}; };
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;  // of V (transposed)
   int x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
   int st = 0, ph = 0;         // the latter's stage of the warp's ring, and phase
-  bool failed = false;
-  while (x < count) {
+  bool failed = false;  // after a timeout a warp goes on without its units, so that the others never wait for it
+  for (int k = 0; x < count; ++k) {
     const int u0 = cur.u, cnt = min(cur.w.units - u0, count - x);
     const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
     float o[NB][DT][4], m[NB][2], l[NB][2];
@@ -212,6 +214,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) qf[b][k][e] = r < R ? src[8 * k + 4 * e] : 0u;
+    }
+    // the next task's rows and tree towards L1
+    WorkCursor<decltype(work)> nxt = cur;
+    if (x + cnt < count) {
+      nxt.advance(B, work, cnt);
+      const int r = lane / NH;
+      if (r < nxt.s.n * G)
+        prefetch_l1(P.q + (static_cast<size_t>(nxt.s.at + r / G) * P.nq + nxt.task * G + r % G) * HD + 64 * (lane % NH));
+      if (B.parent != nullptr && lane == 0) prefetch_l1(B.parent + nxt.s.at);
     }
     // nodes that the lane's rows (columns 2t, 2t + 1 of each block of 8) see, while the first unit is on its way
     uint32_t see[NB][2];
@@ -341,7 +352,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         ph ^= 1;
       }
     }
-    // the warps' parts of this task meet
+    // The warps' parts of this task meet in a buffer: of a task that lies in this CTA, the warp that comes last adds them
+    // while the others go on.
+    const int mb = k % L::NM, turn = k / L::NM;
+    float* os = reinterpret_cast<float*>(smem_raw + (ring - raw) + L::RING + mb * L::MERGE);  // O [warp][row][OW], then (m, l)
+    float2* mls = reinterpret_cast<float2*>(os + WARPS * ROWS * L::OW);
+    if (turn > 0 && !failed) {
+      const uint64_t w0 = global_timer_ns();
+      while (*reinterpret_cast<volatile int*>(turn_s + mb) < turn && !failed) {
+        if (*abort_flag || global_timer_ns() - w0 > PF_WAIT_LIMIT_NS) {
+          *abort_flag = 1;
+          failed = true;
+        }
+      }
+      failed = __any_sync(0xffffffffu, failed);
+      __threadfence_block();
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -358,8 +384,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           dst[16 * d + 8] = o[b][d][e + 2];
         }
       }
-    failed = __syncthreads_or(failed) != 0;
-    if (failed) break;
     constexpr int LPR = HD / 4;  // threads per row, four columns each
     const int col = (threadIdx.x % LPR) * 4;
     auto store_out = [&](int r, float4 v, float f) {
@@ -367,12 +391,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD + col) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
     };
-    const bool whole = cnt == cur.w.units;
-    const int task_first = ub + x - u0;
-    constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
-    float* mine = P.part + line.place(cta, task_first) * PLACE;
-    for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
-      float mw[WARPS], mr = -INFINITY, lr = 0.f;
+    // row r of the warps' parts: its maximum, sum and the thread's four columns
+    auto add_row = [&](int r, float& mr, float& lr) {
+      float mw[WARPS];
+      mr = -INFINITY;
+      lr = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
         mw[w] = mls[w * ROWS + r].x;
@@ -386,20 +409,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         lr = fmaf(a, mls[w * ROWS + r].y, lr);
         acc = make_float4(fmaf(a, v.x, acc.x), fmaf(a, v.y, acc.y), fmaf(a, v.z, acc.z), fmaf(a, v.w, acc.w));
       }
-      if (whole) {
-        store_out(r, acc, 1.f / lr);
-      } else {
+      return acc;
+    };
+    if (cnt == cur.w.units) {
+      __syncwarp();
+      int in = 0;
+      if (lane == 0) {
+        __threadfence_block();
+        in = atomicAdd(arrived_s + mb, 1);
+        __threadfence_block();
+      }
+      in = __shfl_sync(0xffffffffu, in, 0);
+      __syncwarp();
+      if (in == WARPS - 1) {
+        for (int r = lane / LPR; r < R; r += 32 / LPR) {
+          float mr, lr;
+          const float4 acc = add_row(r, mr, lr);
+          store_out(r, acc, 1.f / lr);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          arrived_s[mb] = 0;
+          __threadfence_block();
+          *reinterpret_cast<volatile int*>(turn_s + mb) = turn + 1;
+        }
+      }
+    } else {
+      failed = __syncthreads_or(failed) != 0;
+      const int task_first = ub + x - u0;
+      constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
+      float* mine = P.part + line.place(cta, task_first) * PLACE;
+      for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
+        float mr, lr;
+        const float4 acc = add_row(r, mr, lr);
         *reinterpret_cast<float4*>(mine + r * HD + col) = acc;
         if (col == 0) reinterpret_cast<float2*>(mine + ROWS * HD)[r] = make_float2(mr, lr);
       }
-    }
-    if (!whole) {
       const int c0 = line.owner(task_first), c1 = line.owner(task_first + cur.w.units - 1);
       int* ctr = P.counters + cur.b * P.nkv + kvh;
       __syncthreads();
       if (threadIdx.x == 0) {
-        __threadfence();  // the CTA's part, before the count
-        last_s = atomicAdd(ctr, 1) == c1 - c0;
+        turn_s[mb] = turn + 1;  // the buffer is free
+        __threadfence();        // the CTA's part, before the count
+        last_s = !failed && atomicAdd(ctr, 1) == c1 - c0;
         __threadfence();  // the count, before the other parts
       }
       __syncthreads();
@@ -434,11 +486,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     x += cnt;
-    if (x < count) cur.advance(B, work, cnt);
-    __syncthreads();  // the merge area is free
+    cur = nxt;
   }
-  if (failed) {
-    __syncthreads();
+  if (__syncthreads_or(failed)) {
     // let the copies in flight land before shared memory is released
     if (threadIdx.x < NS && issued_s[threadIdx.x] > 0) {
       const uint64_t t0 = global_timer_ns();

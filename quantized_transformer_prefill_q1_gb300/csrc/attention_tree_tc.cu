@@ -586,49 +586,78 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
-// CTA = MERGE_ROWS rows of a (sequence, kv head), a thread per row and eight columns; parts that saw no key of a row hold
-// no O. Eight rows a CTA spread few rows with many parts over the SMs (one tree of 26 nodes at 8,189: 18.5 us with the
-// attention, 23 with 32 rows); many rows take 32, since CTAs start at about 200 a microsecond.
-template <int HD, int MERGE_ROWS>
-__global__ void __launch_bounds__(MERGE_ROWS* HD / 8) tree_merge_kernel(const BatchDev B, int nq, int nkv, const Line* line_p, const int* prefix,
-                                                                        const float* part, int part_rows, __half* out) {
+// CTA = MR rows of a (sequence, kv head); a thread takes a row, eight columns and every GROUPS-th part, PF of them in
+// flight. Parts that saw no key of a row hold no O.
+template <int HD, int MR, int GROUPS, int PF, int CTAS>
+__global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(const BatchDev B, int nq, int nkv, const Line* line_p,
+                                                                               const int* prefix, const float* part, int part_rows,
+                                                                               __half* out) {
   PF_TIMELINE(TL_TREE_MERGE);
+  constexpr int COLS = HD / 8;
+  __shared__ float join[GROUPS > 1 ? (GROUPS - 1) * MR * COLS * 10 : 1];
   griddep_launch_dependents();
   griddep_wait();
   const int b = blockIdx.z, kvh = blockIdx.y, G = nq / nkv;
   const SeqRows s = batch_seq(B, b, true);
-  const int row = blockIdx.x * MERGE_ROWS + threadIdx.x % MERGE_ROWS, oct = threadIdx.x / MERGE_ROWS;
-  if (static_cast<int>(blockIdx.x) * MERGE_ROWS >= s.n * G) return;
   const Line line = *line_p;
-  const int rb = row / BLOCK, blocks = (s.n * G + BLOCK - 1) / BLOCK, units = (s.start + s.n + TK - 1) / TK;
-  const int first = prefix[b] + (kvh * blocks + rb) * units;
+  const int seq_first = prefix[b];
+  const int rows = s.n * G;
+  if (static_cast<int>(blockIdx.x) * MR >= rows) return;
+  const int row = blockIdx.x * MR + threadIdx.x % MR, oct = threadIdx.x / MR % COLS, group = threadIdx.x / (MR * COLS);
+  const int rb = blockIdx.x * MR / BLOCK, blocks = (rows + BLOCK - 1) / BLOCK, units = (s.start + s.n + TK - 1) / TK;
+  const int first = seq_first + (kvh * blocks + rb) * units;
   const int c0 = line.owner(first), c1 = line.owner(first + units - 1);
-  if (c0 == c1 || row >= s.n * G) return;
-  const int pr = row - rb * BLOCK, place0 = line.place(c0, first);
+  if (c0 == c1) return;  // the same for the whole CTA: its rows lie in one block
+  const int pr = min(row, rows - 1) - rb * BLOCK, place0 = line.place(c0, first);
   float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  constexpr int Q = 8;  // parts in flight
-  for (int c = c0; c <= c1; c += Q) {
-    float4 v[Q][2];
-    float2 ml[Q];
+  auto add = [&](float m, float l, const float* w) {
+    if (m == -INFINITY) return;
+    const float mn = fmaxf(mr, m);
+    const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ex2(m - mn);
+    mr = mn;
+    lr = lr * a + f * l;
 #pragma unroll
-    for (int y = 0; y < Q; ++y) {
-      const float* src = part + (c + y == c0 ? place0 : 2 * min(c + y, c1)) * (static_cast<size_t>(part_rows) * (HD + 2));
+    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + f * w[e];
+  };
+  for (int c = c0 + group; c <= c1; c += PF * GROUPS) {
+    float4 v[PF][2];
+    float2 ml[PF];
+#pragma unroll
+    for (int y = 0; y < PF; ++y) {
+      const int p = c + y * GROUPS;
+      if (p > c1) break;
+      const float* src = part + (p == c0 ? place0 : 2 * p) * (static_cast<size_t>(part_rows) * (HD + 2));
       ml[y] = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(part_rows) * HD) + pr);
 #pragma unroll
       for (int u = 0; u < 2; ++u) v[y][u] = __ldcg(reinterpret_cast<const float4*>(src) + static_cast<size_t>(2 * oct + u) * part_rows + pr);
     }
 #pragma unroll
-    for (int y = 0; y < Q; ++y) {
-      if (c + y > c1 || ml[y].x == -INFINITY) continue;
-      const float mn = fmaxf(mr, ml[y].x);
-      const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ex2(ml[y].x - mn);
-      mr = mn;
-      lr = lr * a + f * ml[y].y;
-      const float* w = reinterpret_cast<const float*>(v[y]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + f * w[e];
+    for (int y = 0; y < PF; ++y) {
+      if (c + y * GROUPS > c1) break;
+      add(ml[y].x, ml[y].y, reinterpret_cast<const float*>(v[y]));
     }
   }
+  if (GROUPS > 1) {
+    float* mine = join + (threadIdx.x - MR * COLS);  // [value][thread of the groups behind the first]
+    constexpr int STRIDE = (GROUPS - 1) * MR * COLS;
+    if (group > 0) {
+      mine[0] = mr;
+      mine[STRIDE] = lr;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine[(2 + e) * STRIDE] = acc[e];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g + 1 < GROUPS; ++g) {
+      const float* other = join + g * MR * COLS + threadIdx.x;
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = other[(2 + e) * STRIDE];
+      add(other[0], other[STRIDE], w);
+    }
+  }
+  if (row >= rows) return;
   const float inv = 1.f / lr;
   uint32_t h[4];
 #pragma unroll
@@ -675,14 +704,17 @@ cudaError_t launch_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
   const cudaError_t e = launch_pdl(attn_tree_tc_kernel<HD, BF16>, dim3(ctas), dim3(THREADS), TSmem<HD>::BYTES, stream, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
+  // Few rows may have many parts: eight rows a CTA and the parts in four groups spread them over the SMs; many rows have few
+  // parts each.
   const int rows = max_rows * G;
-  auto merge = [&](auto kernel, int per) {
-    return launch_pdl(kernel, dim3((rows + per - 1) / per, c.n_kv_heads, a.b->n_seq), dim3(per * HD / 8), 0, stream, p.B, p.nq, p.nkv,
+  auto merge = [&](auto kernel, int per, int threads) {
+    return launch_pdl(kernel, dim3((rows + per - 1) / per, c.n_kv_heads, a.b->n_seq), dim3(threads), 0, stream, p.B, p.nq, p.nkv,
                       static_cast<const Line*>(p.line), static_cast<const int*>(p.prefix), static_cast<const float*>(p.part),
                       p.part_rows, p.out);
   };
   const int64_t small = static_cast<int64_t>((rows + 7) / 8) * c.n_kv_heads * a.b->n_seq;
-  return small <= 4 * ctas ? merge(tree_merge_kernel<HD, 8>, 8) : merge(tree_merge_kernel<HD, 32>, 32);
+  return small <= 2 * ctas ? merge(tree_merge_kernel<HD, 8, 4, 5, 1>, 8, 4 * HD)
+                           : merge(tree_merge_kernel<HD, 16, 1, 4, 4>, 16, 2 * HD);
 }
 
 template <int HD, int BF16>
