@@ -32,7 +32,7 @@ struct ASmem {
   static constexpr int WS = RT == 16 ? (KS == 1 ? 3 : (KS == 2 ? 2 : 1)) : (KS <= 2 ? 4 : 2);
   static constexpr int NS = KW * WS;
   static constexpr int RED = KW * RT * R * 4;   // the groups' sums, over the rings
-  static constexpr int PART = RT * R * 4;       // the CTA's
+  static constexpr int PART = RT == 16 ? RT * R * 4 : 0;  // the CTA's (RT 64: the other CTAs add its two groups' themselves)
   static constexpr int RING = NS * STAGE > RED + PART ? NS * STAGE : RED + PART;
   static constexpr int PITCH = (4 * R + 127) / 128 * 128 + 32;  // bytes between rows of h: conflict-free 8-byte reads of 4 rows
   static constexpr int BYTES = 1024 + RING + RT * PITCH + RT * 4 + NS * 8;
@@ -71,10 +71,19 @@ __device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+__device__ __forceinline__ float2 ld_cluster(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
+}
+// Two f32 values as f16 pairs hi + lo.
+__device__ __forceinline__ void split(float2 v, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  const float2 b = __half22float2(h);
+  const float rx = v.x - b.x, ry = v.y - b.y;  // 0 beside an infinity or a NaN
+  const __half2 l = __floats2half2_rn(fabsf(rx) <= 65504.f ? rx : 0.f, fabsf(ry) <= 65504.f ? ry : 0.f);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 __device__ __forceinline__ bool bar_and(int id, int threads, bool pred) {
   uint32_t r;
@@ -130,6 +139,15 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
       reinterpret_cast<float4*>(out + r * P.ldo)[q] = reinterpret_cast<const float4*>(base + r * P.ldb)[q];
     }
     return;
+  }
+
+  // Columns of the second product, 32 at a time (see below): groups gb .. ge - 1 of this CTA.
+  const int groups = (P.N + 31) / 32;
+  const int gb = groups * c / CL, ge = groups * (c + 1) / CL;
+  if (RT > 16 && threadIdx.x < rows && ge > gb) {
+    // base towards L2 meanwhile: the second product would wait for it after the shares have met, with nothing else to do
+    const int bytes = (min(P.N, 32 * ge) - 32 * gb) * 4;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(base + threadIdx.x * P.ldb + 32 * gb), "r"(bytes) : "memory");
   }
 
   // ------------------------------------------------------------------ h = x A^T over this CTA's share of K
@@ -197,21 +215,21 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     *reinterpret_cast<float2*>(dst + 8 * R) = make_float2(acc[j][2], acc[j][3]);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < RT * R / 4; i += THREADS) {
-    float4 v = reinterpret_cast<const float4*>(red)[i];
+  if (RT == 16) {
+    for (int i = threadIdx.x; i < RT * R / 4; i += THREADS) {
+      float4 v = reinterpret_cast<const float4*>(red)[i];
 #pragma unroll
-    for (int w = 1; w < KW; ++w) {
-      const float4 y = reinterpret_cast<const float4*>(red)[w * (RT * R / 4) + i];
-      v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+      for (int w = 1; w < KW; ++w) {
+        const float4 y = reinterpret_cast<const float4*>(red)[w * (RT * R / 4) + i];
+        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+      }
+      reinterpret_cast<float4*>(part)[i] = v;
     }
-    reinterpret_cast<float4*>(part)[i] = v;
   }
 
-  // ------------------------------------------------------------------ B of the warp's first columns, while the shares meet
-  // 32 columns at a time: pair p (16 columns) of MMA tiles; n = g of tile u is column 16 p + 4 (g / 2) + g % 2 + 2 u, so
-  // that a lane's four accumulators of a row are four columns in a line. k runs as 4 t .. 4 t + 3 in both operands.
-  const int groups = (P.N + 31) / 32;
-  const int gb = groups * c / CL, ge = groups * (c + 1) / CL;
+  // ------------------------------------------------------------------ B and base of the warp's first columns, while the shares meet
+  // Pair p (16 columns) of MMA tiles; n = g of tile u is column 16 p + 4 (g / 2) + g % 2 + 2 u, so that a lane's four
+  // accumulators of a row are four columns in a line. k runs as 4 t .. 4 t + 3 in both operands.
   const __half* wb = P.wb + static_cast<size_t>(a) * P.N * P.rank;
   uint2 wf[4][KS];
   auto load_b = [&](int gi) {
@@ -225,30 +243,52 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
                        : make_uint2(0u, 0u);
     }
   };
-  if (gb + warp < ge) load_b(gb + warp);
+  auto load_base = [&](int gi, int m, float4 (&y)[2][2]) {  // [row half][pair]
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = 16 * m + 8 * hh + g, col = 32 * gi + 16 * p + 4 * t;
+        y[hh][p] = r < rows && col < P.N ? *reinterpret_cast<const float4*>(base + r * P.ldb + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+  };
+  float4 y[2][2];
+  if (gb + warp < ge) {
+    load_b(gb + warp);
+    load_base(gb + warp, 0, y);
+  }
 
-  // ------------------------------------------------------------------ the cluster's sum: CTA c adds rows c RT / 8 .., a warp a row
+  // ------------------------------------------------------------------ the cluster's sum, a warp a row, a lane two columns
+  // RT 16: every CTA adds all rows for itself (one barrier of latency); RT 64: CTA c adds rows 8 c .. 8 c + 7 for all.
   __syncwarp();
   cluster_arrive_release();
   cluster_wait();
   const float scale = P.scale[a];
-  for (int i = warp; i < RT / CL; i += WARPS) {
-    const int r = c * (RT / CL) + i;
-    constexpr int PER = (R + 31) / 32;
-    float v[PER], big = 0.f;
+  constexpr int OWN = RT == 16 ? RT : RT / CL;
+  for (int i = warp; i < OWN; i += WARPS) {
+    const int r = RT == 16 ? i : c * OWN + i;
+    if (r >= rows) break;
+    constexpr int PER = (R + 63) / 64;
+    float2 v[PER];
+    float big = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int col = lane + 32 * e;
-      v[e] = 0.f;
+      const int col = 2 * lane + 64 * e;
+      v[e] = make_float2(0.f, 0.f);
       if (col < P.rank) {
-        const uint32_t at = smem_u32(part + r * R + col);
-        float y[CL];
+        constexpr int PARTS = RT == 16 ? 1 : KW;
+        const uint32_t at = smem_u32((RT == 16 ? part : red) + r * R + col);
+        float2 y2[CL][PARTS];
 #pragma unroll
-        for (int w = 0; w < CL; ++w) y[w] = ld_cluster(remote(at, w));
+        for (int w = 0; w < CL; ++w)
 #pragma unroll
-        for (int w = 0; w < CL; ++w) v[e] += y[w];
+          for (int k = 0; k < PARTS; ++k) y2[w][k] = ld_cluster(remote(at + k * (RT * R * 4), w));
+#pragma unroll
+        for (int w = 0; w < CL; ++w)
+#pragma unroll
+          for (int k = 0; k < PARTS; ++k) v[e] = make_float2(v[e].x + y2[w][k].x, v[e].y + y2[w][k].y);
       }
-      big = fmaxf(big, fabsf(v[e]));
+      big = fmaxf(big, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -258,43 +298,42 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     const float f = __int_as_float((up + 127) << 23), back = __int_as_float((127 - up) << 23) * scale;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int col = lane + 32 * e;
+      const int col = 2 * lane + 64 * e;
       if (col >= R) continue;
-      const float x = v[e] * f;
-      const __half hi = __float2half_rn(x);
-      const float rest = x - __half2float(hi);
-      const __half lo = __float2half_rn(fabsf(rest) <= 65504.f ? rest : 0.f);  // 0 beside an infinity or a NaN
-      const uint32_t at = smem_u32(h_s + r * L::PITCH) + 2 * col;
+      uint32_t hi, lo;
+      split(make_float2(v[e].x * f, v[e].y * f), hi, lo);
+      uint8_t* at = h_s + r * L::PITCH + 2 * col;
+      if (RT == 16) {
+        *reinterpret_cast<uint32_t*>(at) = hi;
+        *reinterpret_cast<uint32_t*>(at + 2 * R) = lo;
+      } else {
 #pragma unroll
-      for (int w = 0; w < CL; ++w) {
-        const uint32_t dst = remote(at, w);
-        asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(dst), "h"(__half_as_ushort(hi)) : "memory");
-        asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(dst + 2 * R), "h"(__half_as_ushort(lo)) : "memory");
+        for (int w = 0; w < CL; ++w) {
+          const uint32_t dst = remote(smem_u32(at), w);
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(hi) : "memory");
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 2 * R), "r"(lo) : "memory");
+        }
       }
     }
-    if (lane < CL) {
+    if (RT == 16) {
+      if (lane == 0) rs_s[r] = back;
+    } else if (lane < CL) {
       const uint32_t dst = remote(smem_u32(rs_s + r), lane);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(back) : "memory");
     }
   }
   __syncwarp();
-  cluster_arrive_release();
-  cluster_wait();
+  cluster_arrive_release();  // this CTA has read the others' shares (RT 64: and written theirs)
+  if (RT == 16)
+    __syncthreads();
+  else
+    cluster_wait();
 
   // ------------------------------------------------------------------ out = base + scale h B^T
   for (int gi = gb + warp; gi < ge; gi += WARPS) {
-    if (gi != gb + warp) load_b(gi);
 #pragma unroll 1
     for (int m = 0; m < MG; ++m) {
       if (16 * m >= rows) break;
-      float4 y[2][2];  // [row half][pair]
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int r = 16 * m + 8 * hh + g, col = 32 * gi + 16 * p + 4 * t;
-          y[hh][p] = r < rows && col < P.N ? *reinterpret_cast<const float4*>(base + r * P.ldb + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
       float d[4][4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -311,6 +350,18 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
 #pragma unroll
           for (int u = 0; u < 4; ++u) mma16816(d[u], x, wf[u][k].x, wf[u][k].y);
         }
+      // the next rows' base, or the next columns' B and base, are requested before this tile's results are stored
+      float4 z[2][2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) z[hh][p] = y[hh][p];
+      if (m + 1 < MG && 16 * (m + 1) < rows) {
+        load_base(gi, m + 1, y);
+      } else if (gi + WARPS < ge) {
+        load_b(gi + WARPS);
+        load_base(gi + WARPS, 0, y);
+      }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int r = 16 * m + 8 * hh + g;
@@ -320,14 +371,15 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
         for (int p = 0; p < 2; ++p) {
           const int col = 32 * gi + 16 * p + 4 * t;
           if (col >= P.N) continue;
-          const float4 z = y[hh][p];
+          const float4 q = z[hh][p];
           *reinterpret_cast<float4*>(out + r * P.ldo + col) =
-              make_float4(fmaf(f, d[2 * p][2 * hh], z.x), fmaf(f, d[2 * p][2 * hh + 1], z.y), fmaf(f, d[2 * p + 1][2 * hh], z.z),
-                          fmaf(f, d[2 * p + 1][2 * hh + 1], z.w));
+              make_float4(fmaf(f, d[2 * p][2 * hh], q.x), fmaf(f, d[2 * p][2 * hh + 1], q.y), fmaf(f, d[2 * p + 1][2 * hh], q.z),
+                          fmaf(f, d[2 * p + 1][2 * hh + 1], q.w));
         }
       }
     }
   }
+  if (RT == 16) cluster_wait();  // the others have read this CTA's share
   if (threadIdx.x == 0 && *abort_flag) batch_record(P.status, PF_ERR_DEVICE_TIMEOUT);
 }
 
