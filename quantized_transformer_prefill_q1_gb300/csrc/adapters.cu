@@ -32,7 +32,7 @@ struct ASmem {
   static constexpr int WS = RT == 16 ? (KS == 1 ? 3 : (KS == 2 ? 2 : 1)) : (KS <= 2 ? 4 : 2);
   static constexpr int NS = KW * WS;
   static constexpr int RED = KW * RT * R * 4;   // the groups' sums, over the rings
-  static constexpr int PART = RT == 16 ? RT * R * 4 : 0;  // the CTA's (RT 64: the other CTAs add its two groups' themselves)
+  static constexpr int PART = RT * R * 4;       // the CTA's
   static constexpr int RING = NS * STAGE > RED + PART ? NS * STAGE : RED + PART;
   static constexpr int PITCH = (4 * R + 127) / 128 * 128 + 32;  // bytes between rows of h: conflict-free 8-byte reads of 4 rows
   static constexpr int BYTES = 1024 + RING + RT * PITCH + RT * 4 + NS * 8;
@@ -144,11 +144,6 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
   // Columns of the second product, 32 at a time (see below): groups gb .. ge - 1 of this CTA.
   const int groups = (P.N + 31) / 32;
   const int gb = groups * c / CL, ge = groups * (c + 1) / CL;
-  if (RT > 16 && threadIdx.x < rows && ge > gb) {
-    // base towards L2 meanwhile: the second product would wait for it after the shares have met, with nothing else to do
-    const int bytes = (min(P.N, 32 * ge) - 32 * gb) * 4;
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(base + threadIdx.x * P.ldb + 32 * gb), "r"(bytes) : "memory");
-  }
 
   // ------------------------------------------------------------------ h = x A^T over this CTA's share of K
   const int mg = warp % MG, kw = warp / MG;
@@ -215,16 +210,14 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     *reinterpret_cast<float2*>(dst + 8 * R) = make_float2(acc[j][2], acc[j][3]);
   }
   __syncthreads();
-  if (RT == 16) {
-    for (int i = threadIdx.x; i < RT * R / 4; i += THREADS) {
-      float4 v = reinterpret_cast<const float4*>(red)[i];
+  for (int i = threadIdx.x; i < RT * R / 4; i += THREADS) {
+    float4 v = reinterpret_cast<const float4*>(red)[i];
 #pragma unroll
-      for (int w = 1; w < KW; ++w) {
-        const float4 y = reinterpret_cast<const float4*>(red)[w * (RT * R / 4) + i];
-        v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
-      }
-      reinterpret_cast<float4*>(part)[i] = v;
+    for (int w = 1; w < KW; ++w) {
+      const float4 y = reinterpret_cast<const float4*>(red)[w * (RT * R / 4) + i];
+      v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
     }
+    reinterpret_cast<float4*>(part)[i] = v;
   }
 
   // ------------------------------------------------------------------ B and base of the warp's first columns, while the shares meet
@@ -276,17 +269,12 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
       const int col = 2 * lane + 64 * e;
       v[e] = make_float2(0.f, 0.f);
       if (col < P.rank) {
-        constexpr int PARTS = RT == 16 ? 1 : KW;
-        const uint32_t at = smem_u32((RT == 16 ? part : red) + r * R + col);
-        float2 y2[CL][PARTS];
+        const uint32_t at = smem_u32(part + r * R + col);
+        float2 y2[CL];
 #pragma unroll
-        for (int w = 0; w < CL; ++w)
+        for (int w = 0; w < CL; ++w) y2[w] = ld_cluster(remote(at, w));
 #pragma unroll
-          for (int k = 0; k < PARTS; ++k) y2[w][k] = ld_cluster(remote(at + k * (RT * R * 4), w));
-#pragma unroll
-        for (int w = 0; w < CL; ++w)
-#pragma unroll
-          for (int k = 0; k < PARTS; ++k) v[e] = make_float2(v[e].x + y2[w][k].x, v[e].y + y2[w][k].y);
+        for (int w = 0; w < CL; ++w) v[e] = make_float2(v[e].x + y2[w].x, v[e].y + y2[w].y);
       }
       big = fmaxf(big, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
     }
