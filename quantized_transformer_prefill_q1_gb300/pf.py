@@ -476,22 +476,24 @@ def _batch(batch, dev: int, cfg=None):
     return batch.ref
 
 
-def _cache16(cfg, dev: int, t, what: str) -> Optional[int]:
-    """Address of a 16-bit cache buffer of the configuration's type."""
-    slots = cfg.kv_block_pool * KV_BLOCK if cfg.kv_block_pool > 0 else cfg.max_seq
-    return _dense(t, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), what, cfg.n_layers * cfg.n_kv_heads * slots * cfg.head_dim)
+def _caches16(cfg, dev: int, k, v):
+    """Addresses of a 16-bit K and V cache buffer of the configuration's type."""
+    pool = cfg.kv_block_pool
+    n = cfg.n_layers * cfg.n_kv_heads * (pool * KV_BLOCK if pool > 0 else cfg.max_seq) * cfg.head_dim
+    dt = _KV_TORCH.get(cfg.kv_dtype, "float16")
+    return _dense(k, dev, dt, "K cache", n), _dense(v, dev, dt, "V cache", n)
 
 
 def pf_op_batch_append(cfg, batch, qkv, qn, kn, rope, layer, q, k_cache, v_cache, status=None, stream=None):
     """QK-norm, RoPE and KV store of every sequence's rows: qkv f32 [n_rows, (nq + 2 nkv) hd], q of the cache's type
     [n_rows, nq, hd], rope f32 [max_seq, hd / 2, 2] on the device (pf_rope_table_host)."""
-    dev, n, hd = _here(), batch.n_rows, cfg.head_dim
+    dev, n, hd, nq = _here(), batch.n_rows, cfg.head_dim, cfg.n_q_heads
+    k, v = _caches16(cfg, dev, k_cache, v_cache)
     check(lib().pf_op_batch_append(ctypes.byref(cfg), _batch(batch, dev, cfg),
-                                   _dense(qkv, dev, "float32", "qkv", n * (cfg.n_q_heads + 2 * cfg.n_kv_heads) * hd),
+                                   _dense(qkv, dev, "float32", "qkv", n * (nq + 2 * cfg.n_kv_heads) * hd),
                                    _dense(qn, dev, "float32", "q_norm", hd, True), _dense(kn, dev, "float32", "k_norm", hd, True),
                                    _dense(rope, dev, "float32", "rope", cfg.max_seq * hd), layer,
-                                   _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n * cfg.n_q_heads * hd),
-                                   _cache16(cfg, dev, k_cache, "K cache"), _cache16(cfg, dev, v_cache, "V cache"),
+                                   _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n * nq * hd), k, v,
                                    _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
@@ -513,9 +515,9 @@ def pf_op_attention_tree(cfg, batch, q, k_cache, v_cache, layer, out, scratch, s
     """Attention of every sequence's rows over the cache: q of the cache's type [n_rows, nq, hd], out f16 [n_rows, nq * hd]."""
     dev = _here()
     n = batch.n_rows * cfg.n_q_heads * cfg.head_dim
+    k, v = _caches16(cfg, dev, k_cache, v_cache)
     check(lib().pf_op_attention_tree(ctypes.byref(cfg), _batch(batch, dev, cfg),
-                                     _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n),
-                                     _cache16(cfg, dev, k_cache, "K cache"), _cache16(cfg, dev, v_cache, "V cache"), layer,
+                                     _dense(q, dev, _KV_TORCH.get(cfg.kv_dtype, "float16"), "q", n), k, v, layer,
                                      _dense(out, dev, "float16", "out", n), _dense(scratch, dev, "uint8", "scratch", 0),
                                      scratch.numel(), _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
@@ -525,12 +527,13 @@ def pf_op_tree_accept(cfg, batch, tokens, ids, root_ids, path, n_accepted, next_
     """Greedy acceptance of each sequence's tree (int32: tokens, ids, path [n_rows]; root_ids, n_accepted, next_ids
     [n_seq]); the accepted nodes' K and V move up in every layer of the caches (None: nothing is moved)."""
     dev, n, b = _here(), batch.n_rows, batch.n_seq
+    if (k_cache is None) != (v_cache is None):
+        raise PfError(1, "both caches or none")
+    k, v = (None, None) if k_cache is None else _caches16(cfg, dev, k_cache, v_cache)
     check(lib().pf_op_tree_accept(ctypes.byref(cfg), _batch(batch, dev, cfg), _dense(tokens, dev, "int32", "tokens", n),
                                   _dense(ids, dev, "int32", "ids", n), _dense(root_ids, dev, "int32", "root_ids", b),
                                   _dense(path, dev, "int32", "path", n), _dense(n_accepted, dev, "int32", "n_accepted", b),
-                                  _dense(next_ids, dev, "int32", "next_ids", b),
-                                  None if k_cache is None else _cache16(cfg, dev, k_cache, "K cache"),
-                                  None if v_cache is None else _cache16(cfg, dev, v_cache, "V cache"),
+                                  _dense(next_ids, dev, "int32", "next_ids", b), k, v,
                                   _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
