@@ -35,7 +35,7 @@ namespace {
 constexpr int TM = 128;      // rows of a slot
 constexpr int BLOCK = 256;   // rows of a task
 constexpr int TK = 128;      // keys per tile
-constexpr int HK = TK / 2;   // keys that a softmax thread holds at once
+constexpr int HK = TK / 2;   // keys of one product with V
 constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;
 constexpr float RESCALE_LOG2 = 8.f;
@@ -90,6 +90,32 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Two f32 values in one register pair, for the packed multiply-add and addition.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 each(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Bits [0, n) set (n clamped to [0, 32]).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
@@ -120,8 +146,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto s_full = [&](int s) { return bar0 + 8u * (2 * NS + s); };
   auto p_full = [&](int s, int h) { return bar0 + 8u * (2 * NS + 2 + 2 * s + h); };
   auto o_done = [&](int s) { return bar0 + 8u * (2 * NS + 6 + s); };
-  auto o_empty = [&](int s) { return bar0 + 8u * (2 * NS + 10 + s); };
-  const uint32_t q_full = bar0 + 8u * (2 * NS + 12), q_empty = q_full + 8, drain_bar = q_full + 16;
+  auto o_empty = [&](int s) { return bar0 + 8u * (2 * NS + 8 + s); };
+  const uint32_t q_full = bar0 + 8u * (2 * NS + 10), q_empty = q_full + 8, drain_bar = q_full + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (q_full + 24 - raw));
   static_assert(8 * (2 * NS + 16) <= 512, "barrier area");
   const BatchDev& B = P.B;
@@ -371,6 +397,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool mine = r < p.rows - (p.slots == 2 ? slot * TM : 0);
       float m = -INFINITY, l = 0.f;
       const int step = p.slots == 2 ? 1 : 2, j0 = p.slots == 2 ? 0 : slot;
+      // Keys of a tile that the row does not see get the score -inf: it adds nothing to the maximum and has weight 0. n0 =
+      // node of the tile's first key (negative: cached).
+      auto hide = [&](int n0) {
+        uint32_t vis[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) vis[w] = low_bits((mine && B.parent == nullptr ? node + 1 : 0) - (n0 + 32 * w));
+        if (mine && B.parent != nullptr) {
+          for (int a = node; a >= 0 && a >= n0;) {  // ancestors come before their children
+            const int e = a - n0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if ((e >> 5) == w) vis[w] |= 1u << (e & 31);
+            bool bad;
+            a = tree_parent(B.parent + p.at, a, bad);
+            if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
+          }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t see = c == 0 ? vis[0] : (c == 1 ? vis[1] : (c == 2 ? vis[2] : vis[3]));
+          uint32_t u[32];
+          tmem_ld_32x32b_x32(sbuf + 32 * c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) u[e] = 0xff800000u;
+          tmem_st_32x32b_x32(sbuf + 32 * c, u);
+        }
+        tmem_st_wait();
+      };
       // key r of a tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN. Each slot
       // clears it before its own product.
       auto clear_v = [&](int j) {
@@ -385,56 +442,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(slot), done & 1, abort_flag)))) break;
         tc_fence_after();
         const int key0 = (p.u0 + j) * TK, nvalid = p.start + p.n - key0;
-        const bool tail = key0 + TK > p.start;  // the tile holds rows of the sequence itself, or what lies behind them
-        uint32_t vis[4];                        // the keys of such a tile that the row sees
-        if (tail) {
-          const int n0 = key0 - p.start;  // node of the tile's first key (negative: cached)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) vis[w] = low_bits((mine && B.parent == nullptr ? node + 1 : 0) - (n0 + 32 * w));
-          if (mine && B.parent != nullptr) {
-            for (int a = node; a >= 0 && a >= n0;) {  // ancestors come before their children
-              const int e = a - n0;
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                if ((e >> 5) == w) vis[w] |= 1u << (e & 31);
-              bool bad;
-              a = tree_parent(B.parent + p.at, a, bad);
-              if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
-            }
-          }
-        }
-        // the scores of 64 keys; hidden ones -inf: they add nothing to the maximum and get weight 0
-        uint32_t v[64];
+        if (key0 + TK > p.start) hide(key0 - p.start);  // the tile holds rows of the sequence itself, or what lies behind them
+        // The tile in halves of 64 keys, in loops: unrolled over a tile the code outgrows the instruction cache that two SMs
+        // share. First the row's maximum, then the weights, the second half first; P takes the first 32 columns of its half's scores.
+        uint32_t v[HK];
         auto load = [&](int h) {
-          tmem_ld_32x32b_x32(sbuf + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(v));
-          tmem_ld_32x32b_x32(sbuf + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_32x32b_x32(sbuf + HK * h, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld_32x32b_x32(sbuf + HK * h + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
           tmem_ld_wait();
-          if (tail) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (!(((h == 0 ? vis[e >> 5] : vis[2 + (e >> 5)]) >> (e & 31)) & 1u)) v[e] = 0xff800000u;
-          }
         };
-        // The first half is read twice: 128 scores at once do not fit the registers beside the rest. P takes the first
-        // 32 columns of its own half's scores.
-        float mp[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-#pragma unroll
+        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           load(h);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) mp[e & 7] = fmaxf(mp[e & 7], __uint_as_float(v[e]));
+          for (int e = 0; e < HK; e += 2) mp[(e >> 1) & 3] = max3(mp[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
         }
-        const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])), fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
         const bool need = mx > m + RESCALE_LOG2;
         if (j == j0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, need)) {
           const float alpha = need ? ex2(m - mx) : 1.f;
           l *= alpha;
-          // O holds the tiles so far: wait for the last of them, then scale it in place
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_done(slot), (done - 1) & 1, abort_flag)))) break;
+          // O holds the tiles so far, whose products completed before this tile's scores
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < HD / 32; ++c) {
@@ -448,34 +479,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (need) m = mx;
         }
         const float neg_m = m == -INFINITY ? 0.f : -m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+        const uint64_t neg_two = two(neg_m, neg_m), sl2_two = two(sl2, sl2);
+        uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll 1
         for (int h = 1; h >= 0; --h) {
-          if (h == 0) load(0);
+          load(h);
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), sl2, neg_m));
-            const float p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), sl2, neg_m));
-            ls[e & 3] += p0 + p1;
+            const float2 u = each(fma_two(two(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2_two, neg_two));
+            const float p0 = ex2(u.x), p1 = ex2(u.y);
+            ls[e & 3] = add_two(ls[e & 3], two(p0, p1));
             pk[e] = pack2<BF16>(p0, p1);
           }
-          tmem_st_32x32b_x32(sbuf + 64 * h, pk);
-          if (h == 1) {  // the second half's product starts while the first half's weights are formed
-            if (r >= nvalid && r >= 64) clear_v(j);
-            tmem_st_wait();
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_before();
-            mbar_arrive(p_full(slot, 1));
-          }
+          tmem_st_32x32b_x32(sbuf + HK * h, pk);
+          // a half's product starts while the other half's weights are formed
+          if (r >= nvalid && (r >> 6) == h) clear_v(j);
+          tmem_st_wait();
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_before();
+          mbar_arrive(p_full(slot, h));
         }
+        const float2 sum = each(add_two(add_two(ls[0], ls[1]), add_two(ls[2], ls[3])));
+        l += sum.x + sum.y;
         if (!ok) break;
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        if (r >= nvalid && r < 64) clear_v(j);
-        tmem_st_wait();
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_fence_before();
-        mbar_arrive(p_full(slot, 0));
         ++done;
       }
       // ------------------------------------------------------------------ the part's end
