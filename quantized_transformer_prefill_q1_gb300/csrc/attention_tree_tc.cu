@@ -6,8 +6,7 @@
 // lengths are (batch.cuh). A CTA holds two slots, each with 128 rows in the MMA's M side, its own S / P and O in tensor
 // memory and 128 softmax threads, one a row: while one slot's softmax runs, the other's products do.
 //   more than 128 rows: slot s takes rows 128 s .. +127 of every tile: K and V are read once for 256 rows;
-//   128 rows or fewer:  both slots hold the same rows and take the tiles in turn; at the end slot 1's
-//                       (m, l, O) join slot 0's through shared memory.
+//   128 rows or fewer:  both slots hold the same rows and take the tiles in turn; at the end their (m, l, O) are added.
 //
 // Warp roles:
 //   warp 0      TMA: Q (3-D map over q[rows][nq][hd]), K and V tiles into one ring in the order the products need them,
@@ -136,11 +135,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int NH = HD / 64, NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_s;
-  __shared__ float2 ml_s[TM];  // slot 1's (m, l)
+  __shared__ float2 ml_s[TM];  // slot 1's (m, l), then both slots' factors
   volatile int* abort_flag = &abort_s;
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t q_s = base, kv_s = q_s + 2 * L::QT, bar0 = kv_s + NS * L::KV;
-  float* xbuf = reinterpret_cast<float*>(smem_raw + (base - raw) + L::QT);  // slot 1's Q, idle where the slots share the rows
   auto kv_full = [&](int s) { return bar0 + 8u * s; };
   auto kv_empty = [&](int s) { return bar0 + 8u * (NS + s); };
   auto s_full = [&](int s) { return bar0 + 8u * (2 * NS + s); };
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ copies (lane 0; a lane each looks up the tiles' pages)
-    int c = 0, seg = 0, last_slots = 0, q_issued = 0;
+    int c = 0, seg = 0, q_issued = 0;
     bool ok = true;
     for (int x = 0; x < count && ok; ++seg) {
       const Part p = part(x);
@@ -251,9 +249,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto load_q = [&]() {
         if (ok && lane == 0) {
           if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, abort_flag);
-          // slot 1's Q may still be the exchange buffer of the part before
-          if (ok && seg > 0 && p.slots == 2 && last_slots == 1)
-            ok = mbar_wait(o_empty(0), (seg - 1) & 1, abort_flag) && mbar_wait(o_empty(1), (seg - 1) & 1, abort_flag);
           if (ok) {
             mbar_arrive_expect_tx(q_full, p.slots * L::QT);
             for (int s = 0; s < p.slots; ++s)
@@ -280,7 +275,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (seg > 0 && j == min(1, p.cnt + lag - 1)) load_q();
         ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
       }
-      last_slots = p.slots;
       x += p.cnt;
       if (x < count) cur.advance(B, work, p.cnt);
     }
@@ -508,6 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------ the part's end
       const int tiles = p.slots == 2 ? p.cnt : (p.cnt - slot + 1) / 2;
       if (ok && tiles > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done(slot), (done - 1) & 1, abort_flag));
+      if (p.slots == 1 && slot == 1) ml_s[r] = make_float2(m, l);
       if (!bar_and(1, SM_THREADS, ok)) break;
       tc_fence_after();
       const bool whole = p.cnt == cur.w.units;
@@ -549,49 +544,34 @@ __global__ void __launch_bounds__(THREADS, 1)
           put(c, reinterpret_cast<const float*>(o), inv);
         }
       } else {
-        // slot 1's sums join slot 0's: half of the columns at a time through slot 1's Q, [column][row]
-        float a0 = 1.f, a1 = 0.f, inv = 1.f;
-        if (slot == 1) ml_s[r] = make_float2(m, l);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (slot == 1) {
-#pragma unroll 1
-            for (int c = 0; c < HD / 64; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(obuf + h * (HD / 2) + 32 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) xbuf[(32 * c + e) * TM + r] = __uint_as_float(o[e]);
-            }
-          }
-          bar_sync(1, SM_THREADS);
-          if (slot == 0) {
-            if (h == 0) {
-              const float2 y = ml_s[r];
-              const float mm = fmaxf(m, y.x);
-              a0 = m == -INFINITY ? 0.f : ex2(m - mm);
-              a1 = y.x == -INFINITY ? 0.f : ex2(y.x - mm);
-              const float ll = a0 * l + a1 * y.y;
-              inv = 1.f / ll;
-              put_ml(mm, ll);
-            }
-#pragma unroll 1
-            for (int c = 0; c < HD / 64; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(obuf + h * (HD / 2) + 32 * c, o);
-              tmem_ld_wait();
-              float f[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {  // a slot that saw nothing may hold anything
-                const float u = a0 == 0.f ? 0.f : a0 * __uint_as_float(o[e]);
-                f[e] = a1 == 0.f ? u : fmaf(a1, xbuf[(32 * c + e) * TM + r], u);
-              }
-              put(h * (HD / 64) + c, f, inv);
-            }
-          }
-          bar_sync(1, SM_THREADS);
+        // The slots' sums meet where they are: a thread reads its row of both O's, slot 0 for the first half of the columns, slot 1
+        // for the second. Slot 0 forms the factors from slot 1's (m, l) and hands them over.
+        float2 f;
+        if (slot == 0) {
+          const float2 y = ml_s[r];
+          const float mm = fmaxf(m, y.x);
+          f = make_float2(m == -INFINITY ? 0.f : ex2(m - mm), y.x == -INFINITY ? 0.f : ex2(y.x - mm));
+          const float ll = f.x * l + f.y * y.y;
+          put_ml(mm, ll);
+          if (whole) f = make_float2(f.x / ll, f.y / ll);
+          ml_s[r] = f;
         }
-        fence_proxy_async_smem();  // before a later part's Q
+        bar_sync(1, SM_THREADS);
+        if (slot == 1) f = ml_s[r];
+#pragma unroll 1
+        for (int c = slot * (HD / 64); c < (slot + 1) * (HD / 64); ++c) {
+          uint32_t o[2][32];
+          tmem_ld_32x32b_x32(tmem + lane_off + 256 + 32 * c, o[0]);
+          tmem_ld_32x32b_x32(tmem + lane_off + 256 + TK + 32 * c, o[1]);
+          tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {  // a slot that saw nothing may hold anything
+            const float u = f.x == 0.f ? 0.f : f.x * __uint_as_float(o[0][e]);
+            v[e] = f.y == 0.f ? u : fmaf(f.y, __uint_as_float(o[1][e]), u);
+          }
+          put(c, v, 1.f);
+        }
       }
       tc_fence_before();
       mbar_arrive(o_empty(slot));
