@@ -20,7 +20,9 @@
 // A task that lies in one CTA is written by it; parts of a cut one go to scratch as f32 and a second kernel merges
 // them, a thread per row and eight columns.
 //
-// Rounding: P to the cache's type (the product's operand), the output to f16; all else f32.
+// Rounding: P to the cache's type (the product's operand; of a bf16 cache that is the largest error of the f16 output, 1.2e-3
+// in relative L2, as in the attention over one sequence: a second term would double the products with V, which bound the
+// kernel together with the scores), the output to f16; all else f32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
