@@ -429,7 +429,10 @@ cudaError_t prepare_adapters_kernels() {
 }
 
 cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t stream) {
-  return std::min(a.b->max_rows, a.b->n_rows) <= 16 ? launch_rank<16>(a, stream) : launch_rank<64>(a, stream);
+  const int rows = std::min(a.b->max_rows, a.b->n_rows);
+  const int tiles = std::min(a.b->n_seq * ((rows + 15) / 16), a.b->n_rows / 16 + a.b->n_seq);  // of 16 rows, at most
+  const int resident = (a.rank <= 64 ? 2 : 1) * device_sm_count();
+  return rows <= 16 || tiles * CL <= resident ? launch_rank<16>(a, stream) : launch_rank<64>(a, stream);
 }
 
 }  // namespace pf

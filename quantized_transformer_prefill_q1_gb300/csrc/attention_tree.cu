@@ -11,7 +11,7 @@
 // warps meet in shared memory; a task that lies in one CTA is done, parts of a cut one meet in scratch, where the CTA
 // that completes the task's count merges them.
 //
-// The rows of one kv head (row = node * G + head in the group, at most 8 NB) are the n side of warp-level MMAs
+// The rows of one kv head (row = node * G + head in the group, at most FEW_ROWS) are the n side of warp-level MMAs
 // m16n8k16: S^T [keys x rows] = K [16 keys x 16 d] Q^T and O^T [d x rows] += V^T [16 d x 16 keys] P^T, K and V as A
 // operands by ldmatrix (V transposed on the way); P^T comes from S^T by a register transpose (movmatrix).
 // The running maximum is raised only when exceeded by more than 2^8.
@@ -33,17 +33,17 @@ constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int UK = 32;  // keys per unit
 constexpr float RESCALE_LOG2 = 8.f;
-constexpr int FEW_ROWS = 16;  // most rows per kv head of this form
+constexpr int FEW_ROWS = 8;  // most rows per kv head of this form: the n side of an MMA
 
-template <int HD, int NB>
+template <int HD>
 struct FSmem {
   static constexpr int WS = HD == 64 ? 6 : 3;  // stages of a warp's ring: 192 KB in flight an SM
   static constexpr int NS = WARPS * WS;
   static constexpr int TILE = UK * HD * 2;                       // bytes of a K or V unit
   static constexpr int RING = NS * 2 * TILE;
-  static constexpr int ROWS = 8 * NB;
+  static constexpr int ROWS = FEW_ROWS;
   static constexpr int OW = HD + 4;  // floats between rows of the warps' O
-  static constexpr int NM = NB == 1 ? 2 : 1;  // merge buffers
+  static constexpr int NM = 2;  // merge buffers
   static constexpr int MERGE = WARPS * ROWS * (OW + 2) * 4;
   static constexpr int BYTES = 1024 + RING + NM * MERGE + NS * 8;
   static_assert(BYTES <= 232448 - 384, "shared memory");  // beside the static arrays
@@ -110,11 +110,11 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int chunk) 
   return tile + (chunk >> 3) * (UK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-template <int HD, int BF16, int NB>
+template <int HD, int BF16>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tree_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const FewParams P) {
   PF_TIMELINE(TL_ATTENTION_TREE);
-  using L = FSmem<HD, NB>;
+  using L = FSmem<HD>;
   constexpr int KS = HD / 16, DT = HD / 16, NH = HD / 64, ROWS = L::ROWS, NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_s, last_s;
@@ -200,23 +200,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int k = 0; x < count; ++k) {
     const int u0 = cur.u, cnt = min(cur.w.units - u0, count - x);
     const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
-    float o[NB][DT][4], m[NB][2], l[NB][2];
-    uint32_t qf[NB][KS][2];  // Q^T as the B operand: row 8 b + g
+    float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    uint32_t qf[KS][2];  // Q^T as the B operand: row g
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(P.q + (static_cast<size_t>(at + g / G) * P.nq + kvh * G + g % G) * HD) + t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[b][d][e] = 0.f;
-      m[b][0] = m[b][1] = -INFINITY;
-      l[b][0] = l[b][1] = 0.f;
-      const int r = 8 * b + g;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(P.q + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD) + t;
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) qf[b][k][e] = r < R ? src[8 * k + 4 * e] : 0u;
-    }
+      for (int e = 0; e < 2; ++e) qf[k][e] = g < R ? src[8 * k + 4 * e] : 0u;
     // the next task's rows and tree towards L1
     WorkCursor<decltype(work)> nxt = cur;
     if (x + cnt < count) {
@@ -226,27 +220,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         prefetch_l1(P.q + (static_cast<size_t>(nxt.s.at + r / G) * P.nq + nxt.task * G + r % G) * HD + 64 * (lane % NH));
       if (B.parent != nullptr && lane == 0) prefetch_l1(B.parent + nxt.s.at);
     }
-    // nodes that the lane's rows (columns 2t, 2t + 1 of each block of 8) see, while the first unit is on its way
-    uint32_t see[NB][2];
+    // nodes that the lane's rows (2t, 2t + 1) see, while the first unit is on its way
+    uint32_t see[2];
     const bool own_keys = (u0 + cnt) * UK > start;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * b + 2 * t + e, node = r / G;
-        see[b][e] = 0;
-        if (r >= R || !own_keys) continue;
-        if (B.parent == nullptr) {
-          see[b][e] = (2u << node) - 1u;
-        } else {
-          for (int j = node; j >= 0;) {
-            bool bad;
-            see[b][e] |= 1u << j;
-            j = tree_parent(B.parent + at, j, bad);
-            if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
-          }
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * t + e, node = r / G;
+      see[e] = 0;
+      if (r >= R || !own_keys) continue;
+      if (B.parent == nullptr) {
+        see[e] = (2u << node) - 1u;
+      } else {
+        for (int j = node; j >= 0;) {
+          bool bad;
+          see[e] |= 1u << j;
+          j = tree_parent(B.parent + at, j, bad);
+          if (bad) batch_record(P.status, PF_ERR_INVALID_ARG);
         }
       }
+    }
     for (; i < x + cnt && !failed; i += WARPS) {
       const int unit = u0 + i - x, key0 = unit * UK;
       const int stage = warp * L::WS + st;
@@ -266,89 +258,74 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       // scores of 32 keys: two tiles of 16
-      float sc[NB][2][4];
+      float sc[2][4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[b][mt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[mt][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t a[4];
           ldsm4(a, chunk_at(kt, 16 * mt + krow, 2 * k + kch));
-#pragma unroll
-          for (int b = 0; b < NB; ++b) mma16816<BF16>(sc[b][mt], a, qf[b][k][0], qf[b][k][1]);
+          mma16816<BF16>(sc[mt], a, qf[k][0], qf[k][1]);
         }
       if (tail) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = key0 + 16 * mt + 8 * (e >> 1) + g - start;  // node of the key
-              if (j >= 0 && (j >= n || !(see[b][e & 1] >> j & 1u))) sc[b][mt][e] = -INFINITY;
-            }
-      }
-      float mx[NB][2];
-      bool raise = false;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[b][e] = fmaxf(fmaxf(sc[b][0][e], sc[b][0][e + 2]), fmaxf(sc[b][1][e], sc[b][1][e + 2])) * P.scale_log2;
-          raise |= mx[b][e] > m[b][e] + RESCALE_LOG2;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = mx[b][e];
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
-            const float mn = fmaxf(m[b][e], y);
-            const float alpha = mn == -INFINITY ? 1.f : ex2(m[b][e] - mn);
-            m[b][e] = mn;
-            l[b][e] *= alpha;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              o[b][d][e] *= alpha;
-              o[b][d][e + 2] *= alpha;
-            }
-          }
-      }
-      // P^T as the B operand: [16-key tile][register]; of a bf16 cache as two terms, hi + lo
-      uint32_t pf[NB][2][2], pl[NB][2][2];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const float n0 = m[b][0] == -INFINITY ? 0.f : -m[b][0], n1 = m[b][1] == -INFINITY ? 0.f : -m[b][1];
-#pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float p0 = ex2(fmaf(sc[b][mt][2 * hh], P.scale_log2, n0)), p1 = ex2(fmaf(sc[b][mt][2 * hh + 1], P.scale_log2, n1));
-            l[b][0] += p0;
-            l[b][1] += p1;
-            const uint32_t hi = pack2<BF16>(p0, p1);
-            pf[b][mt][hh] = transpose8x8(hi);
-            if (BF16) pl[b][mt][hh] = transpose8x8(pack2<BF16>(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
+          for (int e = 0; e < 4; ++e) {
+            const int j = key0 + 16 * mt + 8 * (e >> 1) + g - start;  // node of the key
+            if (j >= 0 && (j >= n || !(see[e & 1] >> j & 1u))) sc[mt][e] = -INFINITY;
           }
       }
+      float mx[2];
+      bool raise = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(fmaxf(sc[0][e], sc[0][e + 2]), fmaxf(sc[1][e], sc[1][e + 2])) * P.scale_log2;
+        raise |= mx[e] > m[e] + RESCALE_LOG2;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = mx[e];
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+          const float mn = fmaxf(m[e], y);
+          const float alpha = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
+          m[e] = mn;
+          l[e] *= alpha;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d][e] *= alpha;
+            o[d][e + 2] *= alpha;
+          }
+        }
+      }
+      // P^T as the B operand: [16-key tile][register]; of a bf16 cache as two terms, hi + lo
+      uint32_t pf[2][2], pl[2][2];
+      const float n0 = m[0] == -INFINITY ? 0.f : -m[0], n1 = m[1] == -INFINITY ? 0.f : -m[1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float p0 = ex2(fmaf(sc[mt][2 * hh], P.scale_log2, n0)), p1 = ex2(fmaf(sc[mt][2 * hh + 1], P.scale_log2, n1));
+          l[0] += p0;
+          l[1] += p1;
+          const uint32_t hi = pack2<BF16>(p0, p1);
+          pf[mt][hh] = transpose8x8(hi);
+          if (BF16) pl[mt][hh] = transpose8x8(pack2<BF16>(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
+        }
 #pragma unroll
       for (int kt2 = 0; kt2 < 2; ++kt2)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           uint32_t a[4];
           ldsm4_t(a, chunk_at(vt, 16 * kt2 + vrow, 2 * d + vch));
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if (BF16) mma16816<BF16>(o[b][d], a, pl[b][kt2][0], pl[b][kt2][1]);
-            mma16816<BF16>(o[b][d], a, pf[b][kt2][0], pf[b][kt2][1]);
-          }
+          if (BF16) mma16816<BF16>(o[d], a, pl[kt2][0], pl[kt2][1]);
+          mma16816<BF16>(o[d], a, pf[kt2][0], pf[kt2][1]);
         }
       __syncwarp();  // every lane has read the stage
       if (iu < count) {
@@ -377,21 +354,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       __threadfence_block();
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * t + e;
+      float y = l[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * b + 2 * t + e;
-        float y = l[b][e];
+      for (int w = 4; w < 32; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+      if (g == 0) mls[warp * ROWS + r] = make_float2(m[e], y);
+      float* dst = os + (warp * ROWS + r) * L::OW + g;
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-        if (g == 0) mls[warp * ROWS + r] = make_float2(m[b][e], y);
-        float* dst = os + (warp * ROWS + r) * L::OW + g;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          dst[16 * d] = o[b][d][e];
-          dst[16 * d + 8] = o[b][d][e + 2];
-        }
+      for (int d = 0; d < DT; ++d) {
+        dst[16 * d] = o[d][e];
+        dst[16 * d + 8] = o[d][e + 2];
       }
+    }
     constexpr int LPR = HD / 4;  // threads per row, four columns each
     const int col = (threadIdx.x % LPR) * 4;
     auto store_out = [&](int r, float4 v, float f) {
@@ -457,40 +432,81 @@ __global__ void __launch_bounds__(THREADS, 1)
       int* ctr = P.counters + cur.b * P.nkv + kvh;
       __syncthreads();
       if (threadIdx.x == 0) {
-        turn_s[mb] = turn + 1;  // the buffer is free
-        __threadfence();        // the CTA's part, before the count
+        __threadfence();  // the CTA's part, before the count
         last_s = !failed && atomicAdd(ctr, 1) == c1 - c0;
         __threadfence();  // the count, before the other parts
       }
       __syncthreads();
       if (last_s) {
+        // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c: warp w adds parts c0 + w, c0 + w + 4, .., as many of them in
+        // flight as registers hold, and the warps' sums meet as before
+        constexpr int RPW = 32 / LPR, RB = 4, PB = 5;  // rows side by side in a warp, below one another, parts
         const int place0 = line.place(c0, task_first);
-        // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c
-        for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float mr = -INFINITY, lr = 0.f;
-          for (int c = c0; c <= c1; c += 8) {
-            float4 v[8];
-            float2 ml[8];
+        for (int r0 = lane / LPR; r0 < R; r0 += RB * RPW) {
+          float4 acc[RB];
+          float mr[RB], lr[RB];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const float* src = P.part + static_cast<size_t>(c + y == c0 ? place0 : 2 * min(c + y, c1)) * PLACE;
-              v[y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
-              ml[y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
+          for (int y = 0; y < RB; ++y) {
+            acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            mr[y] = -INFINITY;
+            lr[y] = 0.f;
+          }
+          for (int c = c0 + warp; c <= c1; c += WARPS * PB) {
+            float4 v[PB][RB];
+            float2 ml[PB][RB];
+#pragma unroll
+            for (int p = 0; p < PB; ++p) {
+              const int at_c = c + WARPS * p;
+              const float* src = P.part + static_cast<size_t>(at_c == c0 ? place0 : 2 * at_c) * PLACE;
+#pragma unroll
+              for (int y = 0; y < RB; ++y) {
+                const int r = r0 + RPW * y;
+                v[p][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[p][y] = make_float2(-INFINITY, 0.f);
+                if (at_c <= c1 && r < R) {
+                  v[p][y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
+                  ml[p][y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
+                }
+              }
             }
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              if (c + y > c1) break;
-              const float mn = fmaxf(mr, ml[y].x);
-              const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ml[y].x == -INFINITY ? 0.f : ex2(ml[y].x - mn);
-              mr = mn;
-              lr = lr * a + f * ml[y].y;
-              acc = make_float4(acc.x * a + f * v[y].x, acc.y * a + f * v[y].y, acc.z * a + f * v[y].z, acc.w * a + f * v[y].w);
+            for (int y = 0; y < RB; ++y) {
+              float mn = mr[y];
+#pragma unroll
+              for (int p = 0; p < PB; ++p) mn = fmaxf(mn, ml[p][y].x);
+              const float a = mr[y] == -INFINITY ? 0.f : ex2(mr[y] - mn);
+              mr[y] = mn;
+              lr[y] *= a;
+              acc[y] = make_float4(acc[y].x * a, acc[y].y * a, acc[y].z * a, acc[y].w * a);
+#pragma unroll
+              for (int p = 0; p < PB; ++p) {
+                const float w = ml[p][y].x == -INFINITY ? 0.f : ex2(ml[p][y].x - mn);
+                lr[y] = fmaf(w, ml[p][y].y, lr[y]);
+                acc[y] = make_float4(fmaf(w, v[p][y].x, acc[y].x), fmaf(w, v[p][y].y, acc[y].y), fmaf(w, v[p][y].z, acc[y].z),
+                                     fmaf(w, v[p][y].w, acc[y].w));
+              }
             }
           }
+#pragma unroll
+          for (int y = 0; y < RB; ++y) {
+            const int r = r0 + RPW * y;
+            if (r >= R) break;
+            *reinterpret_cast<float4*>(os + (warp * ROWS + r) * L::OW + col) = acc[y];
+            if (col == 0) mls[warp * ROWS + r] = make_float2(mr[y], lr[y]);
+          }
+        }
+        __syncthreads();
+        for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
+          float mr, lr;
+          const float4 acc = add_row(r, mr, lr);
           store_out(r, acc, 1.f / lr);
         }
         if (threadIdx.x == 0) *ctr = 0;  // every part is in: ready for the next call
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) {
+        __threadfence_block();
+        *reinterpret_cast<volatile int*>(turn_s + mb) = turn + 1;  // the buffer is free
       }
     }
     x += cnt;
@@ -507,9 +523,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 
-template <int HD, int BF16, int NB>
+template <int HD, int BF16>
 cudaError_t launch_few(const TreeAttnArgs& a, cudaStream_t stream) {
-  using L = FSmem<HD, NB>;
+  using L = FSmem<HD>;
   const pf_config& c = *a.c;
   const int slots = cache_slots(c);
   const uint64_t dims[2] = {HD, static_cast<uint64_t>(c.n_layers) * c.n_kv_heads * slots}, strides[1] = {HD * 2};
@@ -529,30 +545,25 @@ cudaError_t launch_few(const TreeAttnArgs& a, cudaStream_t stream) {
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c));
   p.status = a.status;
   const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
-  return launch_pdl(attn_tree_few_kernel<HD, BF16, NB>, dim3(ctas), dim3(THREADS), L::BYTES, stream, tk, tv, p);
+  return launch_pdl(attn_tree_few_kernel<HD, BF16>, dim3(ctas), dim3(THREADS), L::BYTES, stream, tk, tv, p);
 }
 
 template <int HD, int BF16>
 cudaError_t launch_rows(const TreeAttnArgs& a, cudaStream_t stream) {
   const int R = std::min(a.b->max_rows, a.b->n_rows) * (a.c->n_q_heads / a.c->n_kv_heads);
-  if (R <= 8) return launch_few<HD, BF16, 1>(a, stream);
-  if (R <= FEW_ROWS) return launch_few<HD, BF16, 2>(a, stream);
-  return launch_attention_tree_tc(a, stream);
+  return R <= FEW_ROWS ? launch_few<HD, BF16>(a, stream) : launch_attention_tree_tc(a, stream);
 }
 
 template <int HD, int BF16>
 cudaError_t set_attr_few() {
-  const cudaError_t e = cudaFuncSetAttribute(attn_tree_few_kernel<HD, BF16, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<HD, 1>::BYTES);
-  const cudaError_t f = cudaFuncSetAttribute(attn_tree_few_kernel<HD, BF16, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<HD, 2>::BYTES);
-  return e != cudaSuccess ? e : f;
+  return cudaFuncSetAttribute(attn_tree_few_kernel<HD, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<HD>::BYTES);
 }
 
 }  // namespace
 
 size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows) {
   // either form: a call with fewer rows than max_rows may take the other
-  const int rows = std::min(FEW_ROWS, (max_rows * (c.n_q_heads / c.n_kv_heads) + 7) / 8 * 8);
-  const size_t few = tree_counter_bytes(c) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * rows * (c.head_dim + 2) * sizeof(float);
+  const size_t few = tree_counter_bytes(c) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * FEW_ROWS * (c.head_dim + 2) * sizeof(float);
   return std::max(few, attention_tree_tc_scratch_bytes(c, n_seq, max_rows));
 }
 

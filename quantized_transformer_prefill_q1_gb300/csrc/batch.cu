@@ -18,7 +18,7 @@ namespace {
 // A CTA takes PAIRS (row, head) pairs of one sequence. What a row needs (slot, depth in its tree) is a chain of
 // dependent loads (rows -> parents -> table): one thread per row runs it while the heads' values are on their way.
 constexpr int AP_THREADS = 256;
-constexpr int AP_ROWS = 64;  // most rows that a CTA's pairs lie in: 128 / 4 + 2 at hd 64 (4 heads), 64 / 3 + 2 at 128
+constexpr int AP_ROWS = 20;  // most rows that a CTA's pairs lie in: 64 / 4 + 2 at hd 64 (4 heads or more), 32 / 3 + 2 at 128
 
 template <typename T>
 __device__ __forceinline__ void put4(T* dst, float a, float b, float c, float d);
@@ -123,12 +123,15 @@ __global__ void __launch_bounds__(AP_THREADS) batch_append_kernel(const BatchDev
 template <int HD, typename T>
 cudaError_t append(const pf_config& c, const pf_batch& b, const float* qkv, const float* qn, const float* kn, const float* rope,
                    int layer, void* q, void* kc, void* vc, int* status, cudaStream_t stream) {
-  constexpr int SLOTS = 4, PAIRS = AP_THREADS / (HD / 8) * SLOTS;
-  const int heads = c.n_q_heads + 2 * c.n_kv_heads;
-  const dim3 grid((std::min(b.max_rows, b.n_rows) * heads + PAIRS - 1) / PAIRS, b.n_seq);
-  return launch_pdl(batch_append_kernel<HD, T, SLOTS>, grid, dim3(AP_THREADS), 0, stream, batch_dev(c, b), qkv, qn, kn, rope,
-                    c.n_q_heads, c.n_kv_heads, layer, c.eps, c.qk_norm, static_cast<T*>(q), static_cast<T*>(kc),
-                    static_cast<T*>(vc), status);
+  constexpr int PER = AP_THREADS / (HD / 8);
+  const int pairs = std::min(b.max_rows, b.n_rows) * (c.n_q_heads + 2 * c.n_kv_heads);
+  auto go = [&](auto kernel, int per) {
+    return launch_pdl(kernel, dim3((pairs + per - 1) / per, b.n_seq), dim3(AP_THREADS), 0, stream, batch_dev(c, b), qkv, qn, kn, rope,
+                      c.n_q_heads, c.n_kv_heads, layer, c.eps, c.qk_norm, static_cast<T*>(q), static_cast<T*>(kc),
+                      static_cast<T*>(vc), status);
+  };
+  const int64_t ctas = static_cast<int64_t>((pairs + PER - 1) / PER) * b.n_seq;
+  return ctas <= 2 * device_sm_count() ? go(batch_append_kernel<HD, T, 1>, PER) : go(batch_append_kernel<HD, T, 2>, 2 * PER);
 }
 
 // ------------------------------------------------------------------ accept
