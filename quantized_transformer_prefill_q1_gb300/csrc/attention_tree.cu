@@ -32,6 +32,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int UK = 32;  // keys per unit
+constexpr int LEAD = 4;  // what a task costs beside its keys, in units
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr int FEW_ROWS = 8;  // most rows per kv head of this form: the n side of an MMA
 
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x < L::NM) arrived_s[threadIdx.x] = turn_s[threadIdx.x] = 0;
   __syncthreads();
   griddep_wait();
-  auto work = [&](const SeqRows& s) -> SeqWork { return {P.nkv, s.n > 0 ? (s.start + s.n + UK - 1) / UK : 0}; };
+  const int lead = task_lead(B, LEAD);
+  auto work = [&](const SeqRows& s) -> SeqWork { return {P.nkv, s.n > 0 ? lead + (s.start + s.n + UK - 1) / UK : 0}; };
   // every CTA has a unit for each warp, as far as the work goes
   const WorkStart ws = batch_scan<THREADS>(B, work, WARPS, nullptr, P.status);
   const Line& line = ws.line;
@@ -153,10 +155,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   cur.seek(B, work, ws.b, ub - ws.first);
   // the warp's next copy: its place in the line, as a row of the cache (-1: none)
   iss = cur;
-  int iu = warp;  // unit of the range
+  int iu;  // unit of the range
   int irow = 0;
   auto locate = [&]() {
-    int slot = batch_slot(B, iss.b, iss.u * UK);
+    int slot = batch_slot(B, iss.b, (iss.u - lead) * UK);
     if (slot < 0) {
       if (lane == 0) batch_record(P.status, PF_ERR_KV_CAPACITY);
       slot = 0;
@@ -175,17 +177,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   };
-  auto ahead = [&](int d) {  // to the warp's next copy
-    iu += d;
-    if (iu < count) {
+  auto ahead = [&](int d) {  // to the warp's next copy: the next of its units that has keys
+    for (iu += d; iu < count; iu += d) {
       iss.advance(B, work, d);
-      locate();
+      d = WARPS;
+      if (iss.u >= lead) {
+        locate();
+        break;
+      }
     }
   };
-  if (iu < count) {
-    iss.advance(B, work, warp);
-    locate();
-  }
+  iu = 0;
+  ahead(warp);
 #pragma unroll 1
   for (int y = 0; y < L::WS; ++y) {
     if (iu < count) issue(warp * L::WS + y);
@@ -197,8 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   int x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
   int st = 0, ph = 0;         // the latter's stage of the warp's ring, and phase
   bool failed = false;  // after a timeout a warp goes on without its units, so that the others never wait for it
-  for (int k = 0; x < count; ++k) {
-    const int u0 = cur.u, cnt = min(cur.w.units - u0, count - x);
+  for (int k = 0; x < count;) {
+    const int u0 = cur.u - lead, cnt = min(cur.w.units - cur.u, count - x);  // key units from u0 (below 0: the lead) on
+    if (u0 + cnt <= 0) break;  // the range ends before the task's keys
     const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
     float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     uint32_t qf[KS][2];  // Q^T as the B operand: row g
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (; i < x + cnt && !failed; i += WARPS) {
       const int unit = u0 + i - x, key0 = unit * UK;
+      if (unit < 0) continue;
       const int stage = warp * L::WS + st;
       const uint32_t kt = ring + stage * (2 * L::TILE), vt = kt + L::TILE;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, ph, abort_flag))) {
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       return acc;
     };
-    if (cnt == cur.w.units) {
+    if (u0 <= 0 && u0 + cnt == cur.w.units - lead) {
       __syncwarp();
       int in = 0;
       if (lane == 0) {
@@ -405,10 +410,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       in = __shfl_sync(0xffffffffu, in, 0);
       __syncwarp();
       if (in == WARPS - 1) {
-        for (int r = lane / LPR; r < R; r += 32 / LPR) {
-          float mr, lr;
-          const float4 acc = add_row(r, mr, lr);
-          store_out(r, acc, 1.f / lr);
+        constexpr int RB = 4;  // rows at once: their chains overlap
+        for (int r0 = lane / LPR; r0 < R; r0 += RB * (32 / LPR)) {
+          float4 acc[RB];
+          float lr[RB];
+#pragma unroll
+          for (int y = 0; y < RB; ++y) {
+            float mr;
+            acc[y] = add_row(min(r0 + y * (32 / LPR), R - 1), mr, lr[y]);
+          }
+#pragma unroll
+          for (int y = 0; y < RB; ++y)
+            if (r0 + y * (32 / LPR) < R) store_out(r0 + y * (32 / LPR), acc[y], 1.f / lr[y]);
         }
         __syncwarp();
         if (lane == 0) {
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else {
       failed = __syncthreads_or(failed) != 0;
-      const int task_first = ub + x - u0;
+      const int task_first = ub + x - cur.u;
       constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
       float* mine = P.part + line.place(cta, task_first) * PLACE;
       for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         *reinterpret_cast<float4*>(mine + r * HD + col) = acc;
         if (col == 0) reinterpret_cast<float2*>(mine + ROWS * HD)[r] = make_float2(mr, lr);
       }
-      const int c0 = line.owner(task_first), c1 = line.owner(task_first + cur.w.units - 1);
+      const int c0 = line.owner(task_first + lead), c1 = line.owner(task_first + cur.w.units - 1);
       int* ctr = P.counters + cur.b * P.nkv + kvh;
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -511,6 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     x += cnt;
     cur = nxt;
+    ++k;
   }
   if (__syncthreads_or(failed)) {
     // let the copies in flight land before shared memory is released

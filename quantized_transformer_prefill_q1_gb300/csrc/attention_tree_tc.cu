@@ -36,6 +36,7 @@ namespace {
 constexpr int TM = 128;      // rows of a slot
 constexpr int BLOCK = 256;   // rows of a task
 constexpr int TK = 128;      // keys per tile
+constexpr int LEAD = 2;      // what a task costs beside its keys, in tiles
 constexpr int HK = TK / 2;   // keys of one product with V
 constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;
@@ -126,6 +127,8 @@ struct Part {
   int rows;                   // rows of the task (of this block)
   int slots;                  // 2: the slots share the rows; 1: they share the tiles
   int u0, cnt;                // key tiles
+  int all;                    // tiles of the task
+  int units;                  // of the CTA's range: the tiles and the task's lead
 };
 
 template <int HD, int BF16>
@@ -187,8 +190,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
+  const int lead = task_lead(B, LEAD);
   auto work = [&](const SeqRows& s) -> SeqWork {
-    return {P.nkv * ((s.n * G + BLOCK - 1) / BLOCK), s.n > 0 ? (s.start + s.n + TK - 1) / TK : 0};
+    return {P.nkv * ((s.n * G + BLOCK - 1) / BLOCK), s.n > 0 ? lead + (s.start + s.n + TK - 1) / TK : 0};
   };
   // a tile for each slot, as far as the work goes
   const int cta = blockIdx.x;
@@ -210,8 +214,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     p.start = cur.s.start;
     p.rows = min(BLOCK, p.n * G - p.rb * BLOCK);
     p.slots = p.rows > TM ? 2 : 1;
-    p.u0 = cur.u;
-    p.cnt = min(cur.w.units - cur.u, count - x);
+    p.units = min(cur.w.units - cur.u, count - x);
+    p.u0 = max(cur.u - lead, 0);
+    p.cnt = cur.u + p.units - lead - p.u0;  // below 1: the range ends before the task's keys
+    p.all = cur.w.units - lead;
     return p;
   };
   // Order of a part's tiles in the ring: slots == 2: K0 V0 K1 V1 ..; slots == 1: K0 K1 V0 K2 V1 .. (the other
@@ -225,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int x = 0; x < count && ok; ++seg) {
       const Part p = part(x);
+      if (p.cnt < 1) break;
       const int row0 = (P.layer * P.nkv + p.kvh) * B.slots;
       auto tile_row = [&](int j) {  // of tile j + lane
         int slot = 0;
@@ -277,8 +284,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (seg > 0 && j == min(1, p.cnt + lag - 1)) load_q();
         ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
       }
-      x += p.cnt;
-      if (x < count) cur.advance(B, work, p.cnt);
+      x += p.units;
+      if (x < count) cur.advance(B, work, p.units);
     }
     if (lane == 0 && *abort_flag) {  // let copies in flight land before shared memory is released
       if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
@@ -312,6 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int x = 0; x < count && ok; ++seg) {
       const Part p = part(x);
+      if (p.cnt < 1) break;
       auto free_kv = [&](int c) { umma_commit_warp(kv_empty(c % NS)); };
       if (!(ok = wait(q_full, seg & 1))) break;
       if (p.slots == 2) {
@@ -370,8 +378,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       c0 += 2 * p.cnt;
-      x += p.cnt;
-      if (x < count) cur.advance(B, work, p.cnt);
+      x += p.units;
+      if (x < count) cur.advance(B, work, p.units);
     }
     if (!ok) {
       umma_commit_warp(drain_bar);
@@ -388,6 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // tcgen05.ld / st are warp-collective: every branch around them is warp-uniform
     for (int x = 0; x < count; ) {
       const Part p = part(x);
+      if (p.cnt < 1) break;
       const int row = p.rb * BLOCK + (p.slots == 2 ? slot * TM : 0) + r;  // row of the sequence and kv head
       const int node = row / G;
       const bool mine = r < p.rows - (p.slots == 2 ? slot * TM : 0);
@@ -507,8 +516,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (p.slots == 1 && slot == 1) ml_s[r] = make_float2(m, l);
       if (!bar_and(1, SM_THREADS, ok)) break;
       tc_fence_after();
-      const bool whole = p.cnt == cur.w.units;
-      const int task_first = ub + x - p.u0;
+      const bool whole = p.cnt == p.all;
+      const int task_first = ub + x - cur.u;
       float* place = P.part + line.place(cta, task_first) * (static_cast<size_t>(P.part_rows) * (HD + 2));
       __half* dst = P.out + (static_cast<size_t>(p.at + node) * P.nq + p.kvh * G + (row - node * G)) * HD;
       const int pr = row - p.rb * BLOCK;  // row of the place
@@ -578,8 +587,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_before();
       mbar_arrive(o_empty(slot));
       c0 += 2 * p.cnt;
-      x += p.cnt;
-      if (x < count) cur.advance(B, work, p.cnt);
+      x += p.units;
+      if (x < count) cur.advance(B, work, p.units);
     }
   }
 
@@ -613,9 +622,10 @@ __global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(c
   const int rows = s.n * G;
   if (static_cast<int>(blockIdx.x) * MR >= rows) return;
   const int row = blockIdx.x * MR + threadIdx.x % MR, oct = threadIdx.x / MR % COLS, group = threadIdx.x / (MR * COLS);
-  const int rb = blockIdx.x * MR / BLOCK, blocks = (rows + BLOCK - 1) / BLOCK, units = (s.start + s.n + TK - 1) / TK;
+  const int rb = blockIdx.x * MR / BLOCK, blocks = (rows + BLOCK - 1) / BLOCK, lead = task_lead(B, LEAD);
+  const int units = lead + (s.start + s.n + TK - 1) / TK;
   const int first = seq_first + (kvh * blocks + rb) * units;
-  const int c0 = line.owner(first), c1 = line.owner(first + units - 1);
+  const int c0 = line.owner(first + lead), c1 = line.owner(first + units - 1);
   if (c0 == c1) return;  // the same for the whole CTA: its rows lie in one block
   const int pr = min(row, rows - 1) - rb * BLOCK, place0 = line.place(c0, first);
   float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

@@ -53,11 +53,15 @@ __device__ __forceinline__ int tree_parent(const int* parent, int i, bool& bad) 
 
 // ------------------------------------------------------------------ work of a batch cut into even ranges
 // The attention kernels lay the work of all sequences in one line of fewer than 2^31 units: sequence b has `tasks` tasks
-// (a kv head, or a kv head and a block of rows) of `units` key units each, one after the other. CTA c takes
-// units [begin(c), begin(c + 1)), however the lengths lie; a task that a border cuts has one part per CTA.
+// (a kv head, or a kv head and a block of rows) of `units` units each, one after the other: task_lead(..) units that stand for
+// what a task costs beside its keys, then its key units. CTA c takes units [begin(c), begin(c + 1)), however the lengths
+// lie; a task whose keys a border cuts has one part per CTA.
 struct SeqWork {
   int tasks, units;
 };
+
+// Units that a task counts beside its keys (`most` where lengths differ: alone, a sequence's tasks all cost the same).
+__device__ __forceinline__ int task_lead(const BatchDev& B, int most) { return B.n_seq == 1 ? 0 : most; }
 
 struct Line {
   int total, ctas;  // units; CTAs that have any
