@@ -32,7 +32,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int UK = 32;  // keys per unit
-constexpr int LEAD = 4;  // what a task costs beside its keys, in units
+constexpr int LEAD = 3;  // what a task costs beside its keys, in units
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr int FEW_ROWS = 8;  // most rows per kv head of this form: the n side of an MMA
 
@@ -44,10 +44,17 @@ struct FSmem {
   static constexpr int RING = NS * 2 * TILE;
   static constexpr int ROWS = FEW_ROWS;
   static constexpr int OW = HD + 4;  // floats between rows of the warps' O
-  static constexpr int NM = 2;  // merge buffers
-  static constexpr int MERGE = WARPS * ROWS * (OW + 2) * 4;
-  static constexpr int BYTES = 1024 + RING + NM * MERGE + NS * 8;
+  static constexpr int PARTS = 2 * WARPS * ROWS * (OW + 2) * 4;  // two places a warp: O, then (m, l)
+  static constexpr int BYTES = 1024 + RING + PARTS + NS * 8;
   static_assert(BYTES <= 232448 - 384, "shared memory");  // beside the static arrays
+};
+
+// A warp's part of a cut task in shared memory.
+struct WarpPart {
+  int rows;   // 0: none
+  int first;  // the task's first unit in the line
+  int c0, c1; // CTAs that hold its first and its last key units
+  int at, kvh, b;
 };
 
 struct FewParams {
@@ -118,12 +125,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   using L = FSmem<HD>;
   constexpr int KS = HD / 16, DT = HD / 16, NH = HD / 64, ROWS = L::ROWS, NS = L::NS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int abort_s, last_s;
-  __shared__ int arrived_s[L::NM], turn_s[L::NM];  // of each merge buffer: warps whose part is in, tasks it has served
+  __shared__ int abort_s, last_s[2];
+  __shared__ WarpPart part_s[2 * WARPS];
   __shared__ int issued_s[NS];  // copies that each stage has taken (its own warp's lane 0 counts)
   volatile int* abort_flag = &abort_s;
   const uint32_t raw = smem_u32(smem_raw), ring = (raw + 1023u) & ~1023u;
-  const uint32_t bars = ring + L::RING + L::NM * L::MERGE;
+  const uint32_t bars = ring + L::RING + L::PARTS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const BatchDev& B = P.B;
   const int G = P.nq / P.nkv;
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) abort_s = 0;
-  if (threadIdx.x < L::NM) arrived_s[threadIdx.x] = turn_s[threadIdx.x] = 0;
+  if (threadIdx.x < 2 * WARPS) part_s[threadIdx.x].rows = 0;
   __syncthreads();
   griddep_wait();
   const int lead = task_lead(B, LEAD);
@@ -149,15 +156,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   const Line& line = ws.line;
   const int cta = blockIdx.x;
   if (cta >= line.ctas) return;
+  // the warp's units: a run of the CTA's
   const int ub = line.begin(cta), count = line.begin(cta + 1) - ub;
+  const int wb = warp * (count / WARPS) + min(warp, count % WARPS), we = wb + count / WARPS + (warp < count % WARPS ? 1 : 0);
 
   WorkCursor<decltype(work)> cur, iss;
   cur.seek(B, work, ws.b, ub - ws.first);
-  // the warp's next copy: its place in the line, as a row of the cache (-1: none)
+  if (wb < we) cur.advance(B, work, wb);
+  // the warp's next copy: its place in the line, as a row of the cache
   iss = cur;
-  int iu;  // unit of the range
+  int iu = wb;
   int irow = 0;
-  auto locate = [&]() {
+  auto locate = [&]() {  // the next unit with keys from iss on
+    const int d = max(0, lead - iss.u);
+    iu += d;
+    if (iu >= we) return;
+    iss.u += d;
     int slot = batch_slot(B, iss.b, (iss.u - lead) * UK);
     if (slot < 0) {
       if (lane == 0) batch_record(P.status, PF_ERR_KV_CAPACITY);
@@ -176,32 +190,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         tma_load_2d(dst + L::TILE + h * (UK * 128), &tm_v, 64 * h, irow, bar);
       }
     }
-  };
-  auto ahead = [&](int d) {  // to the warp's next copy: the next of its units that has keys
-    for (iu += d; iu < count; iu += d) {
-      iss.advance(B, work, d);
-      d = WARPS;
-      if (iss.u >= lead) {
-        locate();
-        break;
-      }
+    if (++iu < we) {
+      iss.advance(B, work, 1);
+      locate();
     }
   };
-  iu = 0;
-  ahead(warp);
+  if (iu < we) locate();
 #pragma unroll 1
-  for (int y = 0; y < L::WS; ++y) {
-    if (iu < count) issue(warp * L::WS + y);
-    ahead(WARPS);
-  }
+  for (int y = 0; y < L::WS; ++y)
+    if (iu < we) issue(warp * L::WS + y);
+
+  float* os = reinterpret_cast<float*>(smem_raw + (ring - raw) + L::RING);  // O [place][row][OW]
+  float2* mls = reinterpret_cast<float2*>(os + 2 * WARPS * ROWS * L::OW);   // (m, l) [place][row]
+  constexpr int LPR = HD / 4;  // lanes per row, four columns each
+  constexpr int RPW = 32 / LPR;  // rows side by side in a warp
+  const int col = (lane % LPR) * 4, rl = lane / LPR;
+  auto store_out = [&](int at, int kvh, int r, float4 v, float f) {
+    const __half2 a = __floats2half2_rn(v.x * f, v.y * f), c = __floats2half2_rn(v.z * f, v.w * f);
+    *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD + col) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+  };
 
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;   // ldmatrix address of K: keys x chunks
   const int vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;  // of V (transposed)
-  int x = 0, i = warp;  // units of the range: where the task's part begins, the warp's next one
-  int st = 0, ph = 0;         // the latter's stage of the warp's ring, and phase
-  bool failed = false;  // after a timeout a warp goes on without its units, so that the others never wait for it
-  for (int k = 0; x < count;) {
-    const int u0 = cur.u - lead, cnt = min(cur.w.units - cur.u, count - x);  // key units from u0 (below 0: the lead) on
+  int st = 0, ph = 0;   // stage of the warp's ring, and phase
+  bool failed = false;  // after a timeout
+  for (int x = wb; x < we;) {
+    const int u0 = cur.u - lead, cnt = min(cur.w.units - cur.u, we - x);  // key units from u0 (below 0: the lead) on
     if (u0 + cnt <= 0) break;  // the range ends before the task's keys
     const int kvh = cur.task, at = cur.s.at, n = cur.s.n, start = cur.s.start, len = start + n, R = n * G;
     float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -217,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int e = 0; e < 2; ++e) qf[k][e] = g < R ? src[8 * k + 4 * e] : 0u;
     // the next task's rows and tree towards L1
     WorkCursor<decltype(work)> nxt = cur;
-    if (x + cnt < count) {
+    if (x + cnt < we) {
       nxt.advance(B, work, cnt);
       const int r = lane / NH;
       if (r < nxt.s.n * G)
@@ -243,9 +258,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    for (; i < x + cnt && !failed; i += WARPS) {
-      const int unit = u0 + i - x, key0 = unit * UK;
-      if (unit < 0) continue;
+    for (int unit = max(u0, 0); unit < u0 + cnt; ++unit) {
+      const int key0 = unit * UK;
       const int stage = warp * L::WS + st;
       const uint32_t kt = ring + stage * (2 * L::TILE), vt = kt + L::TILE;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, ph, abort_flag))) {
@@ -333,198 +347,206 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma16816<BF16>(o[d], a, pf[kt2][0], pf[kt2][1]);
         }
       __syncwarp();  // every lane has read the stage
-      if (iu < count) {
-        issue(stage);
-        ahead(WARPS);
-      }
+      if (iu < we) issue(stage);
       if (++st == L::WS) {
         st = 0;
         ph ^= 1;
       }
     }
-    // The warps' parts of this task meet in a buffer: of a task that lies in this CTA, the warp that comes last adds them
-    // while the others go on.
-    const int mb = k % L::NM, turn = k / L::NM;
-    float* os = reinterpret_cast<float*>(smem_raw + (ring - raw) + L::RING + mb * L::MERGE);  // O [warp][row][OW], then (m, l)
-    float2* mls = reinterpret_cast<float2*>(os + WARPS * ROWS * L::OW);
-    if (turn > 0 && !failed) {
-      const uint64_t w0 = global_timer_ns();
-      while (*reinterpret_cast<volatile int*>(turn_s + mb) < turn && !failed) {
-        if (*abort_flag || global_timer_ns() - w0 > PF_WAIT_LIMIT_NS) {
-          *abort_flag = 1;
-          failed = true;
-        }
-      }
-      failed = __any_sync(0xffffffffu, failed);
-      __threadfence_block();
+    if (failed) break;
+    // O and (m, l) to one of the warp's places: of a task that began before the warp's range (or with it) the first, else the
+    // second, which only the warp's last task may need for a part; the whole ones before it pass through it to the output.
+    const int first = ub + x - cur.u;
+    const bool whole = u0 <= 0 && u0 + cnt == cur.w.units - lead;
+    const int place = 2 * warp + (whole || first > ub + wb ? 1 : 0);
+    if (!whole) {
+      const WarpPart T{R, first, line.owner(first + lead), line.owner(first + cur.w.units - 1), at, kvh, cur.b};
+      if (lane == 0) part_s[place] = T;
     }
+    __syncwarp();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * t + e;
       float y = l[e];
 #pragma unroll
       for (int w = 4; w < 32; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-      if (g == 0) mls[warp * ROWS + r] = make_float2(m[e], y);
-      float* dst = os + (warp * ROWS + r) * L::OW + g;
+      if (g == 0) mls[place * ROWS + r] = make_float2(m[e], y);
+      float* dst = os + (place * ROWS + r) * L::OW + g;
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         dst[16 * d] = o[d][e];
         dst[16 * d + 8] = o[d][e + 2];
       }
     }
-    constexpr int LPR = HD / 4;  // threads per row, four columns each
-    const int col = (threadIdx.x % LPR) * 4;
-    auto store_out = [&](int r, float4 v, float f) {
-      const __half2 a = __floats2half2_rn(v.x * f, v.y * f), c = __floats2half2_rn(v.z * f, v.w * f);
-      *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(at + r / G) * P.nq + kvh * G + r % G) * HD + col) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    };
-    // row r of the warps' parts: its maximum, sum and the thread's four columns
-    auto add_row = [&](int r, float& mr, float& lr) {
-      float mw[WARPS];
-      mr = -INFINITY;
-      lr = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        mw[w] = mls[w * ROWS + r].x;
-        mr = fmaxf(mr, mw[w]);
-      }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float a = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - mr);
-        const float4 v = *reinterpret_cast<const float4*>(os + (w * ROWS + r) * L::OW + col);
-        lr = fmaf(a, mls[w * ROWS + r].y, lr);
-        acc = make_float4(fmaf(a, v.x, acc.x), fmaf(a, v.y, acc.y), fmaf(a, v.z, acc.z), fmaf(a, v.w, acc.w));
-      }
-      return acc;
-    };
-    if (u0 <= 0 && u0 + cnt == cur.w.units - lead) {
+    if (whole) {
       __syncwarp();
-      int in = 0;
-      if (lane == 0) {
-        __threadfence_block();
-        in = atomicAdd(arrived_s + mb, 1);
-        __threadfence_block();
-      }
-      in = __shfl_sync(0xffffffffu, in, 0);
-      __syncwarp();
-      if (in == WARPS - 1) {
-        constexpr int RB = 4;  // rows at once: their chains overlap
-        for (int r0 = lane / LPR; r0 < R; r0 += RB * (32 / LPR)) {
-          float4 acc[RB];
-          float lr[RB];
+      constexpr int RB = 4;  // rows at once: their loads overlap
+      for (int r0 = rl; r0 < R; r0 += RB * RPW) {
+        float4 v[RB];
+        float inv[RB];
 #pragma unroll
-          for (int y = 0; y < RB; ++y) {
-            float mr;
-            acc[y] = add_row(min(r0 + y * (32 / LPR), R - 1), mr, lr[y]);
-          }
-#pragma unroll
-          for (int y = 0; y < RB; ++y)
-            if (r0 + y * (32 / LPR) < R) store_out(r0 + y * (32 / LPR), acc[y], 1.f / lr[y]);
+        for (int y = 0; y < RB; ++y) {
+          const int r = place * ROWS + min(r0 + y * RPW, R - 1);
+          v[y] = *reinterpret_cast<const float4*>(os + r * L::OW + col);
+          inv[y] = 1.f / mls[r].y;
         }
-        __syncwarp();
-        if (lane == 0) {
-          arrived_s[mb] = 0;
-          __threadfence_block();
-          *reinterpret_cast<volatile int*>(turn_s + mb) = turn + 1;
-        }
-      }
-    } else {
-      failed = __syncthreads_or(failed) != 0;
-      const int task_first = ub + x - cur.u;
-      constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
-      float* mine = P.part + line.place(cta, task_first) * PLACE;
-      for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
-        float mr, lr;
-        const float4 acc = add_row(r, mr, lr);
-        *reinterpret_cast<float4*>(mine + r * HD + col) = acc;
-        if (col == 0) reinterpret_cast<float2*>(mine + ROWS * HD)[r] = make_float2(mr, lr);
-      }
-      const int c0 = line.owner(task_first + lead), c1 = line.owner(task_first + cur.w.units - 1);
-      int* ctr = P.counters + cur.b * P.nkv + kvh;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        __threadfence();  // the CTA's part, before the count
-        last_s = !failed && atomicAdd(ctr, 1) == c1 - c0;
-        __threadfence();  // the count, before the other parts
-      }
-      __syncthreads();
-      if (last_s) {
-        // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c: warp w adds parts c0 + w, c0 + w + 4, .., as many of them in
-        // flight as registers hold, and the warps' sums meet as before
-        constexpr int RPW = 32 / LPR, RB = 4, PB = 5;  // rows side by side in a warp, below one another, parts
-        const int place0 = line.place(c0, task_first);
-        for (int r0 = lane / LPR; r0 < R; r0 += RB * RPW) {
-          float4 acc[RB];
-          float mr[RB], lr[RB];
 #pragma unroll
-          for (int y = 0; y < RB; ++y) {
-            acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-            mr[y] = -INFINITY;
-            lr[y] = 0.f;
-          }
-          for (int c = c0 + warp; c <= c1; c += WARPS * PB) {
-            float4 v[PB][RB];
-            float2 ml[PB][RB];
-#pragma unroll
-            for (int p = 0; p < PB; ++p) {
-              const int at_c = c + WARPS * p;
-              const float* src = P.part + static_cast<size_t>(at_c == c0 ? place0 : 2 * at_c) * PLACE;
-#pragma unroll
-              for (int y = 0; y < RB; ++y) {
-                const int r = r0 + RPW * y;
-                v[p][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                ml[p][y] = make_float2(-INFINITY, 0.f);
-                if (at_c <= c1 && r < R) {
-                  v[p][y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
-                  ml[p][y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
-                }
-              }
-            }
-#pragma unroll
-            for (int y = 0; y < RB; ++y) {
-              float mn = mr[y];
-#pragma unroll
-              for (int p = 0; p < PB; ++p) mn = fmaxf(mn, ml[p][y].x);
-              const float a = mr[y] == -INFINITY ? 0.f : ex2(mr[y] - mn);
-              mr[y] = mn;
-              lr[y] *= a;
-              acc[y] = make_float4(acc[y].x * a, acc[y].y * a, acc[y].z * a, acc[y].w * a);
-#pragma unroll
-              for (int p = 0; p < PB; ++p) {
-                const float w = ml[p][y].x == -INFINITY ? 0.f : ex2(ml[p][y].x - mn);
-                lr[y] = fmaf(w, ml[p][y].y, lr[y]);
-                acc[y] = make_float4(fmaf(w, v[p][y].x, acc[y].x), fmaf(w, v[p][y].y, acc[y].y), fmaf(w, v[p][y].z, acc[y].z),
-                                     fmaf(w, v[p][y].w, acc[y].w));
-              }
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < RB; ++y) {
-            const int r = r0 + RPW * y;
-            if (r >= R) break;
-            *reinterpret_cast<float4*>(os + (warp * ROWS + r) * L::OW + col) = acc[y];
-            if (col == 0) mls[warp * ROWS + r] = make_float2(mr[y], lr[y]);
-          }
-        }
-        __syncthreads();
-        for (int r = threadIdx.x / LPR; r < R; r += THREADS / LPR) {
-          float mr, lr;
-          const float4 acc = add_row(r, mr, lr);
-          store_out(r, acc, 1.f / lr);
-        }
-        if (threadIdx.x == 0) *ctr = 0;  // every part is in: ready for the next call
-        __syncthreads();
-      }
-      if (threadIdx.x == 0) {
-        __threadfence_block();
-        *reinterpret_cast<volatile int*>(turn_s + mb) = turn + 1;  // the buffer is free
+        for (int y = 0; y < RB; ++y)
+          if (r0 + y * RPW < R) store_out(at, kvh, r0 + y * RPW, v[y], inv[y]);
       }
     }
     x += cnt;
     cur = nxt;
-    ++k;
+  }
+
+  // ------------------------------------------------------------------ parts of cut tasks
+  // At most eight parts of five tasks lie in shared memory. Those of a task with keys in other CTAs too are added and go
+  // to scratch, where the CTA that completes the task's count adds them; of the others the sum is the result.
+  failed = __syncthreads_or(failed) != 0;
+  // row r of place p and of the first places of the warps behind it, up to warp w1: maximum, sum and the lane's four columns
+  auto add_row = [&](int p, int w1, int r, float& mr, float& lr) {
+    float mw[WARPS];
+    mr = -INFINITY;
+    lr = 0.f;
+    const int w0 = p >> 1;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      mw[w] = w >= w0 && w <= w1 ? mls[(w == w0 ? p : 2 * w) * ROWS + r].x : -INFINITY;
+      mr = fmaxf(mr, mw[w]);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < w0 || w > w1) continue;
+      const int i = (w == w0 ? p : 2 * w) * ROWS + r;
+      const float a = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - mr);
+      const float4 v = *reinterpret_cast<const float4*>(os + i * L::OW + col);
+      lr = fmaf(a, mls[i].y, lr);
+      acc = make_float4(fmaf(a, v.x, acc.x), fmaf(a, v.y, acc.y), fmaf(a, v.z, acc.z), fmaf(a, v.w, acc.w));
+    }
+    return acc;
+  };
+  constexpr size_t PLACE = static_cast<size_t>(ROWS) * (HD + 2);
+  // lane p looks at place p: first parts of a task; parts of one that began in an earlier warp; of one with others elsewhere
+  const WarpPart& own = part_s[lane & (2 * WARPS - 1)];
+  const bool some = lane < 2 * WARPS && own.rows > 0;
+  const int first0 = own.first, first1 = __shfl_up_sync(0xffffffffu, some ? first0 : -1, 1), first2 = __shfl_up_sync(0xffffffffu, some ? first0 : -1, 2);
+  const bool goes_on = some && lane >= 2 && !(lane & 1) && (first0 == first1 || first0 == first2);
+  const unsigned all = __ballot_sync(0xffffffffu, some), later = __ballot_sync(0xffffffffu, goes_on), starts = all & ~later;
+  const unsigned apart = __ballot_sync(0xffffffffu, some && own.c0 != own.c1);
+  // f(task, its first place, the warp of its last)
+  auto each_task = [&](unsigned places, auto f) {
+    for (; places != 0; places &= places - 1) {
+      const int p = __ffs(places) - 1;
+      int w1 = p >> 1;
+      // a warp's second place, where it has one, is what goes on in the next warp
+      while ((later >> (2 * w1 + 2) & 1u) && (p == 2 * w1 + 1 || !(all >> (2 * w1 + 1) & 1u))) ++w1;
+      f(part_s[p], p, w1);
+    }
+  };
+  int cut[2] = {0, 0}, cuts = 0;  // first places of the tasks with parts in other CTAs
+  if (!failed)
+    each_task(starts & apart, [&](const WarpPart& T, int p, int w1) {
+      float* mine = P.part + (2 * cta + (T.first > ub ? 1 : 0)) * PLACE;  // line.place(cta, ..)
+      for (int r = warp * RPW + rl; r < T.rows; r += WARPS * RPW) {
+        float mr, lr;
+        const float4 acc = add_row(p, w1, r, mr, lr);
+        *reinterpret_cast<float4*>(mine + r * HD + col) = acc;
+        if (col == 0) reinterpret_cast<float2*>(mine + ROWS * HD)[r] = make_float2(mr, lr);
+      }
+      (cuts == 0 ? cut[0] : cut[1]) = p;
+      ++cuts;
+    });
+  int before = 0;
+  const bool counts = static_cast<int>(threadIdx.x) < cuts;
+  const WarpPart& mine = part_s[threadIdx.x == 0 ? cut[0] : cut[1]];
+  if (cuts > 0) __syncthreads();
+  if (counts) {
+    __threadfence();  // the CTA's part, before the count
+    before = atomicAdd(P.counters + mine.b * P.nkv + mine.kvh, 1);
+  }
+  if (!failed)
+    each_task(starts & ~apart, [&](const WarpPart& T, int p, int w1) {
+      for (int r = warp * RPW + rl; r < T.rows; r += WARPS * RPW) {
+        float mr, lr;
+        const float4 acc = add_row(p, w1, r, mr, lr);
+        store_out(T.at, T.kvh, r, acc, 1.f / lr);
+      }
+    });
+  if (counts) {
+    last_s[threadIdx.x] = before == mine.c1 - mine.c0;
+    __threadfence();  // the count, before the other parts
+  }
+  if (cuts > 0) __syncthreads();
+  for (int k = 0; k < cuts; ++k) {
+    if (!last_s[k]) continue;
+    const WarpPart T = part_s[k == 0 ? cut[0] : cut[1]];
+    const int c0 = T.c0, c1 = T.c1;
+    // O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c: warp w adds parts c0 + w, c0 + w + 4, .., as many of them in
+    // flight as registers hold, and the warps' sums meet as before
+    constexpr int RB = 4, PB = 5;  // rows below one another, parts
+    const int place0 = line.place(c0, T.first);
+    for (int r0 = rl; r0 < T.rows; r0 += RB * RPW) {
+      float4 acc[RB];
+      float mr[RB], lr[RB];
+#pragma unroll
+      for (int y = 0; y < RB; ++y) {
+        acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        mr[y] = -INFINITY;
+        lr[y] = 0.f;
+      }
+      for (int c = c0 + warp; c <= c1; c += WARPS * PB) {
+        float4 v[PB][RB];
+        float2 ml[PB][RB];
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+          const int from = c + WARPS * p;
+          const float* src = P.part + static_cast<size_t>(from == c0 ? place0 : 2 * from) * PLACE;
+#pragma unroll
+          for (int y = 0; y < RB; ++y) {
+            const int r = r0 + RPW * y;
+            v[p][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            ml[p][y] = make_float2(-INFINITY, 0.f);
+            if (from <= c1 && r < T.rows) {
+              v[p][y] = __ldcg(reinterpret_cast<const float4*>(src + r * HD + col));
+              ml[p][y] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * HD) + r);
+            }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < RB; ++y) {
+          float mn = mr[y];
+#pragma unroll
+          for (int p = 0; p < PB; ++p) mn = fmaxf(mn, ml[p][y].x);
+          const float a = mr[y] == -INFINITY ? 0.f : ex2(mr[y] - mn);
+          mr[y] = mn;
+          lr[y] *= a;
+          acc[y] = make_float4(acc[y].x * a, acc[y].y * a, acc[y].z * a, acc[y].w * a);
+#pragma unroll
+          for (int p = 0; p < PB; ++p) {
+            const float w = ml[p][y].x == -INFINITY ? 0.f : ex2(ml[p][y].x - mn);
+            lr[y] = fmaf(w, ml[p][y].y, lr[y]);
+            acc[y] = make_float4(fmaf(w, v[p][y].x, acc[y].x), fmaf(w, v[p][y].y, acc[y].y), fmaf(w, v[p][y].z, acc[y].z),
+                                 fmaf(w, v[p][y].w, acc[y].w));
+          }
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < RB; ++y) {
+        const int r = r0 + RPW * y;
+        if (r >= T.rows) break;
+        *reinterpret_cast<float4*>(os + (2 * warp * ROWS + r) * L::OW + col) = acc[y];
+        if (col == 0) mls[2 * warp * ROWS + r] = make_float2(mr[y], lr[y]);
+      }
+    }
+    __syncthreads();
+    for (int r = warp * RPW + rl; r < T.rows; r += WARPS * RPW) {
+      float mr, lr;
+      const float4 acc = add_row(0, WARPS - 1, r, mr, lr);
+      store_out(T.at, T.kvh, r, acc, 1.f / lr);
+    }
+    if (threadIdx.x == 0) P.counters[T.b * P.nkv + T.kvh] = 0;  // every part is in: ready for the next call
+    __syncthreads();
   }
   if (__syncthreads_or(failed)) {
     // let the copies in flight land before shared memory is released

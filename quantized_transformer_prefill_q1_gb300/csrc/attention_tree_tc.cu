@@ -36,7 +36,7 @@ namespace {
 constexpr int TM = 128;      // rows of a slot
 constexpr int BLOCK = 256;   // rows of a task
 constexpr int TK = 128;      // keys per tile
-constexpr int LEAD = 2;      // what a task costs beside its keys, in tiles
+constexpr int LEAD = 4;      // what a task costs beside its keys, in tiles
 constexpr int HK = TK / 2;   // keys of one product with V
 constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;

@@ -1527,11 +1527,11 @@ pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, cons
   if (!q || !kc || !vc || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out))
     return fail(PF_ERR_INVALID_ARG, "q, caches and out must be 16-B aligned");
-  // units of 32 keys of the longest sequences (and four that a task counts beside them), in blocks of 256 rows: the kernels
+  // units of 32 keys of the longest sequences (and up to 16 that a task counts beside them), in blocks of 256 rows: the kernels
   // count them in 32 bits
   const int64_t blocks = (static_cast<int64_t>(batch->max_rows) * (cfg->n_q_heads / cfg->n_kv_heads) + 255) / 256;
-  if (static_cast<int64_t>(batch->n_seq) * cfg->n_kv_heads * blocks * ((cfg->max_seq + 31) / 32 + 4) > 0x7fffffff)
-    return fail(PF_ERR_SHAPE, "sequences x kv heads x blocks of 256 query rows x (max_seq / 32 + 4): below 2^31");
+  if (static_cast<int64_t>(batch->n_seq) * cfg->n_kv_heads * blocks * ((cfg->max_seq + 31) / 32 + 16) > 0x7fffffff)
+    return fail(PF_ERR_SHAPE, "sequences x kv heads x blocks of 256 query rows x (max_seq / 32 + 16): below 2^31");
   const size_t need = attention_tree_scratch_bytes(*cfg, batch->n_seq, batch->max_rows);
   if (scratch_bytes < need || !scratch)
     return fail(PF_ERR_WORKSPACE, "tree attention scratch %zu bytes, need %zu", scratch_bytes, need);
