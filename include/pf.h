@@ -564,7 +564,8 @@ pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const 
  * as either grows: a larger batch's scratch serves every smaller one of the same heads), zero before its first call with a
  * number of kv heads; each call that completes leaves it ready for the next (after PF_ERR_DEVICE_TIMEOUT zero it
  * again). Calls sharing one scratch must not overlap in time, nor graphs that captured them. Softmax weights enter the
- * product with V in the cache's type (up to 8 query rows, nodes x G, per kv head of a bf16 cache: as two bf16 terms), sums in f32. */
+ * product with V in the cache's type (up to max_rows G = 8 query rows per kv head of a bf16 cache: as two bf16 terms),
+ * sums in f32. */
 size_t pf_attention_tree_scratch_bytes(const pf_config* cfg, int32_t n_seq, int32_t max_rows);
 pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, const void* q_dev, const void* k_cache_dev,
                                const void* v_cache_dev, int32_t layer, uint16_t* out_f16_dev, void* scratch_dev,
@@ -586,7 +587,8 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
  * with the same ld: the residual form, and rows without an adapter are then not touched), A f16 [n_adapters][rank][K], B f16
  * [n_adapters][N][rank], scale f32 [n_adapters]. rank a multiple of 8 up to PF_MAX_RANK (adapters of lower rank:
  * zero rows of A); K a multiple of 16, N of 8, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
- * aligned. Products and sums in f32 (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
+ * aligned; n_adapters * rank below 2^31. out overlaps neither x nor, unless it is base, base. Products and sums in f32
+ * (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
  * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. batch: row_begin only; sequences of
  * up to 8192 rows. No scratch. */
 pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x_f16_dev, int64_t ldx, const float* base_dev, int64_t ld_base,

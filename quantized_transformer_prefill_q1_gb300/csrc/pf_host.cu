@@ -1527,6 +1527,7 @@ pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, cons
   if (!q || !kc || !vc || !out) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out))
     return fail(PF_ERR_INVALID_ARG, "q, caches and out must be 16-B aligned");
+  if (q == out) return fail(PF_ERR_INVALID_ARG, "out must not be q");
   // units of 32 keys of the longest sequences (and up to 16 that a task counts beside them), in blocks of 256 rows: the kernels
   // count them in 32 bits
   const int64_t blocks = (static_cast<int64_t>(batch->max_rows) * (cfg->n_q_heads / cfg->n_kv_heads) + 255) / 256;
@@ -1563,7 +1564,8 @@ pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, 
   PF_TRY(check_batch_rows(batch, false));
   if (rank < 8 || rank > PF_MAX_RANK || rank % 8) return fail(PF_ERR_SHAPE, "rank %d: a multiple of 8 up to %d", rank, PF_MAX_RANK);
   if (K < 16 || K % 16 || N < 8 || N % 8) return fail(PF_ERR_SHAPE, "K %d: a multiple of 16; N %d: of 8", K, N);
-  if (n_adapters < 1) return fail(PF_ERR_SHAPE, "n_adapters %d", n_adapters);
+  if (n_adapters < 1 || static_cast<int64_t>(n_adapters) * rank > 0x7fffffff)
+    return fail(PF_ERR_SHAPE, "n_adapters %d: at least 1, n_adapters x rank below 2^31", n_adapters);
   if (ldx < K || ldx % 8 || ld_base < N || ld_base % 4 || ld_out < N || ld_out % 4)
     return fail(PF_ERR_SHAPE, "ldx %lld: at least K, a multiple of 8; ld_base %lld, ld_out %lld: at least N, multiples of 4",
                 (long long)ldx, (long long)ld_base, (long long)ld_out);

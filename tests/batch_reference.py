@@ -43,9 +43,9 @@ def append(qkv, nq, nkv, hd, qn, kn, eps, theta, positions):
     return y[:, :nq], y[:, nq:], x[:, nq + nkv:], size
 
 
-def attention(q, k, v, start, parent, kind):
+def attention(q, k, v, start, parent, weights):
     """(out [n, nq, hd], bound): q [n, nq, hd] over k, v [nkv, start + n, hd]. The bound on a result in f16: half a
-    step of the output; weights rounded to the cache's type; a score's error d from the f32 sums of hd products and
+    step of the output; `weights`, the weights' own rounding; a score's error d from the f32 sums of hd products and
     its scaling, which changes a weight and the weights' sum by a factor 1 + d each; f32 sums over the keys; the
     exponential's 2^-21."""
     n, nq, hd = q.shape
@@ -62,7 +62,7 @@ def attention(q, k, v, start, parent, kind):
         out[:, h] = p @ vv
         size = np.where(see, np.abs(q[:, h]) @ np.abs(kk).T / np.sqrt(hd), 0).max(1, keepdims=True)
         d = (hd + 4) * 2.0 ** -24 * size
-        bound[:, h] = 2.0 ** -11 * np.abs(out[:, h]) + 2.0 ** -25 + (half_step(kind) + 2 * d + (length + 64) * 2.0 ** -24 + 2.0 ** -20) * (p @ np.abs(vv))
+        bound[:, h] = 2.0 ** -11 * np.abs(out[:, h]) + 2.0 ** -25 + (weights + 2 * d + (length + 64) * 2.0 ** -24 + 2.0 ** -20) * (p @ np.abs(vv))
     return out, bound
 
 

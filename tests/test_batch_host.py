@@ -33,7 +33,7 @@ def append(lib, c=None, b=None, qkv=P, qn=P, kn=P, rope=P, layer=1, q=P, kc=P, v
     return name(lib.pf_op_batch_append(ctypes.byref(c), ctypes.byref(b) if b else None, qkv, qn, kn, rope, layer, q, kc, vc, None, None))
 
 
-def attend(lib, c=None, b=None, q=P, kc=P, vc=P, layer=1, out=P, scratch=P, nbytes=1 << 40):
+def attend(lib, c=None, b=None, q=P, kc=P, vc=P, layer=1, out=2 * P, scratch=P, nbytes=1 << 40):
     c, b = c or config(), b if b is not None else batch()
     return name(lib.pf_op_attention_tree(ctypes.byref(c), ctypes.byref(b) if b else None, q, kc, vc, layer, out, scratch, nbytes, None, None))
 
@@ -75,6 +75,7 @@ def test_pointer_refusals(lib):
     for kw in ("q", "kc", "vc", "out"):
         assert attend(lib, **{kw: None}) == "PF_ERR_INVALID_ARG", kw
         assert attend(lib, **{kw: P + 8}) == "PF_ERR_INVALID_ARG", kw
+    assert attend(lib, out=P) == "PF_ERR_INVALID_ARG"  # q
     assert attend(lib, scratch=None) == "PF_ERR_WORKSPACE"
     assert attend(lib, scratch=P + 4) == "PF_ERR_INVALID_ARG"
     need = lib.pf_attention_tree_scratch_bytes(ctypes.byref(config()), 1, 10)
@@ -91,10 +92,20 @@ def test_adapter_refusals(lib):
         assert adapters(lib, **{kw: None}) == "PF_ERR_INVALID_ARG", kw
     for kw in ("x", "base", "out", "wa", "wb"):
         assert adapters(lib, **{kw: P + 8}) == "PF_ERR_INVALID_ARG", kw
-    for kw in (dict(rank=0), dict(rank=12), dict(rank=136), dict(k=0), dict(k=24), dict(n=0), dict(n=12), dict(count=0), dict(ldx=56), dict(ldx=68),
+    for kw in (dict(rank=0), dict(rank=12), dict(rank=136), dict(k=0), dict(k=24), dict(n=0), dict(n=12), dict(count=0), dict(count=2 ** 28), dict(ldx=56), dict(ldx=68),
                dict(ldb=28), dict(ldb=34), dict(ldo=28), dict(ldo=33), dict(out=P, ldo=36), dict(b=batch(max_rows=8193)), dict(b=batch(n_seq=2000))):
         assert adapters(lib, **kw) == "PF_ERR_SHAPE", kw
     assert adapters(lib, b=batch(n_rows=0)) == "PF_ERR_EMPTY_CHUNK"
+
+
+def test_attention_counts(lib):
+    """The work of the longest sequences possible stays below 2^31 units."""
+    big = config(pool=4, max_seq=2 ** 24)
+    paged = dict(block_table_dev=P, n_rows=4000)
+    assert attend(lib, c=big, b=batch(n_seq=511, **paged), nbytes=0) == "PF_ERR_WORKSPACE"  # 511 * 8 * (2^19 + 16)
+    assert attend(lib, c=big, b=batch(n_seq=512, **paged), nbytes=0) == "PF_ERR_SHAPE"
+    assert attend(lib, c=big, b=batch(n_seq=256, **{**paged, "max_rows": 65}), nbytes=0) == "PF_ERR_SHAPE"  # two blocks of 256 rows
+    assert attend(lib, c=big, b=batch(n_seq=255, **{**paged, "max_rows": 65}), nbytes=0) == "PF_ERR_WORKSPACE"
 
 
 def test_sizes(lib):

@@ -86,13 +86,19 @@ class Step:
                                 self.status)
         return out
 
+    def weights(self):
+        """Rounding of the softmax weights: to the cache's type; for up to 8 query rows per kv head of a bf16 cache as
+        two terms, where the second, at most half a step of the first, is rounded."""
+        two = self.kind == "bf16" and max(1, *self.rows) * (self.nq // self.nkv) <= 8
+        return R.half_step(self.kind) ** 2 if two else R.half_step(self.kind)
+
     def check_attention(self, q, out):
         got, qq = out.double().cpu().numpy().reshape(self.n_rows, self.nq, self.hd), q.double().cpu().numpy()
         for b, n in enumerate(self.rows):
             if n == 0:
                 continue
             rows = slice(self.begin[b], self.begin[b + 1])
-            ref, bound = R.attention(qq[rows], self.held(self.k, b), self.held(self.v, b), self.start[b], self.parents[b], self.kind)
+            ref, bound = R.attention(qq[rows], self.held(self.k, b), self.held(self.v, b), self.start[b], self.parents[b], self.weights())
             off = np.abs(got[rows] - ref)
             assert (off <= bound).all(), (b, n, self.start[b], float((off / bound).max()), np.argwhere(~(off <= bound))[:3])
         assert (got[self.total:] == 7).all()
@@ -252,6 +258,245 @@ def test_attention_repeats_and_streams(top):
     pf.pf_status_read(s.status)
 
 
+@pytest.mark.parametrize("n_seq", [33, 200, 1024])
+@pytest.mark.parametrize("top", [1, 20])
+def test_attention_many_sequences(n_seq, top):
+    """Hundreds of short tasks, several to a warp, with sequences of no rows between them."""
+    rng = np.random.default_rng(n_seq)
+    rows = [int(x) for x in rng.integers(0, top + 1, n_seq)]
+    rows[0] = top
+    start = [int(x) for x in rng.integers(0, 400, n_seq)]
+    s = Step("bf16", 4, 2, 128, rows, start, True, trees(rng, rows), n_layers=1, layer=0)
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("n_seq", [1, 3, 40])
+@pytest.mark.parametrize("top", [1, 30])
+def test_nothing_to_do(n_seq, top):
+    """No sequence has a row: nothing is written, nothing recorded."""
+    s = Step("f16", 8, 2, 64, [0] * n_seq, [5] * n_seq, True, [np.zeros(0, np.int32)] * n_seq)
+    s.batch = s.make_batch(top)
+    q = s.q()
+    out = torch.full((s.n_rows, s.nq * s.hd), 7.0, dtype=torch.float16, device="cuda")
+    pf.pf_op_attention_tree(s.cfg, s.batch, q, s.k, s.v, 1, out, pf.attention_tree_scratch(s.cfg, n_seq, top), s.status)
+    rope = torch.zeros(s.max_seq, 32, 2, device="cuda")
+    pf.pf_op_batch_append(s.cfg, s.batch, torch.zeros(s.n_rows, 12 * 64, device="cuda"), None, None, rope, 1, q, s.k, s.v, s.status)
+    rows, seqs = (torch.full((m,), 9, dtype=torch.int32, device="cuda") for m in (s.n_rows, n_seq))
+    path, count, after = rows.clone(), seqs.clone(), seqs.clone()
+    pf.pf_op_tree_accept(s.cfg, s.batch, rows, rows, seqs, path, count, after, s.k, s.v, s.status)
+    x, a = torch.ones(s.n_rows, 64, dtype=torch.float16, device="cuda"), torch.ones(1, 8, 64, dtype=torch.float16, device="cuda")
+    y = torch.full((s.n_rows, 64), 7.0, device="cuda")
+    pf.pf_op_adapters(s.batch, x, torch.zeros_like(y), y, torch.zeros_like(seqs), a, a.reshape(1, 64, 8), torch.ones(1, device="cuda"), s.status)
+    pf.pf_status_read(s.status)
+    assert (out == 7).all() and (y == 7).all() and (path == 9).all() and (count == 0).all() and (after == 9).all()
+    assert torch.isnan(s.k).all() and torch.isnan(s.v).all()
+
+
+@pytest.mark.parametrize("nq,nkv,hd", [(64, 1, 64), (16, 1, 128)])
+def test_attention_many_row_blocks(nq, nkv, hd):
+    """The most rows that a kv head can have: 256 nodes of all query heads, in blocks of 256."""
+    rng = np.random.default_rng(3)
+    rows, start = [256, 1, 250], [200, 0, 33]
+    s = Step("bf16", nq, nkv, hd, rows, start, True, trees(rng, rows))
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_attention_drawn(seed):
+    rng = np.random.default_rng(100 + seed)
+    nq, nkv, hd = [(32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (32, 4, 128), (64, 8, 128)][rng.integers(6)]
+    n_seq = int(np.exp(rng.uniform(0, np.log(70))))
+    top = int(np.exp(rng.uniform(0, np.log(65))))
+    rows = [int(x) for x in rng.integers(0 if n_seq > 1 else 1, top + 1, n_seq)]
+    rows[0] = top
+    start = [int(x) for x in rng.integers(0, max(2, int(np.exp(rng.uniform(0, np.log(40000 // n_seq))))), n_seq)]
+    s = Step(["bf16", "f16"][seed % 2], nq, nkv, hd, rows, start, True, trees(rng, rows) if seed % 3 else None, seed=seed)
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("nq,nkv", [(4, 2), (32, 8)])
+def test_hidden_keys(nq, nkv):
+    """NaN and infinities in the K of a node reach the rows that see it and no other."""
+    n = 24 if nq == 32 else 4
+    parent = np.arange(n, dtype=np.int32) // 2 - 1  # a binary tree with two roots
+    s = Step("bf16", nq, nkv, 128, [n], [130], True, [parent])
+    s.fill()
+    q = s.q()
+    want = s.attend(q)
+    see = R.ancestors(parent)
+    for j, bad in ((0, float("nan")), (n - 1, float("inf")), (n // 2, float("-inf"))):
+        keep = s.k.clone()
+        s.k[:, :, int(s.slot(0, 130 + j))] = bad
+        got = s.attend(q)
+        blind = torch.from_numpy(~see[:, j]).cuda()
+        assert torch.equal(got[:n][blind], want[:n][blind]) and not torch.isfinite(got[:n][~blind]).all(1).any()
+        s.k.copy_(keep)
+    pf.pf_status_read(s.status)
+
+
+def test_one_scratch_for_both_forms():
+    """A scratch for the most rows serves calls of one row and of many in turn, and smaller batches."""
+    rng = np.random.default_rng(8)
+    big = Step("bf16", 32, 8, 128, [20, 3, 20, 1], [700, 0, 900, 40], True, trees(rng, [20, 3, 20, 1]))
+    one = Step("bf16", 32, 8, 128, [1, 1, 1], [900, 2, 1500], True, trees(rng, [1, 1, 1]))
+    scratch = pf.attention_tree_scratch(big.cfg, 4, 20)
+    runs = []
+    for s in (big, one):
+        s.fill()
+        runs.append((s, s.q()))
+    first = [s.attend(q, scratch) for s, q in runs]
+    for (s, q), out in zip(runs, first):
+        s.check_attention(q, out)
+    for _ in range(5):
+        for (s, q), out in zip(runs, first):
+            assert torch.equal(s.attend(q, scratch), out)
+            pf.pf_status_read(s.status)
+
+
+@pytest.mark.parametrize("top", [1, 30])
+def test_two_streams_at_once(top):
+    """Calls on two streams, each with a scratch of its own, and adapters beside them."""
+    rng = np.random.default_rng(31)
+    steps = []
+    for seed in (1, 2):
+        rows = [top, 1, top, top]
+        s = Step("bf16", 32, 8, 128, rows, [3000 * seed, 50, 700, 5000], True, trees(rng, rows), seed=seed)
+        s.fill()
+        q = s.q()
+        steps.append((s, q, s.attend(q), s.scratch(), torch.cuda.Stream()))
+    batch = pf.Batch(ints([0, 70, 100]), n_rows=100, max_rows=70)
+    x, base = torch.randn(100, 1024, device="cuda").half(), torch.randn(100, 512, device="cuda")
+    a, b = torch.randn(2, 16, 1024, device="cuda").half() * 0.03, torch.randn(2, 512, 16, device="cuda").half()
+    args = ints([1, 0]), a, b, torch.ones(2, device="cuda")
+    plain = torch.empty_like(base)
+    pf.pf_op_adapters(batch, x, base, plain, *args)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(15):
+        for s, q, want, scratch, stream in steps:
+            with torch.cuda.stream(stream):
+                y = torch.empty_like(base)
+                pf.pf_op_adapters(batch, x, base, y, *args)
+                outs.append((s.attend(q, scratch), want))
+                outs.append((y, plain))
+    torch.cuda.synchronize()
+    for s, *_ in steps:
+        pf.pf_status_read(s.status)
+    for i, (got, want) in enumerate(outs):
+        assert torch.equal(got, want), i
+
+
+def test_cache_past_32_bits():
+    """A cache of more than 2^32 bytes: append, attention and acceptance in its last layer and last blocks."""
+    rng = np.random.default_rng(12)
+    nq, nkv, hd, layers = 32, 8, 128, 9
+    rows, start = [26, 1, 40], [1000, 300, 127]
+    s = Step("bf16", nq, nkv, hd, rows, start, True, trees(rng, rows), n_layers=1, layer=0)
+    high = 1900
+    assert layers * nkv * high * 128 * hd * 2 > 2 ** 32
+    s.table[s.table >= 0] += high - s.pool  # the last blocks of a larger pool
+    s.table_dev.copy_(ints(s.table))
+    shape = dataclasses.replace(synth.QWEN3_8B_LAYER, n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, kv_dtype="bf16", qk_norm=False)
+    s.cfg = pf.make_config(shape, 256, n_layers=layers, max_seq=s.max_seq, kv_block_pool=high)
+    s.layer, s.slots = layers - 1, high * 128
+    s.k, s.v = (torch.full((layers, nkv, s.slots, hd), 3.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    s.fill(own_rows=False)
+    before = s.k.clone()
+    qkv = torch.randn(s.n_rows, (nq + 2 * nkv) * hd, device="cuda")
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, hd, s.max_seq)).cuda()
+    q = torch.empty(s.n_rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+    pf.pf_op_batch_append(s.cfg, s.batch, qkv, None, None, rope, s.layer, q, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    changed = (s.k != before).any(-1)
+    mine = sorted(int(s.slot(b, start[b] + i)) for b in range(3) for i in range(rows[b]))
+    assert not changed[:-1].any() and changed[-1].any(0).nonzero().flatten().tolist() == mine
+    v = qkv[:, (nq + nkv) * hd:].reshape(s.n_rows, nkv, hd)
+    for b in range(3):
+        i = torch.from_numpy(np.asarray(s.slot(b, start[b] + np.arange(rows[b])), np.int64)).cuda()
+        assert torch.equal(s.v[-1][:, i], v[s.begin[b]:s.begin[b + 1]].transpose(0, 1).bfloat16())
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+    tokens = ints(np.arange(s.n_rows))
+    ids = np.full(s.n_rows, -5, np.int32)
+    last = rows[0] - 1  # the way to the last node is accepted
+    way = [i for i in range(rows[0]) if R.ancestors(s.parents[0])[last, i]]
+    for i, j in zip(way, way[1:]):
+        ids[i] = j
+    path, count, after = (torch.full((m,), 9, dtype=torch.int32, device="cuda") for m in (s.n_rows, 3, 3))
+    old = s.k[:, :, torch.from_numpy(np.asarray(s.slot(0, start[0] + np.array(way)), np.int64)).cuda()].clone()
+    pf.pf_op_tree_accept(s.cfg, s.batch, tokens, ints(ids), ints([way[0], -7, -7]), path, count, after, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    assert path[:len(way)].tolist() == way and count.tolist() == [len(way), 0, 0]
+    new = s.k[:, :, torch.from_numpy(np.asarray(s.slot(0, start[0] + np.arange(len(way))), np.int64)).cuda()]
+    assert torch.equal(new, old)
+
+
+def test_captured_append_accept_and_adapters():
+    """The three other calls captured once and replayed with other rows, starts, trees, tokens and adapters."""
+    rng = np.random.default_rng(40)
+    rows, start = [30, 5, 12], [100, 0, 250]
+    s = Step("f16", 8, 2, 64, rows, start, True, trees(rng, rows), n_layers=2)
+    for c in (s.k, s.v):
+        c.copy_(torch.from_numpy(rng.standard_normal(c.shape)).cuda())
+    width = 12 * 64
+    qkv = torch.from_numpy(rng.standard_normal((s.n_rows, width))).cuda().float()
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, 64, s.max_seq)).cuda()
+    tokens, ids, root, which = ints(rng.integers(0, 3, s.n_rows)), ints(rng.integers(0, 3, s.n_rows)), ints(rng.integers(0, 3, 3)), ints([1, -1, 0])
+    x = torch.from_numpy(rng.standard_normal((s.n_rows, 512))).cuda().half()
+    a, b = torch.from_numpy(rng.standard_normal((2, 32, 512)) * 0.04).cuda().half(), torch.from_numpy(rng.standard_normal((2, width, 32))).cuda().half()
+    scale = torch.tensor([1.0, 0.5], device="cuda")
+
+    def step(o):
+        pf.pf_op_adapters(s.batch, x, qkv, o["y"], which, a, b, scale, s.status)
+        pf.pf_op_batch_append(s.cfg, s.batch, o["y"], None, None, rope, 1, o["q"], o["k"], o["v"], s.status)
+        pf.pf_op_tree_accept(s.cfg, s.batch, tokens, ids, root, o["path"], o["count"], o["next"], o["k"], o["v"], s.status)
+
+    def outputs():
+        i32 = dict(dtype=torch.int32, device="cuda")
+        return {"y": torch.full((s.n_rows, width), 7.0, device="cuda"), "q": torch.full((s.n_rows, 8, 64), 7.0, dtype=torch.float16, device="cuda"),
+                "k": s.k.clone(), "v": s.v.clone(), "path": torch.full((s.n_rows,), 9, **i32), "count": torch.full((3,), 9, **i32),
+                "next": torch.full((3,), 9, **i32)}
+
+    step(outputs())
+    o = outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(o)
+    for change in range(4):
+        if change:
+            s.rows = [int(r) for r in rng.integers(0, 31, 3)]
+            s.begin = np.concatenate([[0], np.cumsum(s.rows)])
+            if s.begin[-1] > s.n_rows:
+                s.rows, s.begin = [10, 0, 3], np.array([0, 10, 10, 13])
+            s.begin_dev.copy_(ints(s.begin))
+            s.start_dev.copy_(ints([int(rng.integers(0, p + r - n + 1)) for p, r, n in zip(start, rows, [min(n, r) for n, r in zip(s.rows, rows)])]))
+            s.parent_dev[:int(s.begin[-1])] = ints(np.concatenate(trees(rng, s.rows)))
+            tokens.copy_(ints(rng.integers(0, 2, s.n_rows)))
+            ids.copy_(ints(rng.integers(0, 2, s.n_rows)))
+            which.copy_(ints(rng.integers(-1, 2, 3)))
+        want = outputs()
+        step(want)
+        for name, t in outputs().items():
+            o[name].copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in o:
+            assert torch.equal(o[name].contiguous().view(torch.uint8), want[name].contiguous().view(torch.uint8)), (change, name)
+
+
 # ------------------------------------------------------------------ acceptance
 @pytest.mark.parametrize("kind,hd,paged", [("bf16", 128, True), ("f16", 64, True), ("f16", 128, False)])
 @pytest.mark.parametrize("tree", [True, False])
@@ -336,6 +581,38 @@ def test_adapters(k, n, rank, top):
     pf.pf_op_adapters(batch, x, block, block, ints(which), a, b, scale, status)
     assert torch.equal(block[:total], out[:total]) and torch.equal(block[total:], base[total:])
     assert (wide[:, :8] == 3).all() and (wide[:, n + 8:] == 3).all()
+
+
+@pytest.mark.parametrize("k,n,rank", [(512, 264, 16), (768, 520, 72), (1040, 128, 40)])
+@pytest.mark.parametrize("n_seq,top", [(40, 45), (300, 3), (3, 200), (70, 17)])
+def test_adapters_many_sequences(k, n, rank, n_seq, top):
+    """Tiles of 16 and of 64 rows, with sequences of no rows and without an adapter between the others."""
+    rng = np.random.default_rng(k + n_seq)
+    rows = [int(x) for x in rng.integers(0, top + 1, n_seq)]
+    rows[-1] = top
+    which = rng.integers(-1, 5, n_seq).astype(np.int32)
+    begin = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    total = int(begin[-1])
+    batch = pf.Batch(ints(begin), n_rows=total + 1, max_rows=top)
+    x = torch.from_numpy(rng.standard_normal((total + 1, k))).cuda().half()
+    base = torch.from_numpy(rng.standard_normal((total + 1, n))).cuda().float()
+    a = torch.from_numpy(rng.standard_normal((5, rank, k)) * k ** -0.5).cuda().half()
+    b = torch.from_numpy(rng.standard_normal((5, n, rank)) * 0.1).cuda().half()
+    scale = torch.tensor([0.5, 2.0, 1.25, 16.0, 0.0], device="cuda")
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out = torch.full((total + 1, n), 7.0, device="cuda")
+    pf.pf_op_adapters(batch, x, base, out, ints(which), a, b, scale, status)
+    pf.pf_status_read(status)
+    got = out.double().cpu().numpy()
+    for i, w in enumerate(which):
+        rs = slice(begin[i], begin[i + 1])
+        if w < 0:
+            assert torch.equal(out[rs], base[rs])
+            continue
+        ref, bound = R.adapters(base[rs].cpu().numpy(), x[rs].cpu().numpy(), a[w].cpu().numpy(), b[w].cpu().numpy(), float(scale[w]))
+        off = np.abs(got[rs] - ref)
+        assert (off <= bound).all(), (i, w, float((off - bound).max()))
+    assert (got[total] == 7).all()
 
 
 def test_adapters_range():
@@ -436,6 +713,25 @@ def test_bad_parents_and_pages(top):
         assert not changed[1].any() and {int(x) for x in changed[0].nonzero()[:, 1]} <= mine
 
 
+def test_accept_with_a_bad_page():
+    """Rows whose block is unknown stay where they are; the answer and the other rows are as with it."""
+    s = Step("f16", 4, 2, 64, [4, 3], [126, 20], True, [np.array([-1, -1, 1, 2], np.int32), np.array([-1, -1, 1], np.int32)], n_layers=1, layer=0)
+    for c in (s.k, s.v):
+        c.copy_(torch.randn(c.shape, device="cuda"))
+    tokens, ids = ints([9, 1, 2, 3, 9, 1, 2, 0, 0, 0]), ints([0, 2, 3, 4, 0, 2, 8, 0, 0, 0])
+    before = s.k.clone()
+    s.table_dev[0, 1] = s.pool  # positions 128 .. of the first: nodes 2 and 3
+    path, count, after = (torch.full((m,), 99, dtype=torch.int32, device="cuda") for m in (s.n_rows, 2, 2))
+    pf.pf_op_tree_accept(s.cfg, s.batch, tokens, ids, ints([1, 1]), path, count, after, s.k, s.v, s.status)
+    assert status_of(lambda: pf.pf_status_read(s.status)) == "PF_ERR_KV_CAPACITY"
+    assert path.tolist() == [1, 2, 3, -1, 1, 2, -1, 99, 99, 99] and count.tolist() == [3, 2] and after.tolist() == [4, 8]
+    want = before.clone()
+    want[:, :, int(s.slot(0, 126))] = before[:, :, int(s.slot(0, 127))]  # node 1 to place 0: both known
+    for j in (0, 1):
+        want[:, :, int(s.slot(1, 20 + j))] = before[:, :, int(s.slot(1, 21 + j))]
+    assert torch.equal(s.k, want)
+
+
 def test_bad_adapters():
     batch = pf.Batch(ints([0, 2, 3]), n_rows=3, max_rows=2)
     x, base = torch.randn(3, 64, device="cuda").half(), torch.randn(3, 32, device="cuda")
@@ -511,7 +807,7 @@ def test_layer_of_several_requests():
         k, v = s.held(s.k, b), s.held(s.v, b)
         k[:, start[b]:], v[:, start[b]:] = rk.transpose(1, 0, 2), rv.transpose(1, 0, 2)
         kv[b] = k, v
-        o = R.attention(rq, k, v, start[b], s.parents[b], "f16")[0].reshape(n, nq * hd)
+        o = R.attention(rq, k, v, start[b], s.parents[b], R.half_step("f16"))[0].reshape(n, nq * hd)
         r = xr + o @ dense["o"].T
         ref[s.begin[b]:s.begin[b + 1]] = r + (lora("o", which[b], o) if which[b] >= 0 else 0)
     got = out.double().cpu().numpy()
