@@ -32,7 +32,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int UK = 32;  // keys per unit
-constexpr int LEAD = 3;  // what a task costs beside its keys, in units
+constexpr int LEAD = 4;  // what a task costs beside its keys, in units
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr int FEW_ROWS = 8;  // most rows per kv head of this form: the n side of an MMA
 

@@ -118,6 +118,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 // Bits [0, n) set (n clamped to [0, 32]).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
@@ -268,6 +269,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       int rows = tile_row(0), rows_next = tile_row(32);  // 32 tiles, and the 32 after them
+      // the tree towards L1, for the rows that look for their ancestors there
+      if (B.parent != nullptr && 32 * lane < p.n && (p.u0 + p.cnt) * TK > p.start) prefetch_l1(B.parent + p.at + 32 * lane);
       if (seg == 0) load_q();
       const int lag = p.slots == 2 ? 0 : 1;  // V follows K by so many tiles
       int rv = 0;
@@ -402,10 +405,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool mine = r < p.rows - (p.slots == 2 ? slot * TM : 0);
       float m = -INFINITY, l = 0.f;
       const int step = p.slots == 2 ? 1 : 2, j0 = p.slots == 2 ? 0 : slot;
-      // Keys of a tile that the row does not see get the score -inf: it adds nothing to the maximum and has weight 0. n0 =
-      // node of the tile's first key (negative: cached).
-      auto hide = [&](int n0) {
-        uint32_t vis[4];
+      // Keys of a tile that the row sees: n0 = node of the tile's first key (negative: cached).
+      auto sight = [&](int n0, uint32_t (&vis)[4]) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) vis[w] = low_bits((mine && B.parent == nullptr ? node + 1 : 0) - (n0 + 32 * w));
         if (mine && B.parent != nullptr) {
@@ -420,18 +421,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t see = c == 0 ? vis[0] : (c == 1 ? vis[1] : (c == 2 ? vis[2] : vis[3]));
-          uint32_t u[32];
-          tmem_ld_32x32b_x32(sbuf + 32 * c, u);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((see >> e) & 1u)) u[e] = 0xff800000u;
-          tmem_st_32x32b_x32(sbuf + 32 * c, u);
-        }
-        tmem_st_wait();
       };
       // key r of a tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN. Each slot
       // clears it before its own product.
@@ -444,10 +433,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();
       };
       for (int j = j0; j < p.cnt; j += step) {
+        const int key0 = (p.u0 + j) * TK, nvalid = p.start + p.n - key0;
+        const bool tail = key0 + TK > p.start;  // the tile holds rows of the sequence itself, or what lies behind them
+        uint32_t vis[4];
+        if (tail) sight(key0 - p.start, vis);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full(slot), done & 1, abort_flag)))) break;
         tc_fence_after();
-        const int key0 = (p.u0 + j) * TK, nvalid = p.start + p.n - key0;
-        if (key0 + TK > p.start) hide(key0 - p.start);  // the tile holds rows of the sequence itself, or what lies behind them
         // The tile in halves of 64 keys, in loops: unrolled over a tile the code outgrows the instruction cache that two SMs
         // share. First the row's maximum, then the weights, the second half first; P takes the first 32 columns of its half's scores.
         uint32_t v[HK];
@@ -457,11 +448,29 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait();
         };
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (tail) {
+          // Keys that the row does not see get the score -inf: it adds nothing to the maximum and has weight 0.
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          load(h);
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = c == 0 ? vis[0] : (c == 1 ? vis[1] : (c == 2 ? vis[2] : vis[3]));
+            uint32_t u[32];
+            tmem_ld_32x32b_x32(sbuf + 32 * c, u);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < HK; e += 2) mp[(e >> 1) & 3] = max3(mp[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) u[e] = 0xff800000u;
+            tmem_st_32x32b_x32(sbuf + 32 * c, u);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) mp[(e >> 1) & 3] = max3(mp[(e >> 1) & 3], __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+          }
+          tmem_st_wait();
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            load(h);
+#pragma unroll
+            for (int e = 0; e < HK; e += 2) mp[(e >> 1) & 3] = max3(mp[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          }
         }
         const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
         const bool need = mx > m + RESCALE_LOG2;
