@@ -317,6 +317,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         umma_f16_ts_warp(tmem + 256 + slot * TK, tmem + slot * TK + h * HK + kc * 8, sdesc_mnmajor_sw128(v + kc * 2048, TK * 128), idesc_o,
                          add || kc > 0);
     };
+    // The V of keys behind the sequence (from key nv of the tile on) may be anything, and a zero weight must not meet a NaN:
+    // cleared here, while the softmax forms the weights.
+    auto wait_v = [&](const Part& p, int j, int c) {
+      if (!wait_kv(c)) return false;
+      const int nv = p.start + p.n - (p.u0 + j) * TK;
+      if (nv < TK) {
+        const uint32_t vt = kv_s + (c % NS) * L::KV;
+        for (int i = lane; i < NH * TK * 8; i += 32) {  // eight lanes a row of 64 columns
+          const int key = (i >> 3) % TK;
+          if (key >= nv)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + i * 16), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return true;
+    };
     int c0 = 0, seg = 0;
     int pc[2] = {0, 0};  // P tiles taken of each slot
     bool ok = true;
@@ -336,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int v = c0 + place_v(p, j), k = c0 + place_k(p, j + 1);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (!(ok = ok && wait(p_full(s, 1), pc[s] & 1) && wait_kv(v))) break;
+            if (!(ok = ok && (s == 1 || wait_v(p, j, v)) && wait(p_full(s, 1), pc[s] & 1))) break;
             values(s, 1, v, j > 0);
             if (!(ok = wait(p_full(s, 0), pc[s] & 1))) break;
             values(s, 0, v, true);
@@ -365,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (seg > 0 && !(ok = wait(o_empty(0), (seg - 1) & 1) && wait(o_empty(1), (seg - 1) & 1))) break;
         for (int j = 0; j < p.cnt && ok; ++j) {
           const int s = j & 1, v = c0 + place_v(p, j), k = c0 + place_k(p, j + 2);
-          if (!(ok = wait(p_full(s, 1), pc[s] & 1) && wait_kv(v))) break;
+          if (!(ok = wait_v(p, j, v) && wait(p_full(s, 1), pc[s] & 1))) break;
           values(s, 1, v, j >= 2);
           if (!(ok = wait(p_full(s, 0), pc[s] & 1))) break;
           values(s, 0, v, true);
@@ -422,18 +439,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       };
-      // key r of a tile lies behind the sequence: its V may be anything, and a zero weight must not meet a NaN. Each slot
-      // clears it before its own product.
-      auto clear_v = [&](int j) {
-        const int c = c0 + place_v(p, j);
-        const uint32_t vt = kv_s + (c % NS) * L::KV + r * 128;
-        ok = mbar_wait(kv_full(c % NS), (c / NS) & 1, abort_flag);
-        for (int y = 0; y < NH * 8; ++y)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (y >> 3) * (TK * 128) + (y & 7) * 16), "r"(0) : "memory");
-        fence_proxy_async_smem();
-      };
       for (int j = j0; j < p.cnt; j += step) {
-        const int key0 = (p.u0 + j) * TK, nvalid = p.start + p.n - key0;
+        const int key0 = (p.u0 + j) * TK;
         const bool tail = key0 + TK > p.start;  // the tile holds rows of the sequence itself, or what lies behind them
         uint32_t vis[4];
         if (tail) sight(key0 - p.start, vis);
@@ -508,18 +515,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tmem_st_32x32b_x32(sbuf + HK * h, pk);
           // a half's product starts while the other half's weights are formed
-          if (r >= nvalid && (r >> 6) == h) clear_v(j);
           tmem_st_wait();
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_before();
           mbar_arrive(p_full(slot, h));
         }
         const float2 sum = each(add_two(add_two(ls[0], ls[1]), add_two(ls[2], ls[3])));
         l += sum.x + sum.y;
-        if (!ok) break;
         ++done;
       }
       // ------------------------------------------------------------------ the part's end
+      WorkCursor<decltype(work)> nxt = cur;  // looked up while the last product runs
+      if (x + p.units < count) nxt.advance(B, work, p.units);
       const int tiles = p.slots == 2 ? p.cnt : (p.cnt - slot + 1) / 2;
       if (ok && tiles > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done(slot), (done - 1) & 1, abort_flag));
       if (p.slots == 1 && slot == 1) ml_s[r] = make_float2(m, l);
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_arrive(o_empty(slot));
       c0 += 2 * p.cnt;
       x += p.units;
-      if (x < count) cur.advance(B, work, p.units);
+      cur = nxt;
     }
   }
 
