@@ -3,8 +3,14 @@
 //
 // One kernel: a cluster of 8 CTAs takes RT rows of one sequence. The CTAs split K for h = x A^T (m16n8k16 on tiles of x
 // and A that TMA brings through rings), add their shares through distributed shared memory, and split N for h B^T, whose
-// accumulators go straight onto base: x, base and out pass once, h never leaves the chip. A CTA's 8 warps are KW = 8 MG
+// accumulators go straight onto base: x, base and out pass once, h never leaves the chip. A CTA's 8 warps are KW = 8 / MG
 // groups over K (MG = RT / 16 warps with 16 rows each), every group with a ring of its own.
+//
+// What bounds it: few rows the chain of launch, first copies, the cluster's barrier and the second product (one token, rank 16,
+// 4,096 -> 4,096: 4.1 us; 24 of them with 16 adapters, 4,096 -> 6,144: 5.4 us). Many rows the traffic between L2 and the SMs, since
+// every tile of rows reads its A and B again: four chunks of 300 .. 700 rows, rank 64, 12,288 -> 4,096, move 178 MB in 33.5 us (121
+// MB of them x, base and out), 13 us the first product, 12 the second, 6 the sum between them. The products are 4 GFLOP: warp
+// MMAs do. Tried and not kept: tiles of 128 rows (49 .. 57 us), base by TMA or two tiles ahead in registers (33.5 .. 34.5).
 //
 // Rounding: x A^T is summed in f32 and enters the second product as two f16 terms, hi + lo (22 bits), after a power of
 // two that brings the row's largest to 2^13 .. 2^14, so that neither its overflow nor its underflow counts; all else f32.
@@ -429,6 +435,10 @@ cudaError_t prepare_adapters_kernels() {
 }
 
 cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t stream) {
+  // 16 rows a cluster spread few rows over more SMs and need one barrier less; A and B are then read for every 16 rows, so
+  // they pay while all clusters are resident at once (two CTAs an SM up to rank 64), or where a sequence has no more.
+  // Both sides measured, 16 against 64 rows, rank 64, 4,096 -> 6,144: eight sequences of 64 rows (256 CTAs of 304) 13.9 and 20.3 us,
+  // one of 300 13.7 and 17.2, 24 of 32 (384 CTAs) 24.4 and 20.1, one of 1,200 (600) 37.5 and 28.2; 32 sequences of 16 13.9 and 16.3.
   const int rows = std::min(a.b->max_rows, a.b->n_rows);
   const int tiles = std::min(a.b->n_seq * ((rows + 15) / 16), a.b->n_rows / 16 + a.b->n_seq);  // of 16 rows, at most
   const int resident = (a.rank <= 64 ? 2 : 1) * device_sm_count();

@@ -5,16 +5,24 @@
 // ancestors, itself): s_j = q . k_j / sqrt(hd), p = softmax_j(s), o = sum_j p_j v_j.
 //
 // The cache is read once and nothing else weighs, so the kernel streams it: all (sequence, kv head) tasks in one
-// line of units of 32 keys, cut evenly over the CTAs whatever the lengths are (batch.cuh). The units go round
-// the CTA's 4 warps in turn, each through its own ring of TMA stages that it refills itself, across task borders, so
-// that the copies never wait for a task's end, with its own running maximum m, sum l and O. At a task's end the
-// warps meet in shared memory; a task that lies in one CTA is done, parts of a cut one meet in scratch, where the CTA
-// that completes the task's count merges them.
+// line of units of 32 keys, cut evenly over the CTAs whatever the lengths are (batch.cuh), and a CTA's units in runs over
+// its 4 warps. A warp has its own ring of TMA stages, which it refills itself across task borders, and its own running
+// maximum m, sum l and O: the copies never wait for a task's end, and a warp writes the tasks that lie in its run by itself.
+// Parts of tasks that a border cuts stay in shared memory to the end; there they are added, and of a task with keys in
+// other CTAs the sum goes to scratch, where the CTA that completes the task's count adds all. LEAD: a task costs a warp
+// about 2 us beside its keys.
 //
 // The rows of one kv head (row = node * G + head in the group, at most FEW_ROWS) are the n side of warp-level MMAs
 // m16n8k16: S^T [keys x rows] = K [16 keys x 16 d] Q^T and O^T [d x rows] += V^T [16 d x 16 keys] P^T, K and V as A
-// operands by ldmatrix (V transposed on the way); P^T comes from S^T by a register transpose (movmatrix).
+// operands by ldmatrix (V transposed on the way); P^T comes from S^T by a register transpose (movmatrix). The tensor
+// cores are 12 % busy with it; 128 rows in tensor memory would be 16 times too many.
 // The running maximum is raised only when exceeded by more than 2^8.
+//
+// Measured (GB300, replayed graphs, 32/8 heads of 128, bf16): one token of each of 48 sequences of 300 .. 8,100 positions
+// (827 MB) 131 us, 6.3 TB/s: HBM. 48 of 100 .. 900 positions 21 us, 200 of 1 .. 300 33 us: the 2 us a task. One
+// token at 513 / 8,190 / 32,001 positions 8.0 / 10.4 / 27.5 us: launch, first copies, the merge of 5 / 19 / 19 parts.
+// The units in turns over the warps, which met at every task's end: 131, 26, 49, 7.6 us. LEAD 0: 135, 27, 56 us; 2 to 6
+// within 5 % of one another.
 //
 // Rounding: P to f16, or for a bf16 cache to two bf16 terms (the product with V takes operands of one type; one term would be
 // the largest error of the f16 output, 1.2e-3 against 2e-4 in relative L2, and the second costs nothing beside the copies),
@@ -31,10 +39,14 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-constexpr int UK = 32;  // keys per unit
-constexpr int LEAD = 4;  // what a task costs beside its keys, in units
+constexpr int UK = 32;   // keys per unit
+constexpr int LEAD = 4;  // what a task costs beside its keys, in units (task_lead)
 constexpr float RESCALE_LOG2 = 8.f;
-constexpr int FEW_ROWS = 8;  // most rows per kv head of this form: the n side of an MMA
+// Most rows per kv head of this form: the n side of an MMA. Both sides measured with 8 rows of 32/8 heads of 128, this form
+// against attention_tree_tc.cu: one sequence at 512 / 8,190 positions 9.4 against 10.4 and 12.3 against 13.8 us, 48
+// sequences of 100 .. 900 24.7 against 30.4, of 300 .. 8,100 133 against 132. With 16 rows (two such sides) one
+// sequence took 32.9 us here and 14.6 there, 16 sequences 91 and 63.
+constexpr int FEW_ROWS = 8;
 
 template <int HD>
 struct FSmem {

@@ -1,6 +1,9 @@
 """Calls over many sequences on the GPU: append, tree attention, acceptance and adapters against their definitions
 in float64, numbers in device memory that are out of range, a whole layer of several requests."""
 import dataclasses
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -495,6 +498,41 @@ def test_captured_append_accept_and_adapters():
         torch.cuda.synchronize()
         for name in o:
             assert torch.equal(o[name].contiguous().view(torch.uint8), want[name].contiguous().view(torch.uint8)), (change, name)
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls of all are captured into a graph."""
+    code = """
+import numpy as np, torch, dataclasses
+from quantized_transformer_prefill_q1_gb300 import pf, synth
+shape = dataclasses.replace(synth.QWEN3_8B_LAYER, n_q_heads=8, n_kv_heads=2, head_dim=64, kv_dtype="f16")
+cfg = pf.make_config(shape, 256, n_layers=1, max_seq=500, kv_block_pool=8)
+i = lambda x: torch.tensor(np.asarray(x, np.int32), device="cuda")
+torch.manual_seed(0)
+b = pf.Batch(i([0, 9, 12]), n_rows=12, max_rows=9, start=i([300, 40]), blocks=i([[0, 1, 2, -1], [5, -1, -1, -1]]))
+one = pf.Batch(i([0, 1, 2]), n_rows=12, max_rows=1, start=i([300, 40]), blocks=i([[0, 1, 2, -1], [5, -1, -1, -1]]))
+k, v = (torch.randn(1, 2, 1024, 64, device="cuda").half() for _ in "kv")
+q, x = torch.randn(12, 8, 64, device="cuda").half(), torch.randn(12, 256, device="cuda").half()
+out, few = (torch.zeros(12, 512, dtype=torch.float16, device="cuda") for _ in "ab")
+a, w, y = torch.randn(1, 16, 256, device="cuda").half(), torch.randn(1, 64, 16, device="cuda").half(), torch.zeros(12, 64, device="cuda")
+scratch, base, which, scale = pf.attention_tree_scratch(cfg, 2, 9), torch.zeros(12, 64, device="cuda"), i([0, -1]), torch.ones(1, device="cuda")
+def step():
+    pf.pf_op_attention_tree(cfg, b, q, k, v, 0, out, scratch)
+    pf.pf_op_attention_tree(cfg, one, q, k, v, 0, few, scratch)
+    pf.pf_op_adapters(b, x, base, y, which, a, w, scale)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (out, few, y)]
+for t in (out, few, y): t.zero_()
+step()
+assert all(torch.equal(s, t) and t.any() for s, t in zip(got, (out, few, y)))
+print("alike")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "alike" in r.stdout, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ acceptance
