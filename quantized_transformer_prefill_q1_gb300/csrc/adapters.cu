@@ -7,10 +7,10 @@
 // groups over K (MG = RT / 16 warps with 16 rows each), every group with a ring of its own.
 //
 // What bounds it: few rows the chain of launch, first copies, the cluster's barrier and the second product (one token, rank 16,
-// 4,096 -> 4,096: 4.1 us; 24 of them with 16 adapters, 4,096 -> 6,144: 5.4 us). Many rows the traffic between L2 and the SMs, since
-// every tile of rows reads its A and B again: four chunks of 300 .. 700 rows, rank 64, 12,288 -> 4,096, move 178 MB in 33.5 us (121
-// MB of them x, base and out), 13 us the first product, 12 the second, 6 the sum between them. The products are 4 GFLOP: warp
-// MMAs do. Tried and not kept: tiles of 128 rows (49 .. 57 us), base by TMA or two tiles ahead in registers (33.5 .. 34.5).
+// 4,096 -> 4,096: 4.1 us; 24 of them with 16 adapters, 4,096 -> 6,144: 5.4 us). Many rows the copies, since every tile of rows
+// reads its A and B again, and a CTA's phases follow one another: four chunks of 300 .. 700 rows, rank 64, 12,288 -> 4,096, take
+// 33.5 us, 13 the first product (x and A, 100 MB), 6 the sum over the cluster, 12 the second (B, base and out, 81 MB). The
+// products are 4 GFLOP: warp MMAs do. Tried and not kept: tiles of 128 rows (49 .. 57 us), base by TMA or two tiles ahead in registers (33.5 .. 34.5).
 //
 // Rounding: x A^T is summed in f32 and enters the second product as two f16 terms, hi + lo (22 bits), after a power of
 // two that brings the row's largest to 2^13 .. 2^14, so that neither its overflow nor its underflow counts; all else f32.

@@ -21,7 +21,8 @@
 // them, a thread per row and eight columns.
 //
 // Measured (GB300, replayed graphs, bf16, 32/8 heads of 128): trees of 40 .. 64 nodes of eight sequences of 20,000 ..
-// 32,700 positions (870 MB) 161 us, 0.81 of the copy rate and 0.55 of the tensor cores' time. What bounds it is the softmax:
+// 32,700 positions (870 MB) 161 us, 0.81 of the copy rate with the tensor cores 61 % busy; under a load of seconds 186 us, the
+// power cap's clocks. What bounds it is the softmax:
 // a tile of 256 x 128 scores takes 1.8 us with its exponentials and the hand-over, the products alone 1.1 us. Short tasks
 // cost about 5 us each beside their tiles, mostly waits of one role for the other (LEAD; with 0, 24 rows of each of 48
 // sequences of 100 .. 900 positions took 61 us, with 1 / 2 / 4 45 / 42 / 40 us): 37 us.
