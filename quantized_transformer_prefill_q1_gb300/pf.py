@@ -537,30 +537,32 @@ def pf_op_tree_accept(cfg, batch, tokens, ids, root_ids, path, n_accepted, next_
                                   _dense(status, dev, "int32", "status", 1, True), _on(dev, stream)))
 
 
-def _strided(t, dev: int, dtype: str, what: str, rows: int):
+def _strided(t, dev: int, dtype: str, what: str, rows: int, width: int):
     """(address, elements between rows) of rows [>= rows, width] with contiguous elements."""
-    if t is None or t.dim() != 2 or t.shape[0] < rows:
-        raise PfError(1, f"{what}: need {dtype} [{rows}, width], got {None if t is None else tuple(t.shape)}")
-    st = t.stride()
-    if t.get_device() != dev or t.dtype is not getattr(_torch, dtype) or (st[1] != 1 and t.shape[1] != 1):
+    if t is None or t.dim() != 2:
+        raise PfError(1, f"{what}: need {dtype} [{rows}, {width}], got {None if t is None else tuple(t.shape)}")
+    (n, w), (apart, step) = t.shape, t.stride()
+    if n < rows or w != width:
+        raise PfError(1, f"{what}: need {dtype} [{rows}, {width}], got {tuple(t.shape)}")
+    if t.get_device() != dev or t.dtype is not getattr(_torch, dtype) or (step != 1 and w != 1):
         raise PfError(1, f"{what}: need {dtype} rows with contiguous elements on the current CUDA device, got {t.dtype} "
-                         f"of strides {st} on {t.device}")
-    return t.data_ptr(), st[0] if rows > 1 else -(-t.shape[1] // 8) * 8
+                         f"of strides {t.stride()} on {t.device}")
+    return t.data_ptr(), apart if rows > 1 else -(-w // 8) * 8
 
 
 def pf_op_adapters(batch, x, base, out, adapter, a, b, scale, status=None, stream=None):
     """out[m] = base[m] + scale[i] (x[m] A_i^T) B_i^T with i = adapter[sequence of m], -1: none. x f16 [n_rows, K], base and
     out f32 [n_rows, N] (views of wider rows; out may be base), a f16 [adapters, rank, K], b f16 [adapters, N, rank],
     scale f32 [adapters], adapter int32 [n_seq]."""
-    dev = _here()
-    if a is None or b is None or a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+    dev, rows = _here(), batch.n_rows
+    if a is None or b is None or a.dim() != 3 or b.dim() != 3:
         raise PfError(1, "A: need f16 [adapters, rank, K], B: f16 [adapters, N, rank]")
-    (count, rank, k), n = a.shape, b.shape[1]
-    xp, ldx = _strided(x, dev, "float16", "x", batch.n_rows)
-    bp, ldb = _strided(base, dev, "float32", "base", batch.n_rows)
-    op, ldo = _strided(out, dev, "float32", "out", batch.n_rows)
-    if x.shape[1] != k or base.shape[1] != n or out.shape[1] != n:
-        raise PfError(1, f"widths: x {x.shape[1]} and A {k}, base {base.shape[1]}, out {out.shape[1]} and B {n}")
+    (count, rank, k), (others, n, r) = a.shape, b.shape
+    if others != count or r != rank:
+        raise PfError(1, f"A {(count, rank, k)} and B {(others, n, r)}: need [adapters, rank, K] and [adapters, N, rank]")
+    xp, ldx = _strided(x, dev, "float16", "x", rows, k)
+    bp, ldb = _strided(base, dev, "float32", "base", rows, n)
+    op, ldo = (bp, ldb) if out is base else _strided(out, dev, "float32", "out", rows, n)
     check(lib().pf_op_adapters(_batch(batch, dev), xp, ldx, bp, ldb, op, ldo, k, n, rank, count,
                                _dense(adapter, dev, "int32", "adapter", batch.n_seq), _dense(a, dev, "float16", "A", count * rank * k),
                                _dense(b, dev, "float16", "B", count * n * rank), _dense(scale, dev, "float32", "scale", count),
