@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t sbuf = tmem + lane_off + slot * TK, obuf = tmem + lane_off + 256 + slot * TK;
     const float sl2 = P.scale_log2;
-    int c0 = 0, done = 0;  // tiles of the parts before; tiles of this slot
+    int done = 0;  // tiles of this slot
     bool ok = true;
     // tcgen05.ld / st are warp-collective: every branch around them is warp-uniform
     for (int x = 0; x < count; ) {
@@ -609,7 +609,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(o_empty(slot));
-      c0 += 2 * p.cnt;
       x += p.units;
       cur = nxt;
     }

@@ -770,6 +770,41 @@ def test_accept_with_a_bad_page():
     assert torch.equal(s.k, want)
 
 
+def test_binding_refusals():
+    """Tensors of another type, place, width or layout, and scratches too small, are refused before a launch."""
+    s = Step("f16", 4, 2, 64, [3, 1], [5, 200], True)
+    s.fill()
+    q, out, scratch = s.q(), torch.zeros(s.n_rows, 256, dtype=torch.float16, device="cuda"), s.scratch()
+
+    def attend(q=q, k=s.k, v=s.v, out=out, scratch=scratch, batch=s.batch):
+        pf.pf_op_attention_tree(s.cfg, batch, q, k, v, 1, out, scratch, s.status)
+
+    attend()
+    narrow = pf.Batch(s.begin_dev, n_rows=s.n_rows, max_rows=3, start=s.start_dev, blocks=s.table_dev[:, :1].contiguous())
+    bare = pf.Batch(s.begin_dev, n_rows=s.n_rows, max_rows=3, start=s.start_dev)
+    for kw in (dict(q=q.bfloat16()), dict(q=q[:2]), dict(q=q.cpu()), dict(q=None), dict(k=s.k.float()), dict(v=s.v[:1]), dict(out=out.float()),
+               dict(out=out[:, ::2]), dict(out=q), dict(scratch=scratch.cpu()), dict(batch=narrow), dict(batch=bare)):
+        assert status_of(lambda: attend(**kw)) == "PF_ERR_INVALID_ARG", kw.keys()
+    assert status_of(lambda: attend(scratch=scratch[:64])) == "PF_ERR_WORKSPACE"
+    for blocks in (s.table_dev.long(), s.table_dev[0], s.table_dev[:1], s.table_dev.cpu()):
+        assert status_of(lambda: pf.Batch(s.begin_dev, n_rows=s.n_rows, max_rows=3, start=s.start_dev, blocks=blocks)) == "PF_ERR_INVALID_ARG"
+    x, y = torch.zeros(s.n_rows, 64, dtype=torch.float16, device="cuda"), torch.zeros(s.n_rows, 32, device="cuda")
+    a, b = torch.zeros(2, 8, 64, dtype=torch.float16, device="cuda"), torch.zeros(2, 32, 8, dtype=torch.float16, device="cuda")
+
+    def adapters(x=x, base=y, out=torch.zeros_like(y), adapter=ints([0, 1]), a=a, b=b, scale=torch.ones(2, device="cuda")):
+        pf.pf_op_adapters(s.batch, x, base, out, adapter, a, b, scale, s.status)
+
+    adapters()
+    for kw in (dict(x=x.float()), dict(x=x[:, :48]), dict(x=x[:2]), dict(x=x.t().contiguous().t()), dict(x=x.cpu()), dict(base=y.half()), dict(base=None),
+               dict(out=y[:, :16]), dict(out=y[0]), dict(adapter=ints([0])), dict(adapter=ints([0, 1]).long()), dict(a=a[0]), dict(a=a[:1]), dict(a=a.float()),
+               dict(b=b[:, :, :4]), dict(b=b.transpose(1, 2)), dict(scale=torch.ones(1, device="cuda")), dict(scale=None)):
+        assert status_of(lambda: adapters(**kw)) == "PF_ERR_INVALID_ARG", kw.keys()
+    assert status_of(lambda: adapters(base=y[:1].expand(s.n_rows, 32))) == "PF_ERR_SHAPE"  # one row for all: rows 0 apart
+    wide = torch.zeros(s.n_rows, 48, device="cuda")
+    assert status_of(lambda: adapters(base=wide[:, :32], out=wide.reshape(-1)[:s.n_rows * 32].reshape(s.n_rows, 32))) == "PF_ERR_SHAPE"
+    pf.pf_status_read(s.status)
+
+
 def test_bad_adapters():
     batch = pf.Batch(ints([0, 2, 3]), n_rows=3, max_rows=2)
     x, base = torch.randn(3, 64, device="cuda").half(), torch.randn(3, 32, device="cuda")
