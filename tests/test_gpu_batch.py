@@ -151,6 +151,38 @@ def test_append(kind, nq, nkv, hd, norm, paged, tree):
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
+def test_longest_chunks():
+    """8,192 rows of one sequence beside others, appended and through adapters."""
+    rng = np.random.default_rng(6)
+    rows, start = [3, 8192, 0, 100], [1, 77, 5, 0]
+    s = Step("bf16", 2, 1, 64, rows, start, True, n_layers=1, layer=0)
+    qkv = torch.from_numpy(rng.standard_normal((s.n_rows, 4 * 64))).cuda().float()
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, 64, s.max_seq)).cuda()
+    q = torch.full((s.n_rows, 2, 64), 7.0, dtype=s.dt, device="cuda")
+    pf.pf_op_batch_append(s.cfg, s.batch, qkv, None, None, rope, 0, q, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    assert (q[s.total:] == 7).all()
+    for b, n in enumerate(rows):
+        pos = start[b] + np.arange(n)
+        at = slice(s.begin[b], s.begin[b + 1])
+        rq, rk, rv, size = R.append(qkv[at].cpu().numpy(), 2, 1, 64, None, None, s.cfg.eps, s.cfg.rope_theta, pos)
+        i = torch.from_numpy(np.asarray(s.slot(b, pos), np.int64)).cuda()
+        for got, ref, sz in ((q[at], rq, size[:, :2]), (s.k[0][:, i].transpose(0, 1), rk, size[:, 2:])):
+            # half a step, and the rotation in f32 as in test_append
+            off = np.abs(got.double().cpu().numpy() - ref)
+            assert (off <= 2.0 ** -8 * (np.abs(ref) + 2.0 ** -20 * sz) + 2.0 ** -20 * sz).all()
+        assert torch.equal(s.v[0][:, i], qkv[at, 3 * 64:].reshape(n, 1, 64).transpose(0, 1).to(s.dt))
+    x = torch.from_numpy(rng.standard_normal((s.n_rows, 128))).cuda().half()
+    a = torch.from_numpy(rng.standard_normal((1, 16, 128)) * 0.1).cuda().half()
+    w = torch.from_numpy(rng.standard_normal((1, 256, 16)) * 0.1).cuda().half()
+    y = qkv.clone()
+    pf.pf_op_adapters(s.batch, x, y, y, ints([0, 0, 0, -1]), a, w, torch.ones(1, device="cuda"), s.status)
+    pf.pf_status_read(s.status)
+    last = int(s.begin[2])
+    ref, bound = R.adapters(qkv[:last].cpu().numpy(), x[:last].cpu().numpy(), a[0].cpu().numpy(), w[0].cpu().numpy(), 1.0)
+    assert (np.abs(y[:last].double().cpu().numpy() - ref) <= bound).all() and torch.equal(y[last:], qkv[last:])
+
+
 # ------------------------------------------------------------------ attention
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("nq,nkv,hd", [(32, 8, 128), (4, 2, 64), (8, 8, 64), (16, 1, 128), (64, 1, 64)])
@@ -305,6 +337,20 @@ def test_attention_many_row_blocks(nq, nkv, hd):
     rng = np.random.default_rng(3)
     rows, start = [256, 1, 250], [200, 0, 33]
     s = Step("bf16", nq, nkv, hd, rows, start, True, trees(rng, rows))
+    s.fill()
+    q = s.q()
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+
+
+@pytest.mark.parametrize("n_seq", [1, 2])
+@pytest.mark.parametrize("top", [1, 20, 200])
+def test_attention_many_heads(n_seq, top):
+    """More tasks of a sequence than SMs."""
+    rng = np.random.default_rng(top)
+    rows, start = [top, 3][:n_seq], [150, 700][:n_seq]
+    s = Step("f16", 200, 200, 64, rows, start, True, trees(rng, rows), n_layers=1, layer=0)
     s.fill()
     q = s.q()
     out = s.attend(q)
