@@ -542,7 +542,8 @@ pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q_f16_dev, c
 typedef struct {
   int32_t n_seq;                  /* 1 .. PF_MAX_SEQS */
   int32_t n_rows;                 /* rows that the row arrays hold */
-  int32_t max_rows;               /* most rows of one sequence */
+  int32_t max_rows;               /* most rows of one sequence: 1 .. 8192, with parents, in the attention and in the
+                                   * acceptance 1 .. PF_MAX_TREE */
   const int32_t* row_begin_dev;   /* [n_seq + 1] */
   const int32_t* start_dev;       /* [n_seq]; not used by pf_op_adapters */
   const int32_t* parent_dev;      /* [n_rows] or NULL */
