@@ -626,7 +626,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
 // CTA = MR rows of a (sequence, kv head); a thread takes a row, eight columns and every GROUPS-th part, PF of them in
-// flight. Parts that saw no key of a row hold no O.
+// flight. Parts that saw no key of a row (m = -inf, l = 0) hold no O; l is NaN where all scores that the row saw were, since the
+// maximum ignores a NaN.
 template <int HD, int MR, int GROUPS, int PF, int CTAS>
 __global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(const BatchDev B, int nq, int nkv, const Line* line_p,
                                                                                const int* prefix, const float* part, int part_rows,
@@ -651,9 +652,9 @@ __global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(c
   const int pr = min(row, rows - 1) - rb * BLOCK, place0 = line.place(c0, first);
   float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   auto add = [&](float m, float l, const float* w) {
-    if (m == -INFINITY) return;
+    if (m == -INFINITY && l == 0.f) return;
     const float mn = fmaxf(mr, m);
-    const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = ex2(m - mn);
+    const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = m == -INFINITY ? 0.f : ex2(m - mn);
     mr = mn;
     lr = lr * a + f * l;
 #pragma unroll
