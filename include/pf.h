@@ -560,8 +560,9 @@ pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const 
 /* Attention of every sequence's rows over its cached positions and its own rows, as far as each sees them: q
  * [n_rows][nq][hd] of the cache's type, out f16 [n_rows][nq hd]. At most PF_MAX_TREE rows a sequence, trees or
  * chains; n_seq * nkv * ceil(max_rows G / 256) * (ceil(max_seq / 32) + 16) below 2^31 (G = nq / nkv). Positions from
- * start + rows on are not used, whatever their slots hold; a key that a row does not see has weight 0 in it, and an infinity
- * or a NaN in the V of a drafted node makes every row of its sequence NaN (0 times it), seen or not. out overlaps no input.
+ * start + rows on are not used, whatever their slots hold; a key that a row does not see has weight 0 in it, whatever its K
+ * holds, but an infinity or a NaN in the V of a cached position or a drafted node makes its column NaN in every row of its
+ * sequence that gives it the weight 0, seen or not (0 times it), and infinite or NaN in the others. out overlaps no input.
  * scratch_dev: 16-B aligned, at least pf_attention_tree_scratch_bytes(cfg, n_seq, max_rows) bytes (which does not fall
  * as either grows: a larger batch's scratch serves every smaller one of the same heads), zero before its first call with a
  * number of kv heads; each call that completes leaves it ready for the next (after PF_ERR_DEVICE_TIMEOUT zero it

@@ -599,9 +599,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait();
           float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {  // a slot that saw nothing may hold anything
-            const float u = f.x == 0.f ? 0.f : f.x * __uint_as_float(o[0][e]);
-            v[e] = f.y == 0.f ? u : fmaf(f.y, __uint_as_float(o[1][e]), u);
+          for (int e = 0; e < 32; ++e) {  // without a tile slot 1 holds anything; a factor of 0 keeps a NaN of V
+            const float u = f.x * __uint_as_float(o[0][e]);
+            v[e] = p.cnt > 1 ? fmaf(f.y, __uint_as_float(o[1][e]), u) : u;
           }
           put(c, v, 1.f);
         }
@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
 // CTA = MR rows of a (sequence, kv head); a thread takes a row, eight columns and every GROUPS-th part, PF of them in
-// flight. Parts that saw no key of a row (m = -inf, l = 0) hold no O; l is NaN where all scores that the row saw were, since the
-// maximum ignores a NaN.
+// flight. A part in which a row saw no key (m = -inf) has the factor 0 and is added like the others: l is NaN where all scores
+// that the row saw were (the maximum ignores a NaN), and O where V of a hidden key was; both reach the row wherever the line is cut.
 template <int HD, int MR, int GROUPS, int PF, int CTAS>
 __global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(const BatchDev B, int nq, int nkv, const Line* line_p,
                                                                                const int* prefix, const float* part, int part_rows,
@@ -652,7 +652,6 @@ __global__ void __launch_bounds__(MR* HD / 8 * GROUPS, CTAS) tree_merge_kernel(c
   const int pr = min(row, rows - 1) - rb * BLOCK, place0 = line.place(c0, first);
   float mr = -INFINITY, lr = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   auto add = [&](float m, float l, const float* w) {
-    if (m == -INFINITY && l == 0.f) return;
     const float mn = fmaxf(mr, m);
     const float a = mr == -INFINITY ? 0.f : ex2(mr - mn), f = m == -INFINITY ? 0.f : ex2(m - mn);
     mr = mn;

@@ -31,3 +31,52 @@ def test_nan_pages(kind, nq, nkv, hd, rows):
         s.k.copy_(keep)
     assert torch.equal(s.attend(q, scratch), want)
     pf.pf_status_read(s.status)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nkv,hd,n", [(8, 2, 128, 2), (8, 2, 128, 26), (8, 8, 64, 26), (16, 1, 128, 26)])
+def test_nan_value_of_a_small_weight(kind, nq, nkv, hd, n):
+    """A NaN in the V of a cached position reaches every row, also where its weight is e^-200 of the largest."""
+    s = Step(kind, nq, nkv, hd, [n, 1], [130, 0], True, [R.chain(n), R.chain(1)], n_layers=1, layer=0)
+    s.fill()
+    first = torch.from_numpy(np.asarray(s.slot(0, np.arange(128)), np.int64)).cuda()
+    s.k[0, :, :, 0] = 0
+    s.k[0][:, first, 0] = 20.0
+    q = s.q()
+    q[:, :, 0] = 20.0 * hd ** 0.5
+    want = s.attend(q)
+    s.check_attention(q, want)
+    s.v[0, :, int(s.slot(0, 128)), 5] = float("nan")
+    got = s.attend(q).reshape(-1, nq, hd)
+    assert torch.isnan(got[:n, :, 5]).all()
+    got[:n, :, 5] = want.reshape(-1, nq, hd)[:n, :, 5]
+    assert torch.equal(got.reshape(want.shape), want)
+    pf.pf_status_read(s.status)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nkv,hd,n", [(8, 8, 64, 8), (32, 8, 128, 2), (8, 8, 64, 200), (32, 8, 128, 26), (4, 1, 128, 256)])
+@pytest.mark.parametrize("others", [0, 3, 40])
+def test_hidden_values(kind, nq, nkv, hd, n, others):
+    """A NaN or an infinity in the V of a node: its column is NaN in every row of the sequence that does not see it, NaN or
+    infinite in those that do, alone and beside other sequences; all else is as without it."""
+    parent = np.full(n, -1, np.int32)
+    parent[n // 2:] = n // 2 - 1  # half of them hang on one node
+    see = R.ancestors(parent)
+    rows, start = [n] + [1 + b % min(n, 3) for b in range(others)], [100] + [37 * b % 600 for b in range(others)]
+    s = Step(kind, nq, nkv, hd, rows, start, True, [parent] + [R.chain(m) for m in rows[1:]], n_layers=1, layer=0)
+    s.fill()
+    q, scratch = s.q(), s.scratch()
+    want = s.attend(q, scratch)
+    s.check_attention(q, want)
+    for j in (0, n // 2 - 1, n - 1):
+        for bad in (float("nan"), float("inf"), float("-inf")):
+            keep = s.v.clone()
+            s.v[0, :, int(s.slot(0, 100 + j)), 3] = bad
+            got = s.attend(q, scratch).reshape(-1, nq, hd)
+            blind = torch.from_numpy(~see[:, j]).cuda()
+            assert torch.isnan(got[:n][blind][:, :, 3]).all() and not torch.isfinite(got[:n, :, 3]).any(), (j, bad)
+            got[:n, :, 3] = want.reshape(-1, nq, hd)[:n, :, 3]
+            assert torch.equal(got.reshape(want.shape), want)
+            s.v.copy_(keep)
+    pf.pf_status_read(s.status)
