@@ -27,10 +27,10 @@
 // cost about 5 us each beside their tiles, mostly waits of one role for the other (LEAD; with 0, 24 rows of each of 48
 // sequences of 100 .. 900 positions took 61 us, with 1 / 2 / 4 45 / 42 / 40 us): 37 us.
 //
-// Rounding: P to the cache's type (the product's operand; of a bf16 cache that is the largest error of the f16 output, 1.2e-3
-// in relative L2, as in the attention over one sequence: two bf16 terms, 2e-4, take 216 us instead of 162 on the case above and
-// 15 to 20 % more on short tasks, since both the softmax and the products with V grow by a half), the output to f16; all
-// else f32.
+// Rounding: P to the cache's type (the product's operand; of an f16 cache after a power of two, see P_UP; of a bf16 cache that
+// is the largest error of the f16 output, 1.2e-3 in relative L2, as in the attention over one sequence: two bf16 terms, 2e-4,
+// take 216 us instead of 162 on the case above and 15 to 20 % more on short tasks, since both the softmax and the products with
+// V grow by a half), the output to f16; all else f32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,6 +50,10 @@ constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;
 constexpr float RESCALE_LOG2 = 8.f;
 static_assert(TK == PF_KV_BLOCK, "a key tile is a page");
+// Weights of an f16 cache are formed 2^7 larger, sums and O with them: up to 2^15 where the running maximum is exceeded by 2^8, and
+// a step of 2^-31 at the small end instead of 2^-24, below which a long cache's many small weights would vanish together.
+template <int BF16>
+constexpr float P_UP = BF16 ? 0.f : 7.f;
 
 template <int HD>
 struct TSmem {
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (need) m = mx;
         }
-        const float neg_m = m == -INFINITY ? 0.f : -m;
+        const float neg_m = m == -INFINITY ? 0.f : P_UP<BF16> - m;
         const uint64_t neg_two = two(neg_m, neg_m), sl2_two = two(sl2, sl2);
         uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll 1

@@ -80,3 +80,42 @@ def test_hidden_values(kind, nq, nkv, hd, n, others):
             assert torch.equal(got.reshape(want.shape), want)
             s.v.copy_(keep)
     pf.pf_status_read(s.status)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("nq,nkv,hd,n", [(8, 8, 64, 1), (8, 2, 128, 2), (8, 8, 64, 26), (8, 2, 128, 40), (16, 1, 128, 30)])
+@pytest.mark.parametrize("power", [12.3, 15.7, 20.4, 22.6, 24.3, 25.2, 26.4, 28.0])
+def test_small_weights(kind, nq, nkv, hd, n, power):
+    """Keys of weight 2^-power with values of one sign beside one key of weight 1 and value 0 in every 32: the small ones are all
+    there is. A weight that an f16 holds is off by half a step or, below 2^-21 of the row's running maximum, by 2^-32 of it:
+    the numbers are formed 2^7 larger, and the smallest step of an f16 is 2^-24."""
+    rng = np.random.default_rng(n)
+    s = Step(kind, nq, nkv, hd, [n, 1], [2000, 700], True, [R.random_tree(rng, n), R.chain(1)], n_layers=1, layer=0)
+    s.fill()
+    s.k.copy_(torch.nan_to_num(s.k) * 0)
+    s.v.copy_(torch.from_numpy(rng.uniform(500, 1000, s.v.shape)).cuda())
+    for b in range(2):
+        p = np.arange(s.start[b] + s.rows[b])
+        i = torch.from_numpy(np.asarray(s.slot(b, p), np.int64)).cuda()
+        large = torch.from_numpy(p % 32 == 0).cuda()
+        s.k[0][:, i, 0] = torch.where(large, 0.0, -power * float(np.log(2))).to(s.dt)
+        s.v[0][:, i] = torch.where(large[:, None], torch.zeros((), dtype=s.dt, device="cuda"), s.v[0][:, i])
+    q = torch.zeros(s.n_rows, nq, hd, dtype=s.dt, device="cuda")
+    q[:, :, 0] = hd ** 0.5  # 8, or the type's nearest to 11.3
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    got, qq = out.double().cpu().numpy().reshape(-1, nq, hd), q.double().cpu().numpy()
+    for b, m in enumerate(s.rows):
+        at = slice(s.begin[b], s.begin[b + 1])
+        k, v = s.held(s.k, b), s.held(s.v, b)
+        ref, bound = R.attention(qq[at], k, v, s.start[b], s.parents[b], s.weights())
+        if kind == "f16":  # a step of 2^-31 of the running maximum, which is at most the true one
+            score = np.einsum("nh,hk->nhk", qq[at][:, :, 0], np.repeat(k[:, :, 0], nq // nkv, 0)) / np.sqrt(hd)
+            see = np.ones((m, score.shape[2]), bool)
+            see[:, s.start[b]:] = R.ancestors(s.parents[b])
+            score = np.where(see[:, None], score, -np.inf)
+            weight = np.exp(score - score.max(2, keepdims=True)).sum(2)
+            values = np.einsum("nk,hkd->nhd", see, np.repeat(np.abs(v), nq // nkv, 0))
+            bound = bound + 2.0 ** -32 * values / weight[:, :, None]
+        off = np.abs(got[at] - ref)
+        assert (off <= bound).all(), (b, float((off / bound).max()), float(got[at].max()), float(ref.max()))
