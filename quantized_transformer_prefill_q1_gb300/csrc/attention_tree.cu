@@ -70,7 +70,7 @@ struct WarpPart {
   int rows;   // 0: none
   int first;  // the task's first unit in the line
   int c0, c1; // CTAs that hold its first and its last key units
-  int at, kvh, b;
+  int at, kvh;
 };
 
 struct FewParams {
@@ -79,7 +79,7 @@ struct FewParams {
   int nq, nkv, layer;
   float scale_log2;
   __half* out;
-  int* counters;  // one per (sequence, kv head)
+  int* counters;  // one per CTA: arrivals of the cut task whose first key units it holds (its last task, so there is one)
   float* part;    // two places a CTA: [rows][HD], then (m, l) per row
   int* status;
 };
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool whole = u0 <= 0 && u0 + cnt == cur.w.units - lead;
     const int place = 2 * warp + (whole || first > ub + wb ? 1 : 0);
     if (!whole) {
-      const WarpPart T{R, first, line.owner(first + lead), line.owner(first + cur.w.units - 1), at, kvh, cur.b};
+      const WarpPart T{R, first, line.owner(first + lead), line.owner(first + cur.w.units - 1), at, kvh};
       if (lane == 0) part_s[place] = T;
     }
     __syncwarp();
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (cuts > 0) __syncthreads();
   if (counts) {
     __threadfence();  // the CTA's part, before the count
-    before = atomicAdd(P.counters + mine.b * P.nkv + mine.kvh, 1);
+    before = atomicAdd(P.counters + mine.c0, 1);
   }
   if (!failed)
     each_task(starts & ~apart, [&](const WarpPart& T, int p, int w1) {
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float4 acc = add_row(0, WARPS - 1, r, mr, lr);
       store_out(T.at, T.kvh, r, acc, 1.f / lr);
     }
-    if (threadIdx.x == 0) P.counters[T.b * P.nkv + T.kvh] = 0;  // every part is in: ready for the next call
+    if (threadIdx.x == 0) P.counters[c0] = 0;  // every part is in: ready for the next call
     __syncthreads();
   }
   if (__syncthreads_or(failed)) {
@@ -593,7 +593,7 @@ cudaError_t launch_few(const TreeAttnArgs& a, cudaStream_t stream) {
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   p.out = static_cast<__half*>(a.out);
   p.counters = static_cast<int*>(a.scratch);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c));
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + TREE_COUNTER_BYTES);
   p.status = a.status;
   const int ctas = std::min(device_sm_count(), GEMM_MAX_CTAS);
   return launch_pdl(attn_tree_few_kernel<HD, BF16>, dim3(ctas), dim3(THREADS), L::BYTES, stream, tk, tv, p);
@@ -614,7 +614,7 @@ cudaError_t set_attr_few() {
 
 size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows) {
   // either form: a call with fewer rows than max_rows may take the other
-  const size_t few = tree_counter_bytes(c) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * FEW_ROWS * (c.head_dim + 2) * sizeof(float);
+  const size_t few = TREE_COUNTER_BYTES + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * FEW_ROWS * (c.head_dim + 2) * sizeof(float);
   return std::max(few, attention_tree_tc_scratch_bytes(c, n_seq, max_rows));
 }
 

@@ -739,7 +739,7 @@ cudaError_t launch_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   p.layer = a.layer;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HD));
   p.out = static_cast<__half*>(a.out);
-  uint8_t* at = static_cast<uint8_t*>(a.scratch) + tree_counter_bytes(c);
+  uint8_t* at = static_cast<uint8_t*>(a.scratch) + TREE_COUNTER_BYTES;
   p.line = reinterpret_cast<Line*>(at);
   p.prefix = reinterpret_cast<int*>(at + LINE_BYTES);
   p.part = reinterpret_cast<float*>(at + plan_bytes(a.b->n_seq));
@@ -770,7 +770,7 @@ cudaError_t set_attr_tc() {
 }  // namespace
 
 size_t attention_tree_tc_scratch_bytes(const pf_config& c, int n_seq, int max_rows) {
-  return tree_counter_bytes(c) + plan_bytes(n_seq) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * place_rows(c, max_rows) * (c.head_dim + 2) * sizeof(float);
+  return TREE_COUNTER_BYTES + plan_bytes(n_seq) + static_cast<size_t>(GEMM_MAX_CTAS) * 2 * place_rows(c, max_rows) * (c.head_dim + 2) * sizeof(float);
 }
 
 cudaError_t prepare_attention_tree_tc_kernels() {

@@ -283,9 +283,9 @@ struct TreeAttnArgs {
   void* scratch;  // attention_tree_scratch_bytes(c, n_seq, max_rows) bytes
   int* status;
 };
-// The scratch begins with an arrival counter per (sequence, kv head), as many as any batch has, zero before the
-// first launch and after every one that completes; behind them what a launch writes before it reads it.
-inline size_t tree_counter_bytes(const pf_config& c) { return (static_cast<size_t>(PF_MAX_SEQS) * c.n_kv_heads * sizeof(int) + 255) / 256 * 256; }
+// The scratch begins with an arrival counter per CTA, as many whatever the heads and the batch are, zero before the first
+// launch and after every one that completes; behind them what a launch writes before it reads it.
+constexpr size_t TREE_COUNTER_BYTES = (GEMM_MAX_CTAS * sizeof(int) + 255) / 256 * 256;
 size_t attention_tree_scratch_bytes(const pf_config& c, int n_seq, int max_rows);
 cudaError_t prepare_attention_tree_kernels();
 // the form for more rows per kv head than the few-row kernel takes (attention_tree_tc.cu)

@@ -119,3 +119,21 @@ def test_small_weights(kind, nq, nkv, hd, n, power):
             bound = bound + 2.0 ** -32 * values / weight[:, :, None]
         off = np.abs(got[at] - ref)
         assert (off <= bound).all(), (b, float((off / bound).max()), float(got[at].max()), float(ref.max()))
+
+
+def test_one_scratch_for_other_heads():
+    """One scratch for calls with other numbers of kv heads, widths and types in turn, few rows and many, without a zero between."""
+    rng = np.random.default_rng(5)
+    steps = []
+    for kind, nq, nkv, hd, rows, start in (("bf16", 2, 1, 64, [1], [9000]), ("f16", 64, 64, 64, [1] * 40, [200 + 7 * b for b in range(40)]),
+                                           ("f16", 8, 2, 128, [30, 4], [3000, 900]), ("bf16", 32, 8, 128, [1, 2, 0, 1], [5000, 100, 3, 40]),
+                                           ("bf16", 200, 200, 64, [1, 1], [150, 700])):
+        s = Step(kind, nq, nkv, hd, rows, start, True, trees(rng, rows), n_layers=1, layer=0)
+        s.fill()
+        steps.append((s, s.q()))
+    scratch = max((s.scratch() for s, _ in steps), key=len)
+    for turn in range(3):
+        for s, q in steps if turn < 2 else steps[::-1]:
+            out = s.attend(q, scratch)
+            pf.pf_status_read(s.status)
+            s.check_attention(q, out)
