@@ -593,8 +593,8 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
  * zero rows of A); K a multiple of 16, N of 8, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
  * aligned; n_adapters * rank below 2^31. out overlaps neither x nor, unless it is base, base. Products and sums in f32
  * (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
- * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. batch: row_begin only; sequences of
- * up to 8192 rows. No scratch. */
+ * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. After PF_ERR_DEVICE_TIMEOUT the rows whose
+ * products were not complete are as they were before the call. batch: row_begin only; sequences of up to 8192 rows. No scratch. */
 pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x_f16_dev, int64_t ldx, const float* base_dev, int64_t ld_base,
                          float* out_dev, int64_t ld_out, int32_t K, int32_t N, int32_t rank, int32_t n_adapters,
                          const int32_t* adapter_dev, const uint16_t* a_f16_dev, const uint16_t* b_f16_dev,

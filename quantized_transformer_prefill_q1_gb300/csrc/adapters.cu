@@ -262,6 +262,9 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
   __syncwarp();
   cluster_arrive_release();
   cluster_wait();
+  // whether a CTA of the cluster gave up a wait (a lane a CTA; looked at below)
+  int gave_up = 0;
+  if (lane < CL) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(gave_up) : "r"(remote(smem_u32(&abort_s), lane)) : "memory");
   const float scale = P.scale[a];
   constexpr int OWN = RT == 16 ? RT : RT / CL;
   for (int i = warp; i < OWN; i += WARPS) {
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(back) : "memory");
     }
   }
-  __syncwarp();
+  const bool whole = !__any_sync(0xffffffffu, gave_up != 0);  // else the sum lacks a share, and out stays as it is
   cluster_arrive_release();  // this CTA has read the others' shares (RT 64: and written theirs)
   if (RT == 16)
     __syncthreads();
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     cluster_wait();
 
   // ------------------------------------------------------------------ out = base + scale h B^T
-  for (int gi = gb + warp; gi < ge; gi += WARPS) {
+  for (int gi = gb + warp; whole && gi < ge; gi += WARPS) {
 #pragma unroll 1
     for (int m = 0; m < MG; ++m) {
       if (16 * m >= rows) break;
