@@ -536,8 +536,8 @@ pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q_f16_dev, c
  * written, and read as any block. A parent outside -1 .. i - 1: PF_ERR_INVALID_ARG, taken as -1. Table entries of
  * the positions that a call writes are distinct. Rows behind the last sequence are neither read nor written. Outputs
  * overlap no input where nothing else is said.
- * Errors of these calls: PF_ERR_INVALID_ARG (pointers, alignment, a table with a linear cache or none with a
- * paged one), PF_ERR_EMPTY_CHUNK (n_rows 0), PF_ERR_SHAPE (counts, layer, rank, widths, strides),
+ * Errors of these calls: PF_ERR_INVALID_ARG (pointers, alignment: 4 B where no more is said; a table with a linear cache
+ * or none with a paged one), PF_ERR_EMPTY_CHUNK (n_rows 0), PF_ERR_SHAPE (counts, layer, rank, widths, strides),
  * PF_ERR_UNSUPPORTED (a ring, a cache that is not bf16 or f16, a linear cache with several sequences),
  * PF_ERR_WORKSPACE, PF_ERR_CUDA. */
 typedef struct {

@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -1470,6 +1471,13 @@ static void prepare_batch() {
   });
 }
 
+// Arrays of 4-byte numbers in device memory (NULL is none); `status` among them in every call over a batch.
+static pf_status check_words(std::initializer_list<const void*> words) {
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(PF_ERR_INVALID_ARG, "int32 and f32 arrays must be 4-B aligned");
+  return PF_OK;
+}
+
 // What every call over a batch checks; `tree`: rows per sequence are bounded by PF_MAX_TREE.
 static pf_status check_batch_rows(const pf_batch* b, bool tree) {
   if (!b) return fail(PF_ERR_INVALID_ARG, "batch is NULL");
@@ -1479,7 +1487,7 @@ static pf_status check_batch_rows(const pf_batch* b, bool tree) {
   const int most = tree ? PF_MAX_TREE : 8192;
   if (b->max_rows < 1 || b->max_rows > most) return fail(PF_ERR_SHAPE, "max_rows %d: 1..%d", b->max_rows, most);
   if (!b->row_begin_dev) return fail(PF_ERR_INVALID_ARG, "row_begin is NULL");
-  return PF_OK;
+  return check_words({b->row_begin_dev, b->start_dev, b->parent_dev, b->block_table_dev});
 }
 
 // Calls over a batch that touch the caches.
@@ -1510,6 +1518,7 @@ pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const 
   if (!aligned16(qkv) || !aligned16(rope) || !aligned16(q) || !aligned16(kc) || !aligned16(vc) ||
       (cfg->qk_norm && (!aligned16(qn) || !aligned16(kn))))
     return fail(PF_ERR_INVALID_ARG, "qkv, norms, RoPE table, q and caches must be 16-B aligned");
+  PF_TRY(check_words({status}));
   PF_CUDA(launch_batch_append(*cfg, *batch, qkv, qn, kn, rope, layer, q, kc, vc, status, static_cast<cudaStream_t>(stream)),
           "batch append");
   return PF_OK;
@@ -1537,6 +1546,7 @@ pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, cons
   if (scratch_bytes < need || !scratch)
     return fail(PF_ERR_WORKSPACE, "tree attention scratch %zu bytes, need %zu", scratch_bytes, need);
   if (!aligned16(scratch)) return fail(PF_ERR_INVALID_ARG, "scratch must be 16-B aligned");
+  PF_TRY(check_words({status}));
   prepare_batch();
   TreeAttnArgs a{cfg, batch, q, kc, vc, layer, out, scratch, status};
   PF_CUDA(launch_attention_tree(a, static_cast<cudaStream_t>(stream)), "tree attention");
@@ -1551,6 +1561,7 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
   if (next == root) return fail(PF_ERR_INVALID_ARG, "next must not be the root ids");
   if (!kc != !vc) return fail(PF_ERR_INVALID_ARG, "both caches or none");
   if (kc && (!aligned16(kc) || !aligned16(vc))) return fail(PF_ERR_INVALID_ARG, "caches must be 16-B aligned");
+  PF_TRY(check_words({tokens, ids, root, path, n_accepted, next, status}));
   PF_CUDA(launch_tree_accept(*cfg, *batch, tokens, ids, root, path, n_accepted, next, kc, vc, status,
                              static_cast<cudaStream_t>(stream)),
           "tree accept");
@@ -1572,6 +1583,7 @@ pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, 
   if (!x || !base || !out || !adapter || !wa || !wb || !scale) return fail(PF_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(wa) || !aligned16(wb))
     return fail(PF_ERR_INVALID_ARG, "x, base, out, A and B must be 16-B aligned");
+  PF_TRY(check_words({adapter, scale, status}));
   if (base == out && ld_base != ld_out) return fail(PF_ERR_SHAPE, "out = base needs ld_out = ld_base");
   prepare_batch();
   AdapterArgs a{batch, x, ldx, base, ld_base, out, ld_out, K, N, rank, n_adapters, adapter, wa, wb, scale, status};
