@@ -590,7 +590,7 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
  * x f16 [n_rows][K] (rows ldx apart), base and out f32 [n_rows][N] (ld_base, ld_out apart; out may be base itself
  * with the same ld: the residual form, and rows without an adapter are then not touched), A f16 [n_adapters][rank][K], B f16
  * [n_adapters][N][rank], scale f32 [n_adapters]. rank a multiple of 8 up to PF_MAX_RANK (adapters of lower rank:
- * zero rows of A); K a multiple of 16, N of 8, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
+ * zero rows of A); K a multiple of 16, N of 8, both up to 2^26, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
  * aligned; n_adapters * rank below 2^31. out overlaps neither x nor, unless it is base, base. Products and sums in f32
  * (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
  * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. After PF_ERR_DEVICE_TIMEOUT the rows whose

@@ -1574,7 +1574,9 @@ pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x, int64_t ldx, 
                          void* stream) {
   PF_TRY(check_batch_rows(batch, false));
   if (rank < 8 || rank > PF_MAX_RANK || rank % 8) return fail(PF_ERR_SHAPE, "rank %d: a multiple of 8 up to %d", rank, PF_MAX_RANK);
-  if (K < 16 || K % 16 || N < 8 || N % 8) return fail(PF_ERR_SHAPE, "K %d: a multiple of 16; N %d: of 8", K, N);
+  constexpr int WIDEST = 1 << 26;  // a tile of 64 rows then has fewer than 2^31 vectors, which the kernel counts in 32 bits
+  if (K < 16 || K % 16 || N < 8 || N % 8 || K > WIDEST || N > WIDEST)
+    return fail(PF_ERR_SHAPE, "K %d: a multiple of 16; N %d: of 8; both up to 2^26", K, N);
   if (n_adapters < 1 || static_cast<int64_t>(n_adapters) * rank > 0x7fffffff)
     return fail(PF_ERR_SHAPE, "n_adapters %d: at least 1, n_adapters x rank below 2^31", n_adapters);
   if (ldx < K || ldx % 8 || ld_base < N || ld_base % 4 || ld_out < N || ld_out % 4)

@@ -32,3 +32,14 @@ def test_words_off_their_alignment(lib, off):  # noqa: F811
                         ("adapters", ("adapter", "scale", "status"))):
         for word in words:
             assert refused(*calls(batch(), **{word: P + off})[name]) == "PF_ERR_INVALID_ARG" and b"4-B" in lib.pf_last_error(), (name, word)
+
+
+def test_adapters_of_the_widest_rows(lib):  # noqa: F811
+    """K and N above 2^26, where a tile's elements or the columns rounded up would pass 32 bits."""
+    def adapters(k, n):
+        b = ctypes.byref(batch(n_rows=64, max_rows=64))
+        return refused(lib.pf_op_adapters, b, P, k, P, n, 2 * P, n, k, n, 8, 1, P + 1, P, P, P, None, None)
+
+    for k, n in ((2 ** 26 + 16, 32), (64, 2 ** 26 + 8), (2 ** 31 - 16, 32), (64, 2 ** 31 - 8), (64, 2 ** 27)):
+        assert adapters(k, n) == "PF_ERR_SHAPE", (k, n)
+    assert adapters(2 ** 26, 2 ** 26) == "PF_ERR_INVALID_ARG"  # the adapters' address, looked at later
