@@ -237,9 +237,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto place_k = [](const Part& p, int j) { return p.slots == 2 ? 2 * j : max(0, 2 * j - 1); };
   auto place_v = [](const Part& p, int j) { return p.slots == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.cnt - 1); };
 
+  int issued = 0, q_issued = 0;  // copies of tiles and of Q (thread 0)
   if (warp == 0) {
     // ------------------------------------------------------------------ copies (lane 0; a lane each looks up the tiles' pages)
-    int c = 0, seg = 0, q_issued = 0;
+    int seg = 0;
     bool ok = true;
     for (int x = 0; x < count && ok; ++seg) {
       const Part p = part(x);
@@ -257,13 +258,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         return row0 + slot;
       };
       auto load = [&](const CUtensorMap* map, int row) {
-        const int s = c % NS;
+        const int s = issued % NS;
         if (ok && lane == 0) {
-          ok = mbar_wait(kv_empty(s), ((c / NS) & 1) ^ 1, abort_flag);
+          ok = mbar_wait(kv_empty(s), ((issued / NS) & 1) ^ 1, abort_flag);
           if (ok) {
             mbar_arrive_expect_tx(kv_full(s), L::KV);
             for (int h = 0; h < NH; ++h) tma_load_2d(kv_s + s * L::KV + h * (TK * 128), map, h * 64, row, kv_full(s));
-            ++c;
+            ++issued;
           }
         }
       };
@@ -300,10 +301,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       x += p.units;
       if (x < count) cur.advance(B, work, p.units);
-    }
-    if (lane == 0 && *abort_flag) {  // let copies in flight land before shared memory is released
-      if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
-      for (int k = max(0, c - NS); k < c; ++k) drain(kv_full(k % NS), (k / NS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
@@ -625,7 +622,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0 && *abort_flag) batch_record(P.status, PF_ERR_DEVICE_TIMEOUT);
+  if (threadIdx.x == 0 && *abort_flag) {
+    // let copies in flight land before shared memory is released, whichever role gave up and when
+    if (q_issued > 0) drain(q_full, (q_issued - 1) & 1);
+    for (int k = max(0, issued - NS); k < issued; ++k) drain(kv_full(k % NS), (k / NS) & 1);
+    batch_record(P.status, PF_ERR_DEVICE_TIMEOUT);
+  }
 }
 
 // Merges the parts of cut tasks: with m* the largest of the parts' maxima, O = sum_c 2^(m_c - m*) O_c / sum_c 2^(m_c - m*) l_c.
