@@ -137,3 +137,115 @@ def test_one_scratch_for_other_heads():
             out = s.attend(q, scratch)
             pf.pf_status_read(s.status)
             s.check_attention(q, out)
+
+
+def test_replays_against_the_definition():
+    """Append, acceptance and adapters captured once and replayed with other rows, starts, trees, tokens, pages and adapters, all
+    of them valid: each replay against float64."""
+    rng = np.random.default_rng(41)
+    nq, nkv, hd, k, width = 8, 2, 64, 512, 12 * 64
+    most, room = [30, 9, 14], [400, 120, 300]  # rows, and positions that fit, of each sequence
+    s = Step("f16", nq, nkv, hd, most, [r - m for r, m in zip(room, most)], True, trees(rng, most), norm=True)
+    x = torch.from_numpy(rng.standard_normal((s.n_rows, k))).cuda().half()
+    a, b = torch.from_numpy(rng.standard_normal((2, 32, k)) * 0.04).cuda().half(), torch.from_numpy(rng.standard_normal((2, width, 32))).cuda().half()
+    scale = torch.tensor([1.0, 0.5], device="cuda")
+    base = torch.empty(s.n_rows, width, device="cuda")
+    qn, kn = (1 + 0.1 * rng.standard_normal((2, hd))).astype(np.float32)
+    qn_dev, kn_dev = torch.from_numpy(qn).cuda(), torch.from_numpy(kn).cuda()
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, hd, s.max_seq)).cuda()
+    tokens, ids, path, root, which, count, after = (ints(np.zeros(m)) for m in [s.n_rows] * 3 + [3] * 4)
+    y, q = torch.empty_like(base), torch.empty(s.n_rows, nq, hd, dtype=torch.float16, device="cuda")
+    held = {}
+
+    def step():
+        pf.pf_op_adapters(s.batch, x, base, y, which, a, b, scale, s.status)
+        pf.pf_op_batch_append(s.cfg, s.batch, y, qn_dev, kn_dev, rope, s.layer, q, s.k, s.v, s.status)
+        for name in "kv":  # what the acceptance moves, as it was before
+            held[name].copy_(getattr(s, name))
+        pf.pf_op_tree_accept(s.cfg, s.batch, tokens, ids, root, path, count, after, s.k, s.v, s.status)
+
+    held.update(k=torch.empty_like(s.k), v=torch.empty_like(s.v))
+    s.k.zero_()
+    s.v.zero_()
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    longest = 0
+    for turn in range(6):
+        s.rows = [int(rng.integers(0, m + 1)) for m in most]
+        s.start = [int(rng.integers(0, r - n + 1)) for r, n in zip(room, s.rows)]
+        s.begin = np.concatenate([[0], np.cumsum(s.rows)]).astype(np.int32)
+        s.total = int(s.begin[-1])
+        s.parents = trees(rng, s.rows)
+        for row in s.table:  # the same pages in another order
+            mine = row >= 0
+            row[mine] = rng.permutation(row[mine])
+        s.table_dev.copy_(ints(s.table))
+        s.begin_dev.copy_(ints(s.begin))
+        s.start_dev.copy_(ints(s.start))
+        s.parent_dev[:s.total] = ints(np.concatenate(s.parents))
+        t, i, r, w = (rng.integers(lo, hi, m).astype(np.int32) for lo, hi, m in ((0, 2, s.n_rows), (0, 2, s.n_rows), (0, 2, 3), (-1, 2, 3)))
+        for to, of in ((tokens, t), (ids, i), (root, r), (which, w)):
+            to.copy_(ints(of))
+        base.copy_(torch.from_numpy(rng.standard_normal(base.shape)))
+        for c, fill in ((y, 7), (q, 7), (path, 9), (count, 9), (after, 9), (s.k, 3), (s.v, 3)):
+            c.fill_(fill)
+        graph.replay()
+        pf.pf_status_read(s.status)
+        assert (y[s.total:] == 7).all() and (q[s.total:] == 7).all() and (path[s.total:] == 9).all()
+        free = torch.ones(s.slots, dtype=torch.bool, device="cuda")
+        moved = {name: held[name].clone() for name in "kv"}
+        for n in range(3):
+            at, rows = slice(s.begin[n], s.begin[n + 1]), s.rows[n]
+            if w[n] < 0:
+                assert torch.equal(y[at], base[at])
+            else:
+                ref, bound = R.adapters(*(z.cpu().numpy() for z in (base[at], x[at], a[w[n]], b[w[n]])), float(scale[w[n]]))
+                assert (np.abs(y[at].double().cpu().numpy() - ref) <= bound).all(), (turn, n)
+            slot = torch.from_numpy(np.asarray(s.slot(n, s.start[n] + np.arange(rows)), np.int64)).cuda()
+            free[slot] = False
+            if rows:
+                rq, rk, rv, size = R.append(y[at].cpu().numpy(), nq, nkv, hd, qn, kn, s.cfg.eps, s.cfg.rope_theta, s.start[n] + R.depths(s.parents[n]))
+                for got, ref, sz in ((q[at], rq, size[:, :nq]), (held["k"][s.layer][:, slot].transpose(0, 1), rk, size[:, nq:])):
+                    # half a step of an f16 (2^-25 below its normal range), and the norm and rotation within 16 roundings in f32
+                    off = np.abs(got.double().cpu().numpy() - ref)
+                    assert (off <= 2.0 ** -11 * (np.abs(ref) + 2.0 ** -20 * sz) + 2.0 ** -20 * sz + 2.0 ** -25).all(), (turn, n)
+                assert torch.equal(held["v"][s.layer][:, slot].transpose(0, 1), y[at, (nq + nkv) * hd:].reshape(rows, nkv, hd).half())
+            want, follow = R.accept(s.parents[n], t[at], i[at], r[n])
+            longest = max(longest, len(want))
+            assert path[at].tolist() == want + [-1] * (rows - len(want)) and int(count[n]) == len(want) and int(after[n]) == follow
+            for name in "kv":
+                moved[name][:, :, slot[:len(want)]] = held[name][:, :, slot[want]]
+        for name in "kv":
+            assert torch.equal(getattr(s, name), moved[name]) and (held[name][:, :, free] == 3).all()
+            assert (held[name][1 - s.layer] == 3).all()
+    assert longest > 1
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nkv,hd,rows", [(32, 8, 128, [1, 2, 1, 1, 2]), (8, 2, 64, [20, 1, 33, 7, 12])])
+def test_shared_pages(kind, nq, nkv, hd, rows):
+    """Sequences that begin with the same pages, those of a prompt that they share: attention reads them, append and acceptance write
+    the pages that each has for itself."""
+    rng = np.random.default_rng(hd)
+    s = Step(kind, nq, nkv, hd, rows, [300, 256, 511, 260, 700], True, trees(rng, rows), norm=False)
+    s.table[1:, :2] = s.table[0, :2]  # positions 0 .. 255
+    s.table_dev.copy_(ints(s.table))
+    s.fill(own_rows=False)
+    before = s.k.clone()
+    qkv = torch.from_numpy(rng.standard_normal((s.n_rows, (nq + 2 * nkv) * hd))).cuda().float()
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, hd, s.max_seq)).cuda()
+    q = torch.empty(s.n_rows, nq, hd, dtype=s.dt, device="cuda")
+    pf.pf_op_batch_append(s.cfg, s.batch, qkv, None, None, rope, s.layer, q, s.k, s.v, s.status)
+    out = s.attend(q)
+    pf.pf_status_read(s.status)
+    s.check_attention(q, out)
+    shared = torch.from_numpy(np.asarray(s.slot(0, np.arange(256)), np.int64)).cuda()
+    tokens = ints(np.arange(s.n_rows))
+    way = [int(s.begin[b]) + next(i for i in range(n) if s.parents[b][i] < 0) for b, n in enumerate(rows)]
+    path, count, after = (ints(np.zeros(m)) for m in (s.n_rows, len(rows), len(rows)))
+    pf.pf_op_tree_accept(s.cfg, s.batch, tokens, ints(np.full(s.n_rows, -5)), ints(way), path, count, after, s.k, s.v, s.status)
+    pf.pf_status_read(s.status)
+    assert count.tolist() == [1] * len(rows)
+    assert torch.equal(s.k[:, :, shared].view(torch.int16), before[:, :, shared].view(torch.int16))
