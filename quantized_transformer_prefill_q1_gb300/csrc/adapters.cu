@@ -27,6 +27,7 @@ constexpr int CL = 8;  // CTAs of a cluster
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
 constexpr int KB = 64;  // K of a stage: 128 bytes of a row
+constexpr uint32_t NO_SHARE = 0x7fc0dead;  // a NaN that no addition gives: in the place of a CTA's sums after a wait that gave up
 
 // RT rows a cluster, rank up to 16 KS
 template <int RT, int KS>
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     *reinterpret_cast<float2*>(dst + 8 * R) = make_float2(acc[j][2], acc[j][3]);
   }
   __syncthreads();
+  const bool complete = !*abort_flag;
   for (int i = threadIdx.x; i < RT * R / 4; i += THREADS) {
     float4 v = reinterpret_cast<const float4*>(red)[i];
 #pragma unroll
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
       const float4 y = reinterpret_cast<const float4*>(red)[w * (RT * R / 4) + i];
       v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
     }
+    if (!complete) v.x = v.y = v.z = v.w = __uint_as_float(NO_SHARE);
     reinterpret_cast<float4*>(part)[i] = v;
   }
 
@@ -262,9 +265,6 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
   __syncwarp();
   cluster_arrive_release();
   cluster_wait();
-  // whether a CTA of the cluster gave up a wait (a lane a CTA; looked at below)
-  int gave_up = 0;
-  if (lane < CL) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(gave_up) : "r"(remote(smem_u32(&abort_s), lane)) : "memory");
   const float scale = P.scale[a];
   constexpr int OWN = RT == 16 ? RT : RT / CL;
   for (int i = warp; i < OWN; i += WARPS) {
@@ -282,8 +282,15 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
         float2 y2[CL];
 #pragma unroll
         for (int w = 0; w < CL; ++w) y2[w] = ld_cluster(remote(at, w));
+        bool lacking = false;
 #pragma unroll
-        for (int w = 0; w < CL; ++w) v[e] = make_float2(v[e].x + y2[w].x, v[e].y + y2[w].y);
+        for (int w = 0; w < CL; ++w) {
+          lacking |= __float_as_uint(y2[w].x) == NO_SHARE;
+          v[e] = make_float2(v[e].x + y2[w].x, v[e].y + y2[w].y);
+        }
+        if (lacking) {  // row 0 says so to every CTA, whether it adds rows or not
+          for (int w = 0; w < CL; ++w) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(smem_u32(&abort_s), w)), "r"(1) : "memory");
+        }
       }
       big = fmaxf(big, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
     }
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(back) : "memory");
     }
   }
-  const bool whole = !__any_sync(0xffffffffu, gave_up != 0);  // else the sum lacks a share, and out stays as it is
+  __syncwarp();
   cluster_arrive_release();  // this CTA has read the others' shares (RT 64: and written theirs)
   if (RT == 16)
     __syncthreads();
@@ -327,6 +334,7 @@ __global__ void __launch_bounds__(THREADS, KS == 8 ? 1 : 2)
     cluster_wait();
 
   // ------------------------------------------------------------------ out = base + scale h B^T
+  const bool whole = !*abort_flag;  // else the sum lacks a share, and out stays as it is
   for (int gi = gb + warp; whole && gi < ge; gi += WARPS) {
 #pragma unroll 1
     for (int m = 0; m < MG; ++m) {
