@@ -536,6 +536,9 @@ pf_status pf_op_attention_kv8(const pf_config* cfg, const uint16_t* q_f16_dev, c
  * written, and read as any block. A parent outside -1 .. i - 1: PF_ERR_INVALID_ARG, taken as -1. Table entries of
  * the positions that a call writes are distinct. Rows behind the last sequence are neither read nor written. Outputs
  * overlap no input where nothing else is said.
+ * Append, adapters and the merge of the attention launch for n_seq * max_rows rows, and the attention takes one form for all
+ * sequences by max_rows: one long sequence among many short ones is cheaper in a call of its own. Its pf_batch points at its own
+ * entry of the same arrays (row_begin_dev + b, start_dev + b, its row of the table, n_seq 1), that of the others behind it.
  * Errors of these calls: PF_ERR_INVALID_ARG (pointers, alignment: 4 B where no more is said; a table with a linear cache
  * or none with a paged one), PF_ERR_EMPTY_CHUNK (n_rows 0), PF_ERR_SHAPE (counts, layer, rank, widths, strides),
  * PF_ERR_UNSUPPORTED (a ring, a cache that is not bf16 or f16, a linear cache with several sequences),
@@ -592,7 +595,7 @@ pf_status pf_op_tree_accept(const pf_config* cfg, const pf_batch* batch, const i
  * [n_adapters][N][rank], scale f32 [n_adapters]. rank a multiple of 8 up to PF_MAX_RANK (adapters of lower rank:
  * zero rows of A); K a multiple of 16, N of 8, both up to 2^26, ldx of 8, ld_base and ld_out of 4; x, A, B, base and out 16-B
  * aligned; n_adapters * rank below 2^31. out overlaps neither x nor, unless it is base, base. Products and sums in f32
- * (x A^T enters the second product as two f16 terms, 22 bits). An adapter index
+ * (x A^T enters the second product as two f16 terms, 22 bits; an infinity of B may come out as a NaN). An adapter index
  * outside -1 .. n_adapters - 1 is taken as -1 and records PF_ERR_INVALID_ARG. After PF_ERR_DEVICE_TIMEOUT the rows whose
  * products were not complete are as they were before the call. batch: row_begin only; sequences of up to 8192 rows. No scratch. */
 pf_status pf_op_adapters(const pf_batch* batch, const uint16_t* x_f16_dev, int64_t ldx, const float* base_dev, int64_t ld_base,

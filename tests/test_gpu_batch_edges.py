@@ -249,3 +249,65 @@ def test_shared_pages(kind, nq, nkv, hd, rows):
     pf.pf_status_read(s.status)
     assert count.tolist() == [1] * len(rows)
     assert torch.equal(s.k[:, :, shared].view(torch.int16), before[:, :, shared].view(torch.int16))
+
+
+@pytest.mark.parametrize("rows,rank", [([3, 1, 2], 16), ([100, 40, 70], 16), ([700, 300], 64), ([9, 300], 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_adapters_that_are_not_finite(rows, rank, bad):
+    """One element of x, base, A or B that is not finite: the results that hold it in the definition are not finite, all others
+    are right."""
+    rng = np.random.default_rng(rank)
+    k, n = 272, 136
+    begin = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    x, base = rng.standard_normal((begin[-1], k)).astype(np.float16), rng.standard_normal((begin[-1], n)).astype(np.float32)
+    a, b = (rng.standard_normal((2, rank, k)) * k ** -0.5).astype(np.float16), rng.standard_normal((2, n, rank)).astype(np.float16)
+    batch, status, scale = pf.Batch(ints(begin), n_rows=int(begin[-1]), max_rows=max(rows)), torch.zeros(4, dtype=torch.int32, device="cuda"), [0.5, 2.0]
+    for spoilt in range(4):
+        t = [x.copy(), base.copy(), a.copy(), b.copy()]
+        t[spoilt][tuple(int(rng.integers(m)) for m in t[spoilt].shape)] = bad
+        dev = [torch.from_numpy(y).cuda() for y in t]
+        out = torch.full((int(begin[-1]), n), 7.0, device="cuda")
+        pf.pf_op_adapters(batch, dev[0], dev[1], out, ints(np.arange(len(rows)) % 2), dev[2], dev[3], torch.tensor(scale, device="cuda"), status)
+        pf.pf_status_read(status)
+        for i in range(len(rows)):
+            at = slice(begin[i], begin[i + 1])
+            got = out[at].cpu().numpy()
+            with np.errstate(invalid="ignore"):
+                ref, bound = R.adapters(t[1][at], t[0][at], t[2][i % 2], t[3][i % 2], scale[i % 2])
+            fine = np.isfinite(ref)
+            assert (np.isfinite(got) == fine).all() and (np.abs(got[fine] - ref[fine]) <= bound[fine]).all(), (spoilt, i)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("long", [0, 2, 4])
+def test_a_long_sequence_in_a_call_of_its_own(kind, long):
+    """Batches that point at entries of the same arrays: one sequence, those before it and those behind it."""
+    rng = np.random.default_rng(long)
+    rows = [1, 2, 1, 1, 2]
+    rows[long] = 90
+    s = Step(kind, 8, 2, 64, rows, [300, 5, 129, 0, 700], True, trees(rng, rows), n_layers=1, layer=0)
+    s.fill(own_rows=False)
+    whole = s.batch
+    parts = [pf.Batch(s.begin_dev[i:j + 1], n_rows=s.n_rows, max_rows=max(rows[i:j]), start=s.start_dev[i:j], parent=s.parent_dev, blocks=s.table_dev[i:j])
+             for i, j in ((0, long), (long, long + 1), (long + 1, 5)) if i < j]
+    qkv = torch.from_numpy(rng.standard_normal((s.n_rows, 12 * 64))).cuda().float()
+    rope = torch.from_numpy(pf.pf_rope_table_host(s.cfg.rope_theta, 64, s.max_seq)).cuda()
+    x = torch.from_numpy(rng.standard_normal((s.n_rows, 256))).cuda().half()
+    a, b = torch.from_numpy(rng.standard_normal((1, 16, 256)) / 16).cuda().half(), torch.from_numpy(rng.standard_normal((1, 512, 16))).cuda().half()
+    which, one, scratch = ints(np.zeros(5)), torch.ones(1, device="cuda"), s.scratch()
+    got = []
+    for batches in ([whole], parts):
+        q = torch.full((s.n_rows, 8, 64), 7.0, dtype=s.dt, device="cuda")
+        out, y = torch.full((s.n_rows, 512), 7.0, dtype=torch.float16, device="cuda"), torch.full((s.n_rows, 512), 7.0, device="cuda")
+        for batch in batches:
+            pf.pf_op_batch_append(s.cfg, batch, qkv, None, None, rope, 0, q, s.k, s.v, s.status)
+        for batch in batches:
+            pf.pf_op_attention_tree(s.cfg, batch, q, s.k, s.v, 0, out, scratch, s.status)
+            pf.pf_op_adapters(batch, x, qkv[:, :512], y, which[:batch.n_seq], a, b, one, s.status)
+        pf.pf_status_read(s.status)
+        s.check_attention(q, out)
+        ref, bound = R.adapters(*(t[:s.total].cpu().numpy() for t in (qkv[:, :512], x)), a[0].cpu().numpy(), b[0].cpu().numpy(), 1.0)
+        assert (np.abs(y[:s.total].cpu().numpy() - ref) <= bound).all() and (y[s.total:] == 7).all()
+        got.append((q, s.k.clone(), s.v.clone()))
+    for t, u in zip(*got):
+        assert torch.equal(t.view(torch.int16), u.view(torch.int16))
