@@ -569,10 +569,10 @@ pf_status pf_op_batch_append(const pf_config* cfg, const pf_batch* batch, const 
  * scratch_dev: 16-B aligned, at least pf_attention_tree_scratch_bytes(cfg, n_seq, max_rows) bytes (which does not fall
  * as either grows: a larger batch's scratch serves every smaller one of the same heads), zero before its first call;
  * each call that completes leaves it ready for the next, of any heads and type for which it is large enough (after
- * PF_ERR_DEVICE_TIMEOUT, where out holds anything, zero it again). Calls sharing one scratch must not overlap in time, nor graphs that captured them. Softmax weights enter the
- * product with V in the cache's type (up to max_rows G = 8 query rows per kv head of a bf16 cache: as two bf16 terms; of an
- * f16 cache scaled so that weights down to 2^-21 of the row's running maximum keep all bits, smaller ones a step of 2^-31
- * of it), sums in f32. */
+ * PF_ERR_DEVICE_TIMEOUT, where out holds anything, zero it again). Calls sharing one scratch must not overlap in time, nor
+ * graphs that captured them. Softmax weights enter the product with V in the cache's type (up to max_rows G = 8 query rows per
+ * kv head of a bf16 cache: as two bf16 terms; of an f16 cache scaled so that weights down to 2^-21 of the row's running maximum
+ * keep all bits, smaller ones a step of 2^-31 of it), sums in f32. */
 size_t pf_attention_tree_scratch_bytes(const pf_config* cfg, int32_t n_seq, int32_t max_rows);
 pf_status pf_op_attention_tree(const pf_config* cfg, const pf_batch* batch, const void* q_dev, const void* k_cache_dev,
                                const void* v_cache_dev, int32_t layer, uint16_t* out_f16_dev, void* scratch_dev,

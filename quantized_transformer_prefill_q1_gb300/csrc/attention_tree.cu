@@ -24,9 +24,9 @@
 // The units in turns over the warps, which met at every task's end: 131, 26, 49, 7.6 us. LEAD 0: 135, 27, 56 us; 2 to 6
 // within 5 % of one another.
 //
-// Rounding: P to f16 (after a power of two, see P_UP), or for a bf16 cache to two bf16 terms (the product with V takes operands
-// of one type; one term would be the largest error of the f16 output, 1.2e-3 against 2e-4 in relative L2, and the second costs
-// nothing beside the copies), the output to f16; all else f32.
+// Rounding: P to f16 (see M_DOWN), or for a bf16 cache to two bf16 terms (the product with V takes operands of one type; one
+// term would be the largest error of the f16 output, 1.2e-3 against 2e-4 in relative L2, and the second costs nothing beside the
+// copies), the output to f16; all else f32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,10 +42,11 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int UK = 32;   // keys per unit
 constexpr int LEAD = 4;  // what a task costs beside its keys, in units (task_lead)
 constexpr float RESCALE_LOG2 = 8.f;
-// Weights of an f16 cache are formed 2^7 larger, sums and O with them: up to 2^15 where the running maximum is exceeded by 2^8, and
-// a step of 2^-31 at the small end instead of 2^-24, below which a long cache's many small weights would vanish together.
+// The running maximum m of an f16 cache is kept 7 below the scores', so that the weights, their sum and O are 2^7 larger: up to
+// 2^15 before m is raised, and with steps of 2^-31 of the largest at the small end instead of 2^-24, below which a long cache's
+// many small weights would vanish together.
 template <int BF16>
-constexpr float P_UP = BF16 ? 0.f : 7.f;
+constexpr float M_DOWN = BF16 ? 0.f : 7.f;
 // Most rows per kv head of this form: the n side of an MMA. Both sides measured with 8 rows of 32/8 heads of 128, this form
 // against attention_tree_tc.cu: one sequence at 512 / 8,190 positions 9.4 against 10.4 and 12.3 against 13.8 us, 48
 // sequences of 100 .. 900 24.7 against 30.4, of 300 .. 8,100 133 against 132. With 16 rows (two such sides) one
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mx[e] = fmaxf(fmaxf(sc[0][e], sc[0][e + 2]), fmaxf(sc[1][e], sc[1][e + 2])) * P.scale_log2;
-        raise |= mx[e] > m[e] + RESCALE_LOG2;
+        raise |= mx[e] > m[e] + (RESCALE_LOG2 + M_DOWN<BF16>);
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           float y = mx[e];
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
-          const float mn = fmaxf(m[e], y);
+          const float mn = fmaxf(m[e], y - M_DOWN<BF16>);
           const float alpha = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
           m[e] = mn;
           l[e] *= alpha;
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // P^T as the B operand: [16-key tile][register]; of a bf16 cache as two terms, hi + lo
       uint32_t pf[2][2], pl[2][2];
-      const float n0 = m[0] == -INFINITY ? 0.f : P_UP<BF16> - m[0], n1 = m[1] == -INFINITY ? 0.f : P_UP<BF16> - m[1];
+      const float n0 = m[0] == -INFINITY ? 0.f : -m[0], n1 = m[1] == -INFINITY ? 0.f : -m[1];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll

@@ -27,10 +27,10 @@
 // cost about 5 us each beside their tiles, mostly waits of one role for the other (LEAD; with 0, 24 rows of each of 48
 // sequences of 100 .. 900 positions took 61 us, with 1 / 2 / 4 45 / 42 / 40 us): 37 us.
 //
-// Rounding: P to the cache's type (the product's operand; of an f16 cache after a power of two, see P_UP; of a bf16 cache that
-// is the largest error of the f16 output, 1.2e-3 in relative L2, as in the attention over one sequence: two bf16 terms, 2e-4,
-// take 216 us instead of 162 on the case above and 15 to 20 % more on short tasks, since both the softmax and the products with
-// V grow by a half), the output to f16; all else f32.
+// Rounding: P to the cache's type (the product's operand; for an f16 cache see M_DOWN; of a bf16 cache that is the largest error
+// of the f16 output, 1.2e-3 in relative L2, as in the attention over one sequence: two bf16 terms, 2e-4, take 216 us instead of
+// 162 on the case above and 15 to 20 % more on short tasks, since both the softmax and the products with V grow by a half), the
+// output to f16; all else f32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,10 +50,11 @@ constexpr int THREADS = 320;
 constexpr int SM_THREADS = 256;
 constexpr float RESCALE_LOG2 = 8.f;
 static_assert(TK == PF_KV_BLOCK, "a key tile is a page");
-// Weights of an f16 cache are formed 2^7 larger, sums and O with them: up to 2^15 where the running maximum is exceeded by 2^8, and
-// a step of 2^-31 at the small end instead of 2^-24, below which a long cache's many small weights would vanish together.
+// The running maximum m of an f16 cache is kept 7 below the scores', so that the weights, their sum and O are 2^7 larger: up to
+// 2^15 before m is raised, and with steps of 2^-31 of the largest at the small end instead of 2^-24, below which a long cache's
+// many small weights would vanish together.
 template <int BF16>
-constexpr float P_UP = BF16 ? 0.f : 7.f;
+constexpr float M_DOWN = BF16 ? 0.f : 7.f;
 
 template <int HD>
 struct TSmem {
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < HK; e += 2) mp[(e >> 1) & 3] = max3(mp[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           }
         }
-        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
+        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2 - M_DOWN<BF16>;
         const bool need = mx > m + RESCALE_LOG2;
         if (j == j0) {
           m = mx;
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (need) m = mx;
         }
-        const float neg_m = m == -INFINITY ? 0.f : P_UP<BF16> - m;
+        const float neg_m = m == -INFINITY ? 0.f : -m;
         const uint64_t neg_two = two(neg_m, neg_m), sl2_two = two(sl2, sl2);
         uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll 1
